@@ -526,6 +526,27 @@ static cudaError_t workspace_pool(cudaMemPool_t* out) {
     return cudaSuccess;
 }
 
+}  // extern "C"
+
+namespace pkv {
+bool launch_fault_injected() { return fault_launch(); }
+pariskv_status take_workspace(void** p, size_t bytes, cudaStream_t st) {
+    *p = nullptr;
+    if (fault_alloc()) return fail(PARISKV_ENOMEM, "attention workspace");
+    cudaMemPool_t pool = nullptr;
+    cudaError_t e = workspace_pool(&pool);
+    if (e == cudaSuccess) e = cudaMallocFromPoolAsync(p, bytes, pool, st);
+    if (e == cudaErrorMemoryAllocation) {
+        cudaGetLastError();
+        return fail(PARISKV_ENOMEM, "attention workspace (%zu bytes)", bytes);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "attention workspace");
+    return PARISKV_OK;
+}
+}  // namespace pkv
+
+extern "C" {
+
 pariskv_status pariskv_sparse_attend(const pariskv_config* cfg, const void* q, const void* K,
                                      const void* V, int64_t ld_tok, int64_t n,
                                      const int32_t* topk_idx, int32_t k, float scale, void* out,

@@ -116,7 +116,10 @@ void prior_levels(float out[8]);
 pariskv_status fail(pariskv_status s, const char* fmt, ...);
 pariskv_status cuda_fail(cudaError_t e, const char* what);
 bool alloc_fault_injected();   // PARISKV_FAULT=alloc: every device allocation fails
+bool launch_fault_injected();  // PARISKV_FAULT=launch: calls fail before their first launch
 pariskv_status check_device_pointer(const void* p, size_t align, const char* name);
+// `bytes` of the per-device workspace pool, in the order of `st` (give back with cudaFreeAsync)
+pariskv_status take_workspace(void** p, size_t bytes, cudaStream_t st);
 pariskv_status validate_config(const pariskv_config* cfg);   // the checks every call makes
 void set_last_launches(int32_t n);   // what pariskv_last_launch_count reports
 int32_t last_launches();

@@ -1,0 +1,593 @@
+// paged.cu -- the paged K/V cache (pariskv_paged.h): argument checks, the kernels that write a
+// chunk into its pages and read pages back, and the plan and join kernels around the attention.
+#include <cuda_fp8.h>
+
+#include "paged.cuh"
+
+namespace pkv {
+
+namespace {
+
+// 8 consecutive elements of a row as fp32
+__device__ __forceinline__ void load8(const float* p, float v[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    const float4 b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void unpack8(uint4 a, float v[8]) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float v[8]) {
+    unpack8(*reinterpret_cast<const uint4*>(p), v);
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint4 pack8(const float v[8]) {
+    return make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
+                      bf16_pair(v[6], v[7]));
+}
+
+// ------------------------------------------------------------------------------------ write
+// A warp takes one new token: 2 * heads rows of 128 elements (K of every head, then V), two at
+// a time, 16 lanes a row and 8 elements a lane, kWriteRows row pairs in flight. Bound by HBM:
+// it reads each row once and writes 256 or 129 bytes of it; neighbouring tokens are in
+// neighbouring warps of a CTA, so the 128-byte pieces of a head's rows meet in L2.
+constexpr int kWriteWarps = 8;
+constexpr int kWriteRows = 4;
+
+template <typename In, bool kE4m3>
+__global__ void __launch_bounds__(kWriteWarps * 32)
+paged_write_kernel(const PagePool pool, const Seqs c, int heads, const In* __restrict__ kn,
+                   const In* __restrict__ vn, int64_t k_ld, int64_t v_ld) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t tok = static_cast<int64_t>(blockIdx.x) * kWriteWarps + warp;
+    if (tok >= c.total_q) return;
+    // the sequence of the token: the last start <= tok
+    int lo = 0;
+    for (int len = c.batch + 1; len > 1;) {
+        const int step = (len + 31) / 32, i = lo + lane * step;
+        const bool le = lane * step < len && i <= c.batch && c.q_start[i] <= tok;
+        const int cnt = __popc(__ballot_sync(0xffffffffu, le));
+        if (cnt == 0) return;   // before the first sequence
+        lo += (cnt - 1) * step;
+        len = step;
+    }
+    if (lo >= c.batch) return;  // behind the last sequence
+    const SeqView v = seq_view(c, pool.shift, lo);
+    const int64_t j = tok - v.row0, pos = v.pos0 + j;
+    if (j < 0 || j >= v.rows || pos < 0 || pos >= v.kv) return;
+    const int32_t page = c.table[static_cast<int64_t>(lo) * c.stride + (pos >> pool.shift)];
+    if (page < 0 || page >= pool.num_pages) return;
+    const int slot = static_cast<int>(pos) & ((1 << pool.shift) - 1);
+    const int half = lane >> 4, l8 = (lane & 15) * 8;
+
+    for (int r0 = 0; r0 < 2 * heads; r0 += 2 * kWriteRows) {
+        float x[kWriteRows][8];
+#pragma unroll
+        for (int i = 0; i < kWriteRows; ++i) {
+            const int r = r0 + 2 * i + half;
+            if (r < 2 * heads) {
+                const bool is_v = r >= heads;
+                load8((is_v ? vn + tok * v_ld : kn + tok * k_ld) +
+                          static_cast<int64_t>(is_v ? r - heads : r) * D + l8, x[i]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[i][k] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kWriteRows; ++i) {
+            const int r = r0 + 2 * i + half;
+            const bool live = r < 2 * heads, is_v = r >= heads;
+            const int64_t row = static_cast<int64_t>(is_v ? r - heads : r) << pool.shift | slot;
+            uint8_t* base = (is_v ? pool.v : pool.k) + page * pool.page_bytes;
+            if (!kE4m3) {
+                if (live) *reinterpret_cast<uint4*>(base + (row * D + l8) * 2) = pack8(x[i]);
+                continue;
+            }
+            // largest magnitude by its bits: a NaN's are above infinity's
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(x[i][k]) & 0x7fffffffu);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const bool finite = top < 0x7f800000u;
+            const int byte = finite ? scale_byte(__uint_as_float(top)) : kNanRow;
+            const float inv = pow2f(finite ? 127 - byte : 0);
+            uint32_t code[2] = {0x7f7f7f7fu, 0x7f7f7f7fu};
+            if (finite) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float* y = x[i] + 4 * k;
+                    code[k] = __nv_cvt_float2_to_fp8x2(make_float2(y[0] * inv, y[1] * inv),
+                                                       __NV_SATFINITE, __NV_E4M3);
+                    code[k] |= uint32_t(__nv_cvt_float2_to_fp8x2(
+                                   make_float2(y[2] * inv, y[3] * inv), __NV_SATFINITE,
+                                   __NV_E4M3)) << 16;
+                }
+            }
+            if (live) {
+                *reinterpret_cast<uint2*>(base + row * D + l8) = make_uint2(code[0], code[1]);
+                if ((lane & 15) == 0)
+                    (is_v ? pool.vs : pool.ks)[page * pool.scale_stride + row] =
+                        static_cast<uint8_t>(byte);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------- read
+// A warp takes 16 consecutive positions (aligned, so they lie in one page) of one KV head of K
+// or of V: 8 loads of two rows in flight, then 8 stores. Both sides are contiguous runs of 16
+// rows. Bound by HBM.
+constexpr int kReadWarps = 8;
+constexpr int kReadRun = 16;
+
+template <typename Out, bool kE4m3>
+__global__ void __launch_bounds__(kReadWarps * 32)
+paged_read_kernel(const PagePool pool, const Seqs c, int heads, int64_t first, int64_t n,
+                  Out* __restrict__ K, Out* __restrict__ V, int64_t ld, int64_t runs,
+                  int64_t total) {
+    const int lane = threadIdx.x & 31;
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * kReadWarps + (threadIdx.x >> 5);
+    if (w >= total) return;
+    const int64_t run = w % runs, x = w / runs;
+    const int h = static_cast<int>(x % heads);
+    const int64_t y = x / heads;
+    const int s = static_cast<int>(y % c.batch);
+    const bool is_v = K == nullptr || y >= c.batch;
+    const int64_t p0 = ((first >> 4) + run) << 4;        // first position of the run
+    const int64_t end = min64(min64(first + n, c.kv_len[s]),
+                              static_cast<int64_t>(c.width) << pool.shift);
+    if (p0 >= end) return;
+    const int32_t page = c.table[static_cast<int64_t>(s) * c.stride + (p0 >> pool.shift)];
+    if (page < 0 || page >= pool.num_pages) return;
+    const int slot = static_cast<int>(p0) & ((1 << pool.shift) - 1);
+    const int64_t row = (static_cast<int64_t>(h) << pool.shift) + slot + (lane >> 4);
+    const int l8 = (lane & 15) * 8;
+    const uint8_t* src = (is_v ? pool.v : pool.k) + page * pool.page_bytes +
+                         (row * D + l8) * (kE4m3 ? 1 : 2);
+    const uint8_t* sc = kE4m3 ? (is_v ? pool.vs : pool.ks) + page * pool.scale_stride + row
+                              : nullptr;
+    uint4 raw[kReadRun / 2];
+    uint32_t byte[kReadRun / 2];
+#pragma unroll
+    for (int i = 0; i < kReadRun / 2; ++i) {
+        const int64_t pos = p0 + 2 * i + (lane >> 4);
+        const bool ok = pos >= first && pos < end;
+        if (kE4m3) {
+            const uint2 t = ok ? __ldcs(reinterpret_cast<const uint2*>(src + 2 * i * D))
+                               : make_uint2(0, 0);
+            raw[i] = make_uint4(t.x, t.y, 0, 0);
+            byte[i] = ok ? sc[2 * i] : 0;
+        } else {
+            raw[i] = ok ? __ldcs(reinterpret_cast<const uint4*>(src + 4 * i * D))
+                        : make_uint4(0, 0, 0, 0);
+        }
+    }
+    Out* dst = (is_v ? V : K) + ((static_cast<int64_t>(s) * heads + h) * ld) * D + l8;
+#pragma unroll
+    for (int i = 0; i < kReadRun / 2; ++i) {
+        const int64_t pos = p0 + 2 * i + (lane >> 4);
+        if (pos < first || pos >= end) continue;
+        Out* o = dst + (pos - first) * D;
+        float v[8];
+        if (kE4m3) {
+            const float f = scale_value(byte[i]);
+            const uint32_t w2[2] = {raw[i].x, raw[i].y};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
+                    static_cast<__nv_fp8x2_storage_t>(w2[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
+                const float2 t = __half22float2(__half2(hr));
+                v[2 * k] = t.x * f;
+                v[2 * k + 1] = t.y * f;
+            }
+        } else {
+            unpack8(raw[i], v);
+        }
+        if constexpr (sizeof(Out) == 2) {
+            *reinterpret_cast<uint4*>(o) = kE4m3 ? pack8(v) : raw[i];
+        } else {
+            *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------- plan
+constexpr int kPlanT = 1024;
+
+// inclusive scan over the CTA; *total is the sum
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* s_warp, int64_t* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();           // the last scan's readers are done with s_warp
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+    for (int w = 0; w < kPlanT / 32; ++w) {
+        const int64_t y = s_warp[w];
+        before += w < warp ? y : 0;
+        all += y;
+    }
+    *total = all;
+    return x + before;
+}
+
+// One CTA: counts each sequence's tiles, writes the tiles in order, and sums their blocks.
+__global__ void __launch_bounds__(kPlanT)
+plan_kernel(const Seqs c, int shift, const PlanShape p, const Plan plan) {
+    __shared__ int64_t s_warp[kPlanT / 32];
+    __shared__ int32_t s_first[kPlanT], s_count[kPlanT];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int64_t tiles = 0;
+    for (int s0 = 0; s0 < c.batch; s0 += kPlanT) {
+        const int s = s0 + threadIdx.x;
+        int64_t nt = 0, all;
+        if (s < c.batch)
+            nt = ceil_div(static_cast<int64_t>(seq_view(c, shift, s).rows) * p.group,
+                          p.tile_rows);
+        const int64_t at = tiles + block_scan(nt, s_warp, &all) - nt;
+        // malformed starts (overlapping sequences) can ask for more tiles than there is room
+        s_first[threadIdx.x] = static_cast<int32_t>(min64(at, plan.max_tiles));
+        s_count[threadIdx.x] = static_cast<int32_t>(min64(nt, max64(0, plan.max_tiles - at)));
+        __syncthreads();
+        for (int i = warp; i < min(kPlanT, c.batch - s0); i += kPlanT / 32) {
+            const int n = s_count[i];
+            if (n == 0) continue;
+            const SeqView v = seq_view(c, shift, s0 + i);
+            for (int t = lane; t < n; t += 32) {
+                const int at2 = s_first[i] + t;
+                plan.seq[at2] = s0 + i;
+                plan.row[at2] = t * p.tile_rows;
+                plan.pre[at2 + 1] = tile_blocks(v, p, t * p.tile_rows);
+            }
+        }
+        tiles = min64(tiles + all, plan.max_tiles);
+        __syncthreads();
+    }
+    const int nt = static_cast<int>(tiles);
+    int64_t sum = 0;
+    if (threadIdx.x == 0) {
+        plan.pre[0] = 0;
+        *plan.ntiles = nt;
+    }
+    for (int t0 = 0; t0 < nt; t0 += kPlanT) {
+        const int t = t0 + threadIdx.x;
+        int64_t all;
+        const int64_t x = block_scan(t < nt ? plan.pre[t + 1] : 0, s_warp, &all);
+        if (t < nt) plan.pre[t + 1] = sum + x;
+        sum += all;
+    }
+}
+
+// ------------------------------------------------------------------------------------- join
+// The tile that the cut before CTA c = blockIdx.x + 1 goes through, if that cut is the tile's
+// first: its parts, from the CTA of its first block to the CTA of its last, are rescaled to the
+// common maximum and summed in that order. One warp a row, 4 elements a lane.
+constexpr int kJoinWarps = 4;
+
+template <typename Out>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+join_kernel(const AttendArgs a, int ctas) {
+    const int nt = *a.plan.ntiles;
+    const int64_t per_head = a.plan.pre[nt], total = per_head * a.heads;
+    if (total == 0) return;
+    const int lane = threadIdx.x & 31;
+    const int64_t lo = cut(total, ctas, blockIdx.x + 1);
+    if (lo >= total) return;
+    const int64_t h = lo / per_head;
+    const int tile = warp_search(a.plan.pre, nt, lo - h * per_head);
+    const int64_t start = h * per_head + a.plan.pre[tile];
+    const int64_t end = h * per_head + a.plan.pre[tile + 1];
+    const int64_t c0 = cut_of(total, ctas, start);
+    if (start == lo || c0 != blockIdx.x) return;
+    const int64_t c1 = cut_of(total, ctas, end - 1);
+    const int R = a.shape.tile_rows, G = a.shape.group;
+    const SeqView v = seq_view(a.seqs, a.pool.shift, a.plan.seq[tile]);
+    const int64_t first = a.plan.row[tile];
+    const int64_t rows = min64(R, static_cast<int64_t>(v.rows) * G - first);
+    for (int64_t r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < rows;
+         r += gridDim.y * kJoinWarps) {
+        float M = -INFINITY;
+        for (int64_t c = c0; c <= c1; ++c) {
+            if (cut(total, ctas, c) == cut(total, ctas, c + 1)) continue;
+            M = fmaxf(M, a.work[(2 * c + (c == c0)) * part_floats(R) + R * D + r]);
+        }
+        const float m = M == -INFINITY ? 0.0f : M;
+        float den = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int64_t c = c0; c <= c1; ++c) {
+            if (cut(total, ctas, c) == cut(total, ctas, c + 1)) continue;
+            const float* w = a.work + (2 * c + (c == c0)) * part_floats(R);
+            const float f = exp2f(w[R * D + r] - m);
+            den += w[R * D + R + r] * f;
+            const float4 x = *reinterpret_cast<const float4*>(w + r * D + 4 * lane);
+            o[0] += x.x * f; o[1] += x.y * f; o[2] += x.z * f; o[3] += x.w * f;
+        }
+        // a row without tokens has den == 0 (a NaN must come through)
+        const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+        const int64_t rr = first + r, tok = v.row0 + rr / G;
+        const int64_t at = tok * (static_cast<int64_t>(a.heads) * G) + h * G + rr % G;
+        Out* dst = static_cast<Out*>(a.out) + at * D + 4 * lane;
+        if constexpr (sizeof(Out) == 2)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(bf16_pair(o[0] * inv, o[1] * inv),
+                                                        bf16_pair(o[2] * inv, o[3] * inv));
+        else
+            *reinterpret_cast<float4*>(dst) =
+                make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+        if (a.lse && lane == 0) a.lse[at] = den == 0.0f ? -INFINITY : M * kLn2 + logf(den);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_plan(const AttendArgs& a, cudaStream_t st) {
+    plan_kernel<<<1, kPlanT, 0, st>>>(a.seqs, a.pool.shift, a.shape, a.plan);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_join(const AttendArgs& a, int ctas, bool f32_out, cudaStream_t st) {
+    if (ctas < 2) return cudaSuccess;
+    const dim3 grid(ctas - 1, static_cast<unsigned>(ceil_div(a.shape.tile_rows, 4 * kJoinWarps)));
+    if (f32_out)
+        join_kernel<float><<<grid, kJoinWarps * 32, 0, st>>>(a, ctas);
+    else
+        join_kernel<__nv_bfloat16><<<grid, kJoinWarps * 32, 0, st>>>(a, ctas);
+    return cudaGetLastError();
+}
+
+namespace {
+
+// Device memory of the current device.
+pariskv_status check_here(const void* p, size_t align, const char* name, int dev) {
+    if (!p) return fail(PARISKV_EINVAL, "%s is NULL", name);
+    if (reinterpret_cast<uintptr_t>(p) % align)
+        return fail(PARISKV_EINVAL, "%s is not %zu-byte aligned", name, align);
+    cudaPointerAttributes at;
+    if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+        cudaGetLastError();
+        return fail(PARISKV_EINVAL, "%s is not a CUDA-visible pointer", name);
+    }
+    if (at.type != cudaMemoryTypeDevice)
+        return fail(PARISKV_EINVAL, "%s is not device memory", name);
+    if (at.device != dev)
+        return fail(PARISKV_EINVAL, "%s lies on device %d but device %d is current", name,
+                    at.device, dev);
+    return PARISKV_OK;
+}
+
+// The checks that need no device come first, so that they hold without one.
+pariskv_status check_shapes(const pariskv_config* cfg, const pariskv_pages* p,
+                            const pariskv_chunk* c) {
+    pariskv_status s = validate_config(cfg);
+    if (s != PARISKV_OK) return s;
+    if (!p) return fail(PARISKV_EINVAL, "pages is NULL");
+    if (!c) return fail(PARISKV_EINVAL, "chunk is NULL");
+    if (p->format != PARISKV_PAGES_BF16 && p->format != PARISKV_PAGES_E4M3)
+        return fail(PARISKV_EINVAL, "page format %d unknown", p->format);
+    if (p->page_size < 16 || p->page_size > 256 || (p->page_size & (p->page_size - 1)))
+        return fail(PARISKV_EINVAL, "page_size %d is not 16, 32, 64, 128 or 256", p->page_size);
+    if (p->num_pages < 1 || p->num_pages > INT32_MAX)
+        return fail(PARISKV_EINVAL, "num_pages %lld not in [1, 2^31 - 1]",
+                    static_cast<long long>(p->num_pages));
+    const int64_t el = p->format == PARISKV_PAGES_BF16 ? 2 : 1;
+    const int64_t rows = static_cast<int64_t>(cfg->num_kv_heads) * p->page_size;
+    if (p->page_stride < rows * D || p->page_stride * el % 16 ||
+        p->page_stride > (int64_t(1) << 38))
+        return fail(PARISKV_EINVAL, "page_stride %lld: need >= num_kv_heads * page_size * 128 "
+                    "elements, a multiple of 16 bytes and at most 2^38",
+                    static_cast<long long>(p->page_stride));
+    if (p->format == PARISKV_PAGES_E4M3 &&
+        (p->scale_stride < rows || p->scale_stride % 16 || p->scale_stride > (int64_t(1) << 31)))
+        return fail(PARISKV_EINVAL, "scale_stride %lld: need >= num_kv_heads * page_size, a "
+                    "multiple of 16 and at most 2^31", static_cast<long long>(p->scale_stride));
+    if (c->table_width < 1 || c->table_stride < c->table_width)
+        return fail(PARISKV_EINVAL, "need 1 <= table_width <= table_stride");
+    if (c->total_q < 0 || c->total_q > INT32_MAX || c->max_q < 0)
+        return fail(PARISKV_EINVAL, "need 0 <= total_q < 2^31 and max_q >= 0");
+    return PARISKV_OK;
+}
+
+pariskv_status check_buffers(const pariskv_pages* p, const pariskv_chunk* c, bool starts, int dev) {
+    pariskv_status s;
+    if ((s = check_here(p->k, 16, "pages.k", dev)) != PARISKV_OK) return s;
+    if ((s = check_here(p->v, 16, "pages.v", dev)) != PARISKV_OK) return s;
+    if (p->format == PARISKV_PAGES_E4M3) {
+        if ((s = check_here(p->k_scale, 16, "pages.k_scale", dev)) != PARISKV_OK) return s;
+        if ((s = check_here(p->v_scale, 16, "pages.v_scale", dev)) != PARISKV_OK) return s;
+    }
+    if ((s = check_here(c->page_table, 4, "page_table", dev)) != PARISKV_OK) return s;
+    if ((s = check_here(c->kv_len, 4, "kv_len", dev)) != PARISKV_OK) return s;
+    if (starts && (s = check_here(c->q_start, 4, "q_start", dev)) != PARISKV_OK) return s;
+    return PARISKV_OK;
+}
+
+pariskv_status check_launch(int* dev) {
+    if (cudaGetDevice(dev) != cudaSuccess) return cuda_fail(cudaGetLastError(), "no device");
+    if (launch_fault_injected())
+        return fail(PARISKV_ECUDA, "injected launch failure (PARISKV_FAULT=launch)");
+    return PARISKV_OK;
+}
+
+PagePool pool_of(const pariskv_pages* p) {
+    PagePool v;
+    v.k = static_cast<uint8_t*>(p->k);
+    v.v = static_cast<uint8_t*>(p->v);
+    v.ks = p->k_scale;
+    v.vs = p->v_scale;
+    v.page_bytes = p->page_stride * (p->format == PARISKV_PAGES_BF16 ? 2 : 1);
+    v.scale_stride = p->scale_stride;
+    v.num_pages = static_cast<int32_t>(p->num_pages);
+    v.shift = 0;
+    while ((1 << v.shift) < p->page_size) ++v.shift;
+    return v;
+}
+
+Seqs seqs_of(const pariskv_config* cfg, const pariskv_chunk* c) {
+    return Seqs{c->page_table, c->kv_len, c->q_start, static_cast<int32_t>(c->total_q),
+                c->table_width, c->table_stride, c->max_q, cfg->batch};
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+pariskv_status pariskv_paged_write(const pariskv_config* cfg, const pariskv_pages* pages,
+                                   const pariskv_chunk* chunk, const void* k_new,
+                                   const void* v_new, int64_t k_ld, int64_t v_ld, void* stream) {
+    pariskv_status s = check_shapes(cfg, pages, chunk);
+    if (s != PARISKV_OK) return s;
+    const bool f32 = cfg->dtype == PARISKV_F32;
+    const int64_t row = static_cast<int64_t>(cfg->num_kv_heads) * D, word = f32 ? 4 : 8;
+    if (k_ld < row || v_ld < row || k_ld % word || v_ld % word)
+        return fail(PARISKV_EINVAL, "k_ld and v_ld must be >= num_kv_heads * 128 and whole "
+                    "16-byte words");
+    int dev = 0;
+    if ((s = check_launch(&dev)) != PARISKV_OK) return s;
+    if ((s = check_buffers(pages, chunk, true, dev)) != PARISKV_OK) return s;
+    set_last_launches(0);
+    if (chunk->total_q == 0) return PARISKV_OK;
+    if ((s = check_here(k_new, 16, "k_new", dev)) != PARISKV_OK) return s;
+    if ((s = check_here(v_new, 16, "v_new", dev)) != PARISKV_OK) return s;
+    const PagePool p = pool_of(pages);
+    const Seqs c = seqs_of(cfg, chunk);
+    const unsigned grid = static_cast<unsigned>(ceil_div(chunk->total_q, kWriteWarps));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int h = cfg->num_kv_heads, t = kWriteWarps * 32;
+    const bool e4 = pages->format == PARISKV_PAGES_E4M3;
+    const float* kf = static_cast<const float*>(k_new);
+    const float* vf = static_cast<const float*>(v_new);
+    const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(k_new);
+    const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(v_new);
+    if (f32 && e4) paged_write_kernel<float, true><<<grid, t, 0, st>>>(p, c, h, kf, vf, k_ld, v_ld);
+    else if (f32) paged_write_kernel<float, false><<<grid, t, 0, st>>>(p, c, h, kf, vf, k_ld, v_ld);
+    else if (e4) paged_write_kernel<__nv_bfloat16, true><<<grid, t, 0, st>>>(p, c, h, kb, vb, k_ld, v_ld);
+    else paged_write_kernel<__nv_bfloat16, false><<<grid, t, 0, st>>>(p, c, h, kb, vb, k_ld, v_ld);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "page write launch");
+    set_last_launches(1);
+    return PARISKV_OK;
+}
+
+pariskv_status pariskv_paged_read(const pariskv_config* cfg, const pariskv_pages* pages,
+                                  const pariskv_chunk* chunk, int64_t first, int64_t n, void* K,
+                                  void* V, int64_t ld_tok, void* stream) {
+    pariskv_status s = check_shapes(cfg, pages, chunk);
+    if (s != PARISKV_OK) return s;
+    if (first < 0 || n < 0 || first > INT32_MAX || n > INT32_MAX || ld_tok < n)
+        return fail(PARISKV_EINVAL, "need 0 <= first, 0 <= n <= ld_tok (below 2^31)");
+    if (!K && !V) return fail(PARISKV_EINVAL, "K and V are both NULL");
+    int dev = 0;
+    if ((s = check_launch(&dev)) != PARISKV_OK) return s;
+    if ((s = check_buffers(pages, chunk, false, dev)) != PARISKV_OK) return s;
+    if (K && (s = check_device_pointer(K, 16, "K")) != PARISKV_OK) return s;
+    if (V && (s = check_device_pointer(V, 16, "V")) != PARISKV_OK) return s;
+    set_last_launches(0);
+    if (n == 0) return PARISKV_OK;
+    const PagePool p = pool_of(pages);
+    const Seqs c = seqs_of(cfg, chunk);
+    const int64_t runs = ((first + n - 1) >> 4) - (first >> 4) + 1;
+    const int64_t total = runs * cfg->num_kv_heads * cfg->batch * (K && V ? 2 : 1);
+    const int64_t blocks = ceil_div(total, kReadWarps);
+    if (blocks > INT32_MAX) return fail(PARISKV_EINVAL, "too many rows for one call");
+    const unsigned grid = static_cast<unsigned>(blocks);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int h = cfg->num_kv_heads, t = kReadWarps * 32;
+    const bool e4 = pages->format == PARISKV_PAGES_E4M3, f32 = cfg->dtype == PARISKV_F32;
+    float *Kf = static_cast<float*>(K), *Vf = static_cast<float*>(V);
+    __nv_bfloat16 *Kb = static_cast<__nv_bfloat16*>(K), *Vb = static_cast<__nv_bfloat16*>(V);
+    if (f32 && e4) paged_read_kernel<float, true><<<grid, t, 0, st>>>(p, c, h, first, n, Kf, Vf, ld_tok, runs, total);
+    else if (f32) paged_read_kernel<float, false><<<grid, t, 0, st>>>(p, c, h, first, n, Kf, Vf, ld_tok, runs, total);
+    else if (e4) paged_read_kernel<__nv_bfloat16, true><<<grid, t, 0, st>>>(p, c, h, first, n, Kb, Vb, ld_tok, runs, total);
+    else paged_read_kernel<__nv_bfloat16, false><<<grid, t, 0, st>>>(p, c, h, first, n, Kb, Vb, ld_tok, runs, total);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "page read launch");
+    set_last_launches(1);
+    return PARISKV_OK;
+}
+
+pariskv_status pariskv_paged_attend(const pariskv_config* cfg, const pariskv_pages* pages,
+                                    const pariskv_chunk* chunk, const void* q, int64_t q_ld,
+                                    float scale, int32_t causal, void* out, int32_t out_dtype,
+                                    float* lse, void* stream) {
+    pariskv_status s = check_shapes(cfg, pages, chunk);
+    if (s != PARISKV_OK) return s;
+    if (cfg->dtype != PARISKV_BF16) return fail(PARISKV_EINVAL, "paged attention takes bf16 q");
+    if (cfg->group > 128) return fail(PARISKV_EINVAL, "group %d > 128", cfg->group);
+    if (out_dtype != PARISKV_F32 && out_dtype != PARISKV_BF16)
+        return fail(PARISKV_EINVAL, "out_dtype %d unknown", out_dtype);
+    if (!(scale == scale)) return fail(PARISKV_EINVAL, "scale is NaN");
+    const int64_t hq = static_cast<int64_t>(cfg->num_kv_heads) * cfg->group;
+    if (q_ld < hq * D || q_ld % 8)
+        return fail(PARISKV_EINVAL, "q_ld must be >= query heads * 128 and a multiple of 8");
+    if (chunk->total_q * cfg->group > INT32_MAX)
+        return fail(PARISKV_EINVAL, "total_q * group must be below 2^31");
+    int dev = 0, sms = 0;
+    if ((s = check_launch(&dev)) != PARISKV_OK) return s;
+    if ((s = check_buffers(pages, chunk, true, dev)) != PARISKV_OK) return s;
+    set_last_launches(0);
+    if (chunk->total_q == 0 || chunk->max_q == 0) return PARISKV_OK;
+    if ((s = check_here(q, 16, "q", dev)) != PARISKV_OK) return s;
+    if ((s = check_here(out, 16, "out", dev)) != PARISKV_OK) return s;
+    if (lse && (s = check_here(lse, 4, "lse", dev)) != PARISKV_OK) return s;
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+
+    AttendArgs a{};
+    a.pool = pool_of(pages);
+    a.seqs = seqs_of(cfg, chunk);
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.q_ld = q_ld;
+    a.heads = cfg->num_kv_heads;
+    a.scale = scale;
+    a.out = out;
+    a.lse = lse;
+    a.shape.group = cfg->group;
+    a.shape.causal = causal != 0;
+    a.shape.tile_rows = 16;
+    a.shape.block = kFewBlock;
+    const int ctas = few_ctas(sms);
+    // tiles: every sequence may end in a part of one
+    const int64_t most = static_cast<int64_t>(chunk->max_q) * cfg->group;
+    const int64_t tiles = min64(cfg->batch * ceil_div(most, a.shape.tile_rows),
+                                chunk->total_q * cfg->group / a.shape.tile_rows + cfg->batch);
+    if (tiles > (1 << 28)) return fail(PARISKV_EINVAL, "too many query rows for one call");
+    const size_t pre = round_up((tiles + 1) * 8, 256), ids = round_up(tiles * 4, 256);
+    const size_t parts = round_up(2 * ctas * part_floats(a.shape.tile_rows) * 4, 256);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    void* ws = nullptr;
+    if ((s = take_workspace(&ws, parts + pre + 2 * ids + 256, st)) != PARISKV_OK) return s;
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    a.work = reinterpret_cast<float*>(w);
+    a.plan.pre = reinterpret_cast<int64_t*>(w + parts);
+    a.plan.seq = reinterpret_cast<int32_t*>(w + parts + pre);
+    a.plan.row = reinterpret_cast<int32_t*>(w + parts + pre + ids);
+    a.plan.ntiles = reinterpret_cast<int32_t*>(w + parts + pre + 2 * ids);
+    a.plan.max_tiles = static_cast<int32_t>(tiles);
+    const bool f32 = out_dtype == PARISKV_F32;
+    cudaError_t e = launch_plan(a, st);
+    if (e == cudaSuccess) e = launch_attend_few(a, pages->format, f32, ctas, st);
+    if (e == cudaSuccess) e = launch_join(a, ctas, f32, st);
+    cudaFreeAsync(ws, st);
+    if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
+    set_last_launches(3);
+    return PARISKV_OK;
+}
+
+}  // extern "C"

@@ -1,6 +1,6 @@
 """Thin ctypes binding over libpariskv.so (the C ABI declared in include/pariskv.h,
-include/pariskv_cache.h, include/pariskv_dense.h, include/pariskv_learned.h and
-include/pariskv_debug.h).
+include/pariskv_cache.h, include/pariskv_dense.h, include/pariskv_learned.h,
+include/pariskv_paged.h and include/pariskv_debug.h).
 
 Only argument marshalling happens here: tensors become data pointers and strides become the
 library's slab strides; every step of the retrieval path runs in the library's CUDA kernels.
@@ -22,11 +22,12 @@ LIB_PATH = os.path.join(_PKG, "_lib", "libpariskv_check.so" if os.environ.get(
     "PARISKV_LIBRARY") == "check" else "libpariskv.so")
 HEADERS = [os.path.join(os.path.dirname(_PKG), "include", h)
            for h in ("pariskv.h", "pariskv_cache.h", "pariskv_dense.h", "pariskv_learned.h",
-                     "pariskv_debug.h")]
+                     "pariskv_paged.h", "pariskv_debug.h")]
 
 OK, EINVAL, ENOMEM, ECUDA, ECAPACITY, ETIMEOUT = range(6)
 F32, BF16 = 0, 1
 LEVELS_UNIFORM, LEVELS_PRIOR, LEVELS_TABLE = range(3)
+PAGES_BF16, PAGES_E4M3 = 0, 1
 
 
 class PariskvError(RuntimeError):
@@ -56,6 +57,20 @@ class CacheConfig(ctypes.Structure):
     _fields_ = [("n_sink", ctypes.c_int32), ("n_local", ctypes.c_int32),
                 ("n_buffer", ctypes.c_int32), ("k", ctypes.c_int32),
                 ("retrieval_capacity", ctypes.c_int64)]
+
+
+class _Pages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class _Chunk(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("q_start", ctypes.c_void_p), ("total_q", ctypes.c_int64),
+                ("table_width", ctypes.c_int32), ("table_stride", ctypes.c_int32),
+                ("max_q", ctypes.c_int32)]
 
 
 if not os.path.exists(LIB_PATH):
@@ -112,6 +127,13 @@ _SIGS = {
     "pariskv_cache_counts": (_S, [_P, ctypes.POINTER(_I64)]),
     "pariskv_cache_index": (_P, [_P]),
     "pariskv_cache_destroy": (_S, [_P]),
+    "pariskv_paged_write": (_S, [ctypes.POINTER(Config), ctypes.POINTER(_Pages),
+                                 ctypes.POINTER(_Chunk), _P, _P, _I64, _I64, _P]),
+    "pariskv_paged_read": (_S, [ctypes.POINTER(Config), ctypes.POINTER(_Pages),
+                                ctypes.POINTER(_Chunk), _I64, _I64, _P, _P, _I64, _P]),
+    "pariskv_paged_attend": (_S, [ctypes.POINTER(Config), ctypes.POINTER(_Pages),
+                                  ctypes.POINTER(_Chunk), _P, _I64, ctypes.c_float, _I32, _P,
+                                  _I32, _P, _P]),
 }
 
 STAGES = ("query_prep", "vote", "threshold", "compact", "rerank", "topk")
@@ -518,3 +540,155 @@ class Cache:
             self.destroy()
         except Exception:
             pass
+
+
+def _refuse(where: str, message: str) -> None:
+    raise PariskvError(EINVAL, where, message)
+
+
+class Pages:
+    """pariskv_pages: a view of the caller's page pool. k, v: [num_pages, num_kv_heads,
+    page_size, 128], bf16 or float8_e4m3fn (8-bit pages, with k_scale and v_scale: uint8
+    [num_pages, num_kv_heads, page_size]). A page's rows are contiguous; pages may lie apart (a
+    slice [:, i] of a pool that holds K and V side by side)."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v.dtype != k.dtype:
+            _refuse("Pages", f"k and v must both be bfloat16 or float8_e4m3fn, not {k.dtype} "
+                    f"and {v.dtype}")
+        e4m3 = k.dtype == torch.float8_e4m3fn
+        if k.dim() != 4 or k.shape[-1] != 128 or v.shape != k.shape:
+            _refuse("Pages", "k and v must be [num_pages, num_kv_heads, page_size, 128], both "
+                    f"alike, not {tuple(k.shape)} and {tuple(v.shape)}")
+        n, h, ps, d = k.shape
+        for x in (k, v):
+            if x.stride()[1:] != (ps * d, d, 1) or (n > 1 and x.stride(0) != k.stride(0)):
+                _refuse("Pages", "a page's rows must be contiguous, and the pages of k and v the "
+                        "same distance apart")
+        if e4m3 != (k_scale is not None) or e4m3 != (v_scale is not None):
+            _refuse("Pages", "k_scale and v_scale go with float8_e4m3fn pages, and only with them")
+        for x in (k_scale, v_scale) if e4m3 else ():
+            if x.dtype != torch.uint8 or x.shape != (n, h, ps) or x.stride()[1:] != (ps, 1) or (
+                    n > 1 and x.stride(0) != k_scale.stride(0)):
+                _refuse("Pages", "scales must be uint8 [num_pages, num_kv_heads, page_size] with "
+                        "contiguous pages, both alike")
+        self.tensors = (k, v, k_scale, v_scale)      # keeps the memory
+        self.num_kv_heads = h
+        self.raw = _Pages(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if e4m3 else None,
+                          v_scale.data_ptr() if e4m3 else None, n,
+                          k.stride(0) if n > 1 else h * ps * d,
+                          (k_scale.stride(0) if n > 1 else h * ps) if e4m3 else 0, ps,
+                          PAGES_E4M3 if e4m3 else PAGES_BF16)
+        self.ref = ctypes.byref(self.raw)
+
+
+class Chunk:
+    """pariskv_chunk: new tokens of a batch of sequences. page_table int32 [batch, width], kv_len
+    int32 [batch] (the new tokens counted in), q_start int32 [batch + 1]; total_q: rows of the
+    per-token tensors; max_q: at least the longest sequence's number of new tokens. The contents
+    may change between calls (in place), and under a captured graph."""
+
+    def __init__(self, page_table, kv_len, q_start, total_q: int, max_q: int):
+        import torch
+        for name, x in (("page_table", page_table), ("kv_len", kv_len), ("q_start", q_start)):
+            if x.dtype != torch.int32 or x.stride(-1) != 1:
+                _refuse("Chunk", f"{name} must be int32 with contiguous rows")
+        if page_table.dim() != 2 or kv_len.shape != page_table.shape[:1] or \
+                q_start.shape != (page_table.shape[0] + 1,):
+            _refuse("Chunk", "need page_table [batch, width], kv_len [batch], q_start [batch + 1]")
+        self.tensors = (page_table, kv_len, q_start)
+        self.batch = page_table.shape[0]
+        width = page_table.shape[1]
+        self.raw = _Chunk(page_table.data_ptr(), kv_len.data_ptr(), q_start.data_ptr(),
+                          int(total_q), width, max(width, page_table.stride(0))
+                          if self.batch > 1 else width, int(max_q))
+        self.ref = ctypes.byref(self.raw)
+
+
+def _paged_args(where: str, cfg: Config, pages: Pages, chunk: Chunk) -> None:
+    if pages.num_kv_heads != cfg.num_kv_heads or chunk.batch != cfg.batch:
+        _refuse(where, f"cfg is for {cfg.batch} sequences and {cfg.num_kv_heads} KV heads, the "
+                f"chunk for {chunk.batch} and the pages for {pages.num_kv_heads}")
+
+
+def _per_token(where: str, name: str, x, dtype, rows: int, heads: int) -> int:
+    """Token stride of a per-token tensor [rows, heads, 128]."""
+    if x.dtype != dtype or x.dim() != 3 or x.shape != (rows, heads, 128) or (
+            rows and x.stride()[1:] != (128, 1) and heads > 1) or (rows and x.stride(2) != 1):
+        _refuse(where, f"{name} must be {dtype} [{rows}, {heads}, 128] with contiguous tokens, "
+                f"not {x.dtype} {tuple(x.shape)} with strides {x.stride()}")
+    return x.stride(0) if rows > 1 else heads * 128
+
+
+def _cfg_dtype(cfg: Config):
+    import torch
+    return torch.bfloat16 if cfg.dtype == BF16 else torch.float32
+
+
+def paged_write(cfg: Config, pages: Pages, chunk: Chunk, k_new, v_new, stream=None) -> None:
+    """pariskv_paged_write: the new tokens' rows (k_new, v_new: [total_q, num_kv_heads, 128] of
+    cfg's dtype) into their pages."""
+    where = "pariskv_paged_write"
+    _paged_args(where, cfg, pages, chunk)
+    n, dt = chunk.raw.total_q, _cfg_dtype(cfg)
+    k_ld = _per_token(where, "k_new", k_new, dt, n, cfg.num_kv_heads)
+    v_ld = _per_token(where, "v_new", v_new, dt, n, cfg.num_kv_heads)
+    _check(lib.pariskv_paged_write(ctypes.byref(cfg), pages.ref, chunk.ref, k_new.data_ptr(),
+                                   v_new.data_ptr(), k_ld, v_ld, _stream(stream)), where)
+
+
+def paged_read(cfg: Config, pages: Pages, chunk: Chunk, first: int, n: int, K=None, V=None,
+               stream=None) -> None:
+    """pariskv_paged_read: positions [first, first + n) of every sequence into the slabs K and/or
+    V ([batch, num_kv_heads, L, 128] of cfg's dtype, device or pinned host, n <= L)."""
+    where = "pariskv_paged_read"
+    _paged_args(where, cfg, pages, chunk)
+    ld = None
+    for name, x in (("K", K), ("V", V)):
+        if x is None:
+            continue
+        shape = (cfg.batch, cfg.num_kv_heads)
+        if x.dtype != _cfg_dtype(cfg) or x.dim() != 4 or x.shape[:2] != shape or \
+                x.shape[3] != 128 or x.shape[2] < n or x.stride()[2:] != (128, 1):
+            _refuse(where, f"{name} must be {_cfg_dtype(cfg)} [batch, num_kv_heads, >= {n}, 128] "
+                    f"with contiguous rows, not {x.dtype} {tuple(x.shape)}")
+        step = x.stride(1) if x.shape[1] > 1 else (x.stride(0) if x.shape[0] > 1
+                                                   else x.shape[2] * 128)
+        if step % 128 or (x.shape[0] > 1 and x.stride(0) != step * x.shape[1]) or \
+                ld not in (None, step // 128):
+            _refuse(where, "the slabs of K and V must be evenly spaced, both alike")
+        ld = step // 128
+    _check(lib.pariskv_paged_read(ctypes.byref(cfg), pages.ref, chunk.ref, int(first), int(n),
+                                  K.data_ptr() if K is not None else None,
+                                  V.data_ptr() if V is not None else None,
+                                  int(n) if ld is None else ld, _stream(stream)), where)
+
+
+def paged_attend(cfg: Config, pages: Pages, chunk: Chunk, q, scale: float, causal: bool = True,
+                 out=None, out_dtype=None, lse=None, want_lse: bool = False, stream=None):
+    """pariskv_paged_attend: attention of the new tokens (q: bf16 [total_q, Hq, 128]) over the
+    pages. Returns (out, lse): out [total_q, Hq, 128] of ``out_dtype`` (torch.bfloat16, the
+    default, or torch.float32), lse fp32 [total_q, Hq] or None (see ``want_lse``). Rows that
+    belong to no sequence are left as they are in tensors given, and are undefined in new ones."""
+    import torch
+    where = "pariskv_paged_attend"
+    _paged_args(where, cfg, pages, chunk)
+    n, hq = chunk.raw.total_q, cfg.num_q_heads
+    q_ld = _per_token(where, "q", q, torch.bfloat16, n, hq)
+    if out is None:
+        out = torch.empty((n, hq, 128), dtype=out_dtype or torch.bfloat16, device=q.device)
+    if out.dtype not in (torch.bfloat16, torch.float32) or out.shape != (n, hq, 128) or \
+            not out.is_contiguous() or out_dtype not in (None, out.dtype):
+        _refuse(where, f"out must be contiguous bfloat16 or float32 [{n}, {hq}, 128]")
+    if lse is None and want_lse:
+        lse = torch.empty((n, hq), dtype=torch.float32, device=q.device)
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, hq)
+                            or not lse.is_contiguous()):
+        _refuse(where, f"lse must be contiguous float32 [{n}, {hq}]")
+    _check(lib.pariskv_paged_attend(ctypes.byref(cfg), pages.ref, chunk.ref, q.data_ptr(), q_ld,
+                                    float(scale), int(bool(causal)), out.data_ptr(),
+                                    BF16 if out.dtype == torch.bfloat16 else F32,
+                                    lse.data_ptr() if lse is not None else None,
+                                    _stream(stream)), where)
+    return out, lse

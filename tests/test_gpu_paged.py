@@ -1,0 +1,403 @@
+"""The paged K/V cache on the GPU (include/pariskv_paged.h) against 64-bit references: codes and
+scale bytes exactly, read-back exactly, attention within bounds counted from its roundings."""
+import numpy as np
+import pytest
+import torch
+
+import paged_reference as ref
+from long_context_kv_srht_b200 import pariskv as pk
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+D = 128
+SCALE = 1 / np.sqrt(D)
+
+
+def _dev(a, dtype=None):
+    return torch.tensor(np.ascontiguousarray(a), device=DEV, dtype=dtype)
+
+
+def _bf(a):
+    return _dev(ref.bf16_round(np.asarray(a, np.float32))).to(torch.bfloat16)
+
+
+class Case:
+    """A ragged batch with its pages in random order. q, kv: lengths; holes: (s, page) entries
+    taken out of the table. Slots that hold no token are NaN (bf16) or NaN rows (8-bit)."""
+
+    def __init__(self, seed, fmt, q, kv, heads=2, group=4, page=16, holes=(), width=None, spare=2,
+                 tail=3, amp=1.0):
+        rng = np.random.default_rng(seed)
+        self.fmt, self.heads, self.group, self.page = fmt, heads, group, page
+        self.q_len, self.kv = list(q), np.array(kv, np.int32)
+        batch = len(q)
+        self.width = width or max(1, max(-(-n // page) for n in kv))
+        need = [min(self.width, -(-n // page)) for n in kv]
+        self.pages = sum(need) + spare
+        order = rng.permutation(self.pages)
+        self.table = np.full((batch, self.width), -1, np.int32)
+        at = 0
+        for s in range(batch):
+            self.table[s, :need[s]] = order[at:at + need[s]]
+            at += need[s]
+        for s, p in holes:
+            self.table[s, p] = [-1, self.pages, -(1 << 31), (1 << 31) - 1][(s + p) % 4]
+        self.q_start = np.concatenate([[0], np.cumsum(q)]).astype(np.int32)
+        self.total = int(self.q_start[-1]) + tail          # rows behind the last sequence
+        shape = (self.pages, heads, page, D)
+        k = rng.standard_normal(shape).astype(np.float32) * amp
+        k[..., rng.integers(0, D, 4)] *= 4
+        v = rng.standard_normal(shape).astype(np.float32)
+        self.q = ref.bf16_round(rng.standard_normal((self.total, heads * group, D)).astype(np.float32))
+        self.live = np.zeros((self.pages, page), bool)
+        c = ref.Cache(k, v, self.table, self.kv, self.q_start)
+        for s in range(batch):
+            for t in c.tokens(s):
+                self.live[c.slot(s, t)] = True
+        if fmt == "bf16":
+            self.k, self.v = ref.bf16_round(k), ref.bf16_round(v)
+            for x in (self.k, self.v):
+                x[~np.broadcast_to(self.live[:, None], x.shape[:3])] = np.nan
+            self.kd, self.vd = _dev(self.k).to(torch.bfloat16), _dev(self.v).to(torch.bfloat16)
+            self.ks = self.vs = None
+        else:
+            (self.kc, self.kb), (self.vc, self.vb) = self._codes(k), self._codes(v)
+            dead = ~np.broadcast_to(self.live[:, None], self.kb.shape)
+            for codes, byte in ((self.kc, self.kb), (self.vc, self.vb)):
+                codes[dead], byte[dead] = 0x7f, 255
+            self.k, self.v = ref.dequantise(self.kc, self.kb), ref.dequantise(self.vc, self.vb)
+            self.kd, self.vd = (_dev(x).view(torch.float8_e4m3fn) for x in (self.kc, self.vc))
+            self.ks, self.vs = _dev(self.kb), _dev(self.vb)
+        self.cfg = pk.config(batch=batch, num_kv_heads=heads, group=group, dtype="bf16")
+        self.chunk = pk.Chunk(_dev(self.table), _dev(self.kv), _dev(self.q_start), self.total,
+                              max(max(q), 1))
+
+    @staticmethod
+    def _codes(x):
+        flat = [ref.quantise_row(r) for r in x.reshape(-1, D)]
+        return (np.stack([c for c, _ in flat]).reshape(x.shape),
+                np.array([b for _, b in flat], np.uint8).reshape(x.shape[:3]))
+
+    def pool(self):
+        return pk.Pages(self.kd, self.vd, self.ks, self.vs)
+
+    def reference(self, causal, scale=SCALE):
+        c = ref.Cache(np.float64(self.k), np.float64(self.v), self.table, self.kv, self.q_start)
+        return ref.attend(c, np.float64(self.q), self.group, scale, causal)
+
+    def check(self, out, lse, causal, scale=SCALE):
+        o, l, w, reach = self.reference(causal, scale)
+        f32 = out.dtype == torch.float32
+        tol, ltol = ref.tolerances(w, reach, o, int(self.kv.max()), 2.0 ** (-24 if f32 else -8),
+                                   2.0 ** (-24 if f32 else -8))
+        got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        n = int(self.q_start[-1])
+        assert np.isnan(got[n:]).all() and np.isnan(gl[n:]).all(), "rows of no sequence written"
+        err = np.abs(got[:n] - o[:n])
+        assert (err <= tol[:n]).all(), (err.max(), (err / tol[:n]).max(),
+                                        np.argwhere(~(err <= tol[:n]))[:5])
+        empty = np.isneginf(l[:n])
+        assert (np.isneginf(gl[:n]) == empty).all()
+        lerr = np.abs(np.where(empty, 0, gl[:n]) - np.where(empty, 0, l[:n]))
+        assert (lerr <= ltol[:n] + 2.0 ** -24 * np.abs(np.where(empty, 0, l[:n]))).all(), lerr.max()
+
+
+def _attend(c, causal=True, out_dtype=torch.bfloat16, q=None, chunk=None, scale=SCALE, pages=None):
+    n, hq = c.total, c.heads * c.group
+    out = torch.full((n, hq, D), float("nan"), dtype=out_dtype, device=DEV)
+    lse = torch.full((n, hq), float("nan"), device=DEV)
+    q = _bf(c.q) if q is None else q
+    pk.paged_attend(c.cfg, pages or c.pool(), chunk or c.chunk, q, scale, causal=causal, out=out,
+                    lse=lse)
+    return out, lse
+
+
+# ------------------------------------------------------------------------------- write, read
+def _fresh(c):
+    """An empty pool of c's shape, filled with a pattern."""
+    k = torch.full(c.kd.shape, 1.5, device=DEV).to(c.kd.dtype)
+    ks = None if c.ks is None else torch.full(c.ks.shape, 77, dtype=torch.uint8, device=DEV)
+    return pk.Pages(k, k.clone(), ks, None if ks is None else ks.clone())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("page,heads,q,kv,holes", [
+    (16, 1, [1], [1], ()),
+    (16, 2, [3, 0, 40, 1], [3, 17, 60, 33], ((2, 2),)),
+    (64, 3, [65, 1, 130], [65, 64, 200], ()),
+    (256, 5, [7, 300], [300, 301], ((1, 1),)),
+    (32, 8, [10, 4], [6, 4], ()),                     # kv_len < q_len: positions below zero
+])
+def test_write_matches_definition(fmt, dtype, page, heads, q, kv, holes):
+    c = Case(11, fmt, q, kv, heads=heads, group=1, page=page, holes=holes)
+    rng = np.random.default_rng(5)
+    new = rng.standard_normal((2, c.total, heads, D)).astype(np.float32)
+    new *= 10.0 ** rng.integers(-6, 6, (2, c.total, heads, 1))
+    new[0, 0, 0] = 0
+    if dtype == "bf16":
+        new = ref.bf16_round(new)
+    c.cfg.dtype = pk.BF16 if dtype == "bf16" else pk.F32
+    pages = _fresh(c)
+    want = [t.clone().float().cpu().numpy() if t is not None and t.dtype != torch.uint8 else
+            None if t is None else t.clone().cpu().numpy() for t in pages.tensors]
+    cache = ref.Cache(np.zeros(c.kd.shape), None, c.table, c.kv, c.q_start)
+    for s in range(len(q)):
+        for row, pos in cache.rows(s):
+            at = cache.slot(s, pos) if pos < c.kv[s] else None
+            if at is None:
+                continue
+            for i in range(2):
+                for h in range(heads):
+                    if fmt == "bf16":
+                        want[i][at[0], h, at[1]] = ref.bf16_round(new[i, row, h])
+                    else:
+                        code, byte = ref.quantise_row(new[i, row, h])
+                        want[i][at[0], h, at[1]] = ref.VALUES[code]
+                        want[2 + i][at[0], h, at[1]] = byte
+    kn, vn = (_bf(x) if dtype == "bf16" else _dev(x) for x in new)
+    pk.paged_write(c.cfg, pages, c.chunk, kn, vn)
+    assert pk.last_launch_count() == 1
+    for t, w in zip(pages.tensors, want):
+        if t is not None:
+            np.testing.assert_array_equal(t.float().cpu().numpy(), w)
+
+
+def test_write_strides_special_rows_and_extremes():
+    """Rows inside a wider tensor; rows with an infinity or NaN; the largest and least floats."""
+    c = Case(3, "e4m3", [8], [8], heads=2, group=1, page=16)
+    c.cfg.dtype = pk.F32
+    rng = np.random.default_rng(2)
+    wide = rng.standard_normal((c.total, 6, D)).astype(np.float32)
+    wide[0, 0, 5], wide[1, 0, 7], wide[2, 1, 0] = np.inf, np.nan, -np.inf
+    wide[3, 0], wide[3, 1] = 3.4e38, 1e-44
+    wide[4, 0, 1:], wide[4, 0, 0] = 0, 448 * 2.0 ** 10
+    wide[5, 0, 1:], wide[5, 0, 0] = 0, np.nextafter(np.float32(448 * 2.0 ** 10), np.float32(np.inf))
+    wide[6, 0] = np.float32(2.0 ** -126) * np.arange(D)
+    t = _dev(wide)
+    pages = _fresh(c)
+    pk.paged_write(c.cfg, pages, c.chunk, t[:, :2], t[:, 2:4])
+    k, v, ks, vs = (x.float().cpu().numpy() for x in pages.tensors)
+    for i in range(8):
+        p = c.table[0, 0]
+        for h in range(2):
+            for got, gs, src in ((k, ks, wide[i, h]), (v, vs, wide[i, 2 + h])):
+                code, byte = ref.quantise_row(src)
+                assert gs[p, h, i] == byte
+                np.testing.assert_array_equal(got[p, h, i], ref.VALUES[code])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("page,kv,first,n,holes", [
+    (16, [1], 0, 1, ()), (16, [50, 7, 0, 91], 5, 60, ((0, 1), (3, 5))),
+    (128, [300, 129], 127, 200, ()), (256, [513], 250, 263, ((0, 1),)), (32, [40], 100, 8, ())])
+def test_read_matches_pages(fmt, dtype, page, kv, first, n, holes):
+    c = Case(7, fmt, [1] * len(kv), kv, heads=3, group=1, page=page, holes=holes)
+    c.cfg.dtype = pk.BF16 if dtype == "bf16" else pk.F32
+    td = torch.bfloat16 if dtype == "bf16" else torch.float32
+    shape = (len(kv), 3, n + 5, D)
+    K, V = (torch.full(shape, -7.0, dtype=td, device=DEV) for _ in range(2))
+    pk.paged_read(c.cfg, c.pool(), c.chunk, first, n, K, V)
+    wK, wV = np.full(shape, -7.0), np.full(shape, -7.0)
+    cache = ref.Cache(np.float64(c.k), np.float64(c.v), c.table, c.kv, c.q_start)
+    for s in range(len(kv)):
+        for t in cache.tokens(s):
+            if first <= t < first + n:
+                p, r = cache.slot(s, t)
+                wK[s, :, t - first], wV[s, :, t - first] = cache.k[p, :, r], cache.v[p, :, r]
+    np.testing.assert_array_equal(K.float().cpu().numpy(), wK)
+    np.testing.assert_array_equal(V.float().cpu().numpy(), wV)
+    # one of the two alone, and into pinned host memory
+    V2 = torch.full(shape, -7.0, dtype=td).pin_memory()
+    pk.paged_read(c.cfg, c.pool(), c.chunk, first, n, V=V2)
+    K2 = torch.full(shape, -7.0, dtype=td, device=DEV)
+    pk.paged_read(c.cfg, c.pool(), c.chunk, first, n, K=K2)
+    torch.cuda.synchronize()
+    assert torch.equal(V2, V.cpu()) and torch.equal(K2, K)
+
+
+# ------------------------------------------------------------------------------------ attend
+LENGTHS = [
+    ([1], [1]), ([1], [100]), ([1, 1, 1], [64, 65, 700]), ([3, 1, 0, 5], [3, 40, 12, 129]),
+    ([17, 1], [17, 300]), ([40, 130], [90, 131]), ([200], [457]),
+]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("q,kv", LENGTHS)
+def test_attend_lengths(fmt, out_dtype, causal, q, kv):
+    c = Case(sum(kv), fmt, q, kv, heads=2, group=4, page=32)
+    out, lse = _attend(c, causal, out_dtype)
+    c.check(out, lse, causal)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,group", [(1, 1), (3, 2), (2, 3), (1, 5), (2, 7), (1, 8), (1, 12),
+                                         (1, 16), (2, 40), (1, 128)])
+@pytest.mark.parametrize("page", [16, 64, 256])
+def test_attend_head_layouts_and_pages(fmt, heads, group, page):
+    c = Case(group * 31 + page, fmt, [1, 4, 33], [70, 4, 290], heads=heads, group=group, page=page)
+    out, lse = _attend(c)
+    c.check(out, lse, True)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_attend_holes_empty_rows_and_positions_below_zero(fmt, out_dtype):
+    """Pages given back (every kind of id that is none), rows whose whole past is gone, sequences
+    shorter than their chunk, and a table too narrow for the length."""
+    holes = [(0, p) for p in (0, 1, 2, 5, 9)] + [(1, 0), (2, 0), (2, 1), (2, 2)]
+    c = Case(9, fmt, [6, 40, 3, 70, 2], [200, 33, 44, 300, 60], heads=2, group=3, page=16,
+             holes=holes, width=16)
+    for causal in (True, False):
+        out, lse = _attend(c, causal, out_dtype)
+        c.check(out, lse, causal)
+    assert torch.isneginf(lse[c.q_start[2]:c.q_start[3]]).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("q,kv", [([5], [70]), ([130], [140]), ([300], [300])])
+def test_nan_and_inf_reach_only_rows_that_see_them(fmt, q, kv):
+    """Tokens of the chunk itself hold NaN or infinity in K and V: earlier rows are exact."""
+    c = Case(21, fmt, q, kv, heads=1, group=4, page=16)
+    base, blse = _attend(c)
+    at = kv[0] - q[0] // 2 - 1                       # a position inside the chunk
+    p, r = c.table[0, at // 16], at % 16
+    row = at - (kv[0] - q[0])                        # its row
+    for which in ("v", "k"):
+        x = getattr(c, which + "d").clone()
+        sc = None if c.ks is None else (c.ks if which == "k" else c.vs).clone()
+        if fmt == "bf16":
+            x[p, 0, r, 3], x[p, 0, r, 100] = float("nan"), float("inf")
+        else:
+            x.view(torch.uint8)[p, 0, r], sc[p, 0, r] = 0x7f, 255
+        pages = pk.Pages(x if which == "k" else c.kd, x if which == "v" else c.vd,
+                         sc if which == "k" else c.ks, sc if which == "v" else c.vs)
+        out, lse = _attend(c, pages=pages)
+        n = q[0]
+        assert torch.equal(out[:row], base[:row]) and torch.equal(lse[:row], blse[:row])
+        seen = out[row:n].float()
+        if which == "k":
+            assert torch.isnan(seen).all() and not torch.isfinite(lse[row:n]).any()
+        else:
+            dims = [3, 100] if fmt == "bf16" else list(range(D))
+            assert not torch.isfinite(seen[..., dims]).any()
+            rest = [d for d in range(D) if d not in dims]
+            assert torch.equal(out[row:n][..., rest], base[row:n][..., rest])
+            assert torch.equal(lse[:n], blse[:n])
+
+
+def test_large_scores_and_strided_q_and_interleaved_pool():
+    """A saturated softmax, q as a slice of a fused projection, K and V side by side in one pool,
+    a table with room behind it, negative and zero scales."""
+    c = Case(4, "bf16", [9, 1], [200, 65], heads=2, group=4, page=32, amp=8.0)
+    fused = torch.zeros((c.total, c.heads * (c.group + 2), D), dtype=torch.bfloat16, device=DEV)
+    fused[:, :c.heads * c.group] = _bf(c.q)
+    pool = torch.stack([c.kd, c.vd], 1)
+    table = torch.full((2, c.width + 3), -5, dtype=torch.int32, device=DEV)
+    table[:, :c.width] = _dev(c.table)
+    chunk = pk.Chunk(table[:, :c.width], _dev(c.kv), _dev(c.q_start), c.total, 9)
+    pages = pk.Pages(pool[:, 0], pool[:, 1])
+    for scale in (3.0, SCALE, 0.0, -0.5):
+        out, lse = _attend(c, out_dtype=torch.float32, q=fused[:, :c.heads * c.group], chunk=chunk,
+                           scale=scale, pages=pages)
+        c.check(out, lse, True, scale)
+
+
+def test_rows_past_max_q_are_left_and_malformed_starts_stay_inside():
+    c = Case(6, "bf16", [40, 2], [90, 2], heads=2, group=4, page=16)
+    full, _ = _attend(c)
+    short = pk.Chunk(_dev(c.table), _dev(c.kv), _dev(c.q_start), c.total, 7)
+    out, lse = _attend(c, chunk=short)
+    assert torch.equal(out[:7], full[:7]) and torch.isnan(out[7:40].float()).all()
+    assert torch.equal(out[40:42], full[40:42])
+    # starts that overlap, run backwards or leave the arrays: nothing outside is touched
+    for starts in ([0, 45, 20], [40, 0, 45], [-5, 10, 1000], [30, 1 << 30, (1 << 31) - 1],
+                   [-(1 << 31), (1 << 31) - 1, 0]):
+        bad = pk.Chunk(_dev(c.table), _dev(c.kv), _dev(np.array(starts, np.int32)), c.total, 45)
+        _attend(c, chunk=bad)
+        kn = torch.zeros((c.total, 2, D), dtype=torch.bfloat16, device=DEV)
+        pk.paged_write(c.cfg, _fresh(c), bad, kn, kn)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_same_bits_on_every_call_streams_and_graphs(fmt):
+    """Twice in a row, on another stream, and from a captured graph that follows new lengths."""
+    c = Case(12, fmt, [1, 1, 1], [900, 33, 400], heads=2, group=4, page=16)
+    q = _bf(c.q)
+    a, al = _attend(c, q=q)
+    b, bl = _attend(c, q=q)
+    assert torch.equal(a[:3], b[:3]) and torch.equal(al[:3], bl[:3])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        b, bl = _attend(c, q=q)
+    s.synchronize()
+    assert torch.equal(a[:3], b[:3]) and torch.equal(al[:3], bl[:3])
+    graphs, outs = [], []
+    pages = c.pool()
+    kv = c.chunk.tensors[1]
+    for _ in range(2):                      # two graphs that live at once
+        out, lse = torch.zeros_like(a), torch.zeros_like(al)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pk.paged_attend(c.cfg, pages, c.chunk, q, SCALE, out=out, lse=lse)
+        graphs.append(g)
+        outs.append((out, lse))
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for out, lse in outs:
+        assert torch.equal(out[:3], a[:3]) and torch.equal(lse[:3], al[:3])
+    kv.copy_(_dev(np.array([77, 20, 399], np.int32)))
+    want, wl = _attend(c, q=q)
+    graphs[1].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[1][0][:3], want[:3]) and torch.equal(outs[1][1][:3], wl[:3])
+
+
+def test_many_sequences():
+    """More sequences than the plan takes at once, lengths from zero on."""
+    rng = np.random.default_rng(0)
+    n = 1500
+    q = rng.integers(0, 3, n).tolist()
+    kv = [int(a + rng.integers(0, 40)) for a in q]
+    c = Case(1, "e4m3", q, kv, heads=1, group=2, page=16)
+    out, lse = _attend(c)
+    c.check(out, lse, True)
+
+
+def test_refusals_with_device_buffers():
+    c = Case(2, "bf16", [2], [20], heads=2, group=4, page=16)
+    q, pages = _bf(c.q), c.pool()
+    host = torch.zeros((c.total, 2, D), dtype=torch.bfloat16)
+    for bad in (host, host.pin_memory()):
+        with pytest.raises(pk.PariskvError) as e:
+            pk.paged_write(c.cfg, pages, c.chunk, bad, bad)
+        assert e.value.status == pk.EINVAL and "device memory" in str(e.value)
+    with pytest.raises(pk.PariskvError):
+        pk.paged_attend(c.cfg, pages, c.chunk, q, float("nan"))
+    f32 = pk.config(batch=1, num_kv_heads=2, group=4, dtype="f32")
+    with pytest.raises(pk.PariskvError):
+        pk.paged_attend(f32, pages, c.chunk, q, SCALE)
+    odd = torch.zeros((c.total, 8, D + 1), dtype=torch.bfloat16, device=DEV)[..., 1:]
+    with pytest.raises(pk.PariskvError):
+        pk.paged_attend(c.cfg, pages, c.chunk, odd, SCALE)
+
+
+@pytest.mark.parametrize("kind,status", [("alloc", pk.ENOMEM), ("launch", pk.ECUDA)])
+def test_injected_failures_leave_outputs_alone(monkeypatch, kind, status):
+    c = Case(2, "bf16", [2], [20], heads=2, group=4, page=16)
+    out = torch.full((c.total, 8, D), 5.0, dtype=torch.bfloat16, device=DEV)
+    monkeypatch.setenv("PARISKV_FAULT", kind)
+    with pytest.raises(pk.PariskvError) as e:
+        pk.paged_attend(c.cfg, c.pool(), c.chunk, _bf(c.q), SCALE, out=out)
+    assert e.value.status == status
+    monkeypatch.delenv("PARISKV_FAULT")
+    assert (out == 5.0).all()
+    pk.paged_attend(c.cfg, c.pool(), c.chunk, _bf(c.q), SCALE, out=out)
