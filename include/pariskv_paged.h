@@ -111,13 +111,18 @@ PARISKV_API pariskv_status pariskv_paged_read(const pariskv_config* cfg,
  * rows that attend it infinite or NaN (V: in the elements concerned) and no others. The same
  * call on the same data gives the same bits. The workspace comes from the library's per-device
  * memory pool, stream-ordered on `stream`.
- * Errors: EINVAL, ENOMEM, ECUDA. */
+ * Errors: EINVAL, ENOMEM, ECUDA; ETIMEOUT from pariskv_paged_sync. */
 PARISKV_API pariskv_status pariskv_paged_attend(const pariskv_config* cfg,
                                                 const pariskv_pages* pages,
                                                 const pariskv_chunk* chunk, const void* q,
                                                 int64_t q_ld, float scale, int32_t causal,
                                                 void* out, int32_t out_dtype, float* lse,
                                                 void* stream);
+
+/* Waits for the work on `stream` and reports whether a device-side wait of a paged attention on
+ * the current device has run out since the last report (PARISKV_ETIMEOUT: the outputs of that
+ * call are not complete; never seen while the device works). Not to be captured. */
+PARISKV_API pariskv_status pariskv_paged_sync(void* stream);
 
 #ifdef __cplusplus
 }

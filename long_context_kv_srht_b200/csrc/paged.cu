@@ -3,6 +3,7 @@
 #include <cuda_fp8.h>
 
 #include "paged.cuh"
+#include "pariskv_debug.h"
 
 namespace pkv {
 
@@ -437,6 +438,8 @@ PagePool pool_of(const pariskv_pages* p) {
     return v;
 }
 
+std::atomic<int> g_inject_wait{0};   // pariskv_debug_inject_paged_timeout
+
 Seqs seqs_of(const pariskv_config* cfg, const pariskv_chunk* c) {
     return Seqs{c->page_table, c->kv_len, c->q_start, static_cast<int32_t>(c->total_q),
                 c->table_width, c->table_stride, c->max_q, cfg->batch};
@@ -535,8 +538,9 @@ pariskv_status pariskv_paged_attend(const pariskv_config* cfg, const pariskv_pag
         return fail(PARISKV_EINVAL, "out_dtype %d unknown", out_dtype);
     if (!(scale == scale)) return fail(PARISKV_EINVAL, "scale is NaN");
     const int64_t hq = static_cast<int64_t>(cfg->num_kv_heads) * cfg->group;
-    if (q_ld < hq * D || q_ld % 8)
-        return fail(PARISKV_EINVAL, "q_ld must be >= query heads * 128 and a multiple of 8");
+    if (q_ld < hq * D || q_ld % 8 || q_ld > (int64_t(1) << 38))
+        return fail(PARISKV_EINVAL, "q_ld must be >= query heads * 128, a multiple of 8 and at "
+                    "most 2^38");
     if (chunk->total_q * cfg->group > INT32_MAX)
         return fail(PARISKV_EINVAL, "total_q * group must be below 2^31");
     int dev = 0, sms = 0;
@@ -560,11 +564,15 @@ pariskv_status pariskv_paged_attend(const pariskv_config* cfg, const pariskv_pag
     a.lse = lse;
     a.shape.group = cfg->group;
     a.shape.causal = causal != 0;
-    a.shape.tile_rows = 16;
-    a.shape.block = kFewBlock;
-    const int ctas = few_ctas(sms);
-    // tiles: every sequence may end in a part of one
+    const bool f32 = out_dtype == PARISKV_F32;
+    // up to one tile of the streaming kernel a sequence: it reads each K/V row once
     const int64_t most = static_cast<int64_t>(chunk->max_q) * cfg->group;
+    const bool few = most <= kFewRows;
+    a.shape.tile_rows = few ? kFewRows : chunk_tile_rows(cfg->group, f32);
+    a.shape.block = few ? kFewBlock : kChunkBlock;
+    const int ctas = few ? few_ctas(sms) : sms;
+    a.inject_wait = !few && g_inject_wait.exchange(0);
+    // tiles: every sequence may end in a part of one
     const int64_t tiles = min64(cfg->batch * ceil_div(most, a.shape.tile_rows),
                                 chunk->total_q * cfg->group / a.shape.tile_rows + cfg->batch);
     if (tiles > (1 << 28)) return fail(PARISKV_EINVAL, "too many query rows for one call");
@@ -580,13 +588,28 @@ pariskv_status pariskv_paged_attend(const pariskv_config* cfg, const pariskv_pag
     a.plan.row = reinterpret_cast<int32_t*>(w + parts + pre + ids);
     a.plan.ntiles = reinterpret_cast<int32_t*>(w + parts + pre + 2 * ids);
     a.plan.max_tiles = static_cast<int32_t>(tiles);
-    const bool f32 = out_dtype == PARISKV_F32;
     cudaError_t e = launch_plan(a, st);
-    if (e == cudaSuccess) e = launch_attend_few(a, pages->format, f32, ctas, st);
+    if (e == cudaSuccess)
+        e = few ? launch_attend_few(a, pages->format, f32, ctas, st)
+                : launch_attend_chunk(a, pages->format, f32, ctas, st);
     if (e == cudaSuccess) e = launch_join(a, ctas, f32, st);
     cudaFreeAsync(ws, st);
     if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
     set_last_launches(3);
+    return PARISKV_OK;
+}
+
+pariskv_status pariskv_paged_sync(void* stream) {
+    int status = ST_OK;
+    const cudaError_t e = take_chunk_status(&status, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "paged attention");
+    if (status == ST_TIMEOUT)
+        return fail(PARISKV_ETIMEOUT, "a bounded device-side wait of the paged attention expired");
+    return PARISKV_OK;
+}
+
+pariskv_status pariskv_debug_inject_paged_timeout(void) {
+    g_inject_wait = 1;
     return PARISKV_OK;
 }
 

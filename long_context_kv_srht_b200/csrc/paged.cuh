@@ -144,6 +144,7 @@ struct AttendArgs {
     void* out;
     float* lse;             // or NULL
     float* work;            // parts
+    int32_t inject_wait;    // test hook: a wait of the chunk kernel runs out
 };
 
 // paged.cu
@@ -151,8 +152,15 @@ cudaError_t launch_plan(const AttendArgs& a, cudaStream_t st);
 cudaError_t launch_join(const AttendArgs& a, int ctas, bool f32_out, cudaStream_t st);
 // paged_attend.cu: few rows a sequence (mma.sync, K/V streamed once)
 constexpr int kFewBlock = 64;
+constexpr int kFewRows = 16;    // rows of a tile
 int few_ctas(int sms);
 cudaError_t launch_attend_few(const AttendArgs& a, int format, bool f32_out, int ctas,
                               cudaStream_t st);
+// paged_chunk.cu: many rows a sequence (tcgen05); one CTA an SM
+constexpr int kChunkBlock = 128;
+int chunk_tile_rows(int group, bool f32_out);
+cudaError_t launch_attend_chunk(const AttendArgs& a, int format, bool f32_out, int ctas,
+                                cudaStream_t st);
+cudaError_t take_chunk_status(int* status, cudaStream_t st);   // read and clear
 
 }  // namespace pkv

@@ -1,0 +1,912 @@
+// paged_chunk.cu -- attention of a chunk of new tokens over pages, on the tcgen05 tensor cores:
+//     S = scale Q K^T (masked),  P = exp(S - m),  O += P V,  out = O / sum P.
+//
+// With many query rows a K/V head the call is bound by the two products (4 * 128 flops a pair of
+// row and token) and, right behind them, by the exponentials: 128 x 128 scores take 1024 cycles
+// of products and 1024 of the SM's 16 exponentials a cycle. So the kernel's aim is to keep the
+// tensor cores and the exponential units busy at the same time:
+//  - a tile is 2 x 128 query rows (tokens x heads of one KV head's group) against blocks of 128
+//    tokens, so a K or V block that has come to shared memory serves 256 rows;
+//  - one thread issues all products; S of both halves (2 x 128 columns) and O of both halves (2 x
+//    128 columns) fill the 512 columns of tensor memory; P overwrites S as bf16 and is the second
+//    product's operand from there, so neither S nor P ever touches shared memory;
+//  - two warpgroups do the softmax, one a half, a thread a row (no shuffles): while one half's
+//    rows are in the exponentials the tensor cores work for the other half;
+//  - O is rescaled only when a row's maximum has grown by more than 2^8 since the last time (P is
+//    then at most 2^8, which costs bf16 nothing), so tensor memory is not read back each block;
+//  - K, V and Q tiles come by TMA through a ring of 32 KB stages, one copy a page and 64 columns;
+//    with 8-bit pages they come as bytes, and six warps widen them into the ring, scale and all
+//    (a power of two: the bf16 values are exact);
+//  - blocks in which some token must not reach some row (the causal edge, the end of the cache,
+//    pages that are not there) are marked: their scores are masked, and their V rows are made
+//    finite first, because 0 * NaN is NaN; what was not finite is put back into the rows that see
+//    it at the end;
+//  - blocks without a single page that is there are passed over.
+//
+// fp32 output takes P in three bf16 parts (24 bits, three products); the parts of one half then
+// take the other half's columns, and a tile is 128 rows.
+//
+// Roles, by warp: 0-3 and 4-7 softmax and output of the halves, 8 loads, 9 products, 10 and up
+// repair (bf16) or widening (8-bit). They meet in mbarriers; every wait gives up after
+// kWaitLimitNs, which ends the whole CTA in order and reaches the caller as a status.
+#include "paged.cuh"
+#include "tcgen05.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kBlk = 128;                      // tokens of a block
+constexpr int kHalfB = kBlk * 128;             // 64 columns x 128 rows of bf16: one swizzled tile
+constexpr int kStageB = 2 * kHalfB;            // a K, V or Q tile: 32 KB
+constexpr int kRawB = kBlk * D;                // a tile of codes: 16 KB
+constexpr int kRing = 8;                       // block entries between the loads and the others
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr float kRescale = 8.0f;               // growth of a maximum (base 2) that rescales O
+
+template <bool kE4m3, int kParts> struct Shape {
+    static constexpr int kHalves = kParts == 1 ? 2 : 1;
+    static constexpr int kStages = kE4m3 ? 3 : 4;
+    static constexpr int kRaw = kE4m3 ? 3 : 0;
+    static constexpr int kAuxWarps = kE4m3 ? 6 : 2;
+    static constexpr int kThreads = (10 + kAuxWarps) * 32;
+    // registers: what the softmax threads give and take must stay within the launch's total
+    static constexpr int kSoftRegs = kE4m3 ? 200 : 216, kOtherRegs = kE4m3 ? 56 : 72;
+    static constexpr int kLaunchRegs = kE4m3 ? 128 : 168;
+    static_assert(256 * kSoftRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs,
+                  "register shares");
+    // tensor memory columns
+    static constexpr int kS = 0;                              // + 128 half
+    static constexpr int kP = kParts == 1 ? 0 : 128;          // + 128 half, + 64 part
+    static constexpr int kO = kParts == 1 ? 256 : 320;        // + 128 half
+    // shared memory
+    static constexpr int kQ = 0;
+    static constexpr int kKV = kHalves * kStageB;
+    static constexpr int kRawAt = kKV + kStages * kStageB;
+    static constexpr int kScaleAt = kRawAt + kRaw * kRawB;
+    static constexpr int kSmem = kScaleAt + kRaw * kBlk + 1024;   // + alignment
+};
+
+// kFirst/kLast: of a segment; kEmpty: a segment without a block; kFix: scores are masked; kTwo:
+// both halves have rows; kEnd: no more entries
+enum : int { kFirst = 1, kLast = 2, kEmpty = 4, kFix = 8, kTwo = 16, kEnd = 32 };
+
+// a block on its way from the load warp to the others
+struct Entry {
+    int32_t block, flags;
+    uint32_t mask[4];      // tokens that are there
+};
+// a range of one tile's blocks
+struct Seg {
+    int64_t pos0;          // position of the sequence's first new token
+    int32_t row0, first, nrow, head;
+    int32_t shared;        // last token that every row of the tile may attend
+    int32_t kv;            // tokens of the sequence
+    int32_t whole, part;   // output, or the slot of the unfinished part
+};
+
+struct Shared {
+    uint64_t info_full[kRing], info_empty[kRing], bad_full[kRing];
+    uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], drain;
+    uint64_t kv_full[4], kv_empty[4], fixed[4], raw_full[4], raw_empty[4];
+    Entry entry[kRing];
+    Seg seg[kRing];
+    int32_t bad[kRing][D];   // per segment: first token whose V is not finite in this element
+    int32_t any_bad[kRing];
+    uint32_t tmem;
+    int32_t abort;
+};
+
+__device__ int g_chunk_status;   // ST_TIMEOUT after a wait ran out
+
+__device__ __forceinline__ uint64_t now_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+// Waits for the phase of `parity` to complete; false once a wait of this CTA has run out.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int32_t* abort,
+                                         uint64_t limit = kWaitLimitNs) {
+    const uint32_t b = smem_addr(bar);
+    for (int i = 0; i < 32; ++i)
+        if (mbar_try_wait(b, parity)) return true;
+    const uint64_t t0 = now_ns();
+    while (!mbar_try_wait(b, parity)) {
+        if (*abort) return false;
+        if (now_ns() - t0 > limit) {
+            *abort = 1;
+            atomicExch(&g_chunk_status, ST_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+// the same by a whole warp, which goes on together
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
+                                          volatile int32_t* abort) {
+    return __all_sync(0xffffffffu, wait_for(bar, parity, abort));
+}
+__device__ __forceinline__ void arrive(uint64_t* bar) { mbar_arrive(smem_addr(bar)); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t bf2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// the last token that row r of a tile may attend (-1: none)
+__device__ __forceinline__ int row_limit(const Seg& g, int causal, int group, int r) {
+    if (r >= g.nrow) return -1;
+    const int64_t lim = causal ? g.pos0 + (g.first + r) / group : g.kv - 1;
+    return static_cast<int>(max64(-1, min64(lim, g.kv - 1)));
+}
+
+// ---------------------------------------------------------------------------------- loads
+// The whole warp walks the CTA's blocks; a lane handles one page of a block.
+template <bool kE4m3, int kParts>
+__device__ void load_role(const AttendArgs& a, const CUtensorMap* mq, const CUtensorMap* mk,
+                          const CUtensorMap* mv, Shared& sh, uint8_t* smem, int64_t x, int64_t hi,
+                          int64_t per_head, int nt) {
+    using S = Shape<kE4m3, kParts>;
+    const int lane = threadIdx.x & 31;
+    const int G = a.shape.group, shift = a.pool.shift, causal = a.shape.causal;
+    const int rt = a.shape.tile_rows / S::kHalves;             // rows of a half
+    const int run = min(1 << shift, kBlk), nrun = kBlk / run;  // tokens a copy, copies a block
+    int64_t h = x / per_head;
+    int tile = warp_search(a.plan.pre, nt, x - h * per_head);
+    uint32_t n = 0, seg = 0, ld = 0, nq = 0;   // entries, segments, tiles loaded, Q tiles loaded
+    volatile int32_t* ab = &sh.abort;
+
+    while (x < hi) {
+        const int64_t start = h * per_head + a.plan.pre[tile];
+        const int64_t nb = a.plan.pre[tile + 1] - a.plan.pre[tile];
+        const int b0 = static_cast<int>(x - start), b1 = static_cast<int>(min64(nb, hi - start));
+        const int s = a.plan.seq[tile];
+        const SeqView v = seq_view(a.seqs, shift, s);
+        Seg g;
+        g.first = a.plan.row[tile];
+        g.pos0 = v.pos0;
+        g.row0 = v.row0;
+        g.nrow = static_cast<int>(min64(a.shape.tile_rows,
+                                        static_cast<int64_t>(v.rows) * G - g.first));
+        g.head = static_cast<int>(h);
+        g.kv = v.kv;
+        g.whole = b0 == 0 && b1 == nb;
+        g.part = 2 * static_cast<int>(blockIdx.x) + (b0 == 0);
+        g.shared = row_limit(g, causal, G, 0);
+        const int end = tile_end(v, a.shape, g.first);
+        const int32_t* table = a.seqs.table + static_cast<int64_t>(s) * a.seqs.stride;
+
+        // page ids come 32 at a time, a lane a run, one window ahead
+        const int per_win = 32 / nrun;                  // blocks of a window
+        int win = b0, id = -1, id_next = -1;
+        auto fetch = [&](int w) -> int {
+            const int64_t tok = static_cast<int64_t>(w) * kBlk + lane * run;
+            return w + lane / nrun < b1 && tok < end ? table[tok >> shift] : -1;
+        };
+        id = fetch(win);
+        id_next = fetch(win + per_win);
+        // the next block with a page that is there, from b on; *ids: this lane's page of it
+        auto live = [&](int b, uint32_t* valid, int* page) -> int {
+            for (; b < b1; ++b) {
+                if (b >= win + per_win) {
+                    win += per_win;
+                    id = id_next;
+                    id_next = fetch(win + per_win);
+                }
+                const uint32_t ok = __ballot_sync(
+                    0xffffffffu, static_cast<uint32_t>(id) < static_cast<uint32_t>(a.pool.num_pages));
+                const int at = (b - win) * nrun;
+                *valid = (ok >> at) & (nrun == 32 ? ~0u : (1u << nrun) - 1);
+                *page = __shfl_sync(0xffffffffu, id, (at + lane) & 31);
+                if (*valid) return b;
+            }
+            return -1;
+        };
+        uint32_t valid = 0;
+        int page = 0;
+        int b = live(b0, &valid, &page);
+        bool first = true;
+        while (first || b >= 0) {
+            const uint32_t cur_valid = valid;
+            const int cur_page = page, cur = b;
+            if (b >= 0) b = live(b + 1, &valid, &page);
+            // the entry
+            const int slot = n % kRing;
+            if (!warp_wait(&sh.info_empty[slot], ((n / kRing) & 1) ^ 1, ab)) return;
+            Entry e;
+            e.block = cur;
+            e.flags = (first ? kFirst : 0) | (b < 0 ? kLast : 0) | (cur < 0 ? kEmpty : 0) |
+                      (S::kHalves == 2 && g.nrow > rt ? kTwo : 0);
+            bool full = cur >= 0;
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                const uint32_t l = cur_valid >> (32 * f / run) & 1,
+                               u = cur_valid >> ((32 * f + 16) / run) & 1;
+                const int left = end - (cur * kBlk + 32 * f);
+                e.mask[f] = cur < 0 || left <= 0
+                                ? 0u
+                                : ((l ? 0xffffu : 0u) | (u ? 0xffff0000u : 0u)) &
+                                      (left >= 32 ? ~0u : (1u << left) - 1);
+                full = full && e.mask[f] == ~0u;
+            }
+            const int last_tok = min(end, (cur + 1) * kBlk) - 1;
+            if (!full || (causal && last_tok > g.shared)) e.flags |= kFix;
+            if (first)
+                for (int i = lane; i < D; i += 32) sh.bad[seg % kRing][i] = INT32_MAX;
+            __syncwarp();
+            if (lane == 0) {
+                if (first) {
+                    sh.seg[seg % kRing] = g;
+                    sh.any_bad[seg % kRing] = 0;
+                }
+                sh.entry[slot] = e;
+                arrive(&sh.info_full[slot]);
+            }
+            ++n;
+            if (cur < 0) break;
+            if (first) {
+                if (!warp_wait(&sh.q_empty, (nq & 1) ^ 1, ab)) return;
+                if (lane == 0) {
+                    const int halves = e.flags & kTwo ? 2 : 1;
+                    mbar_arrive_expect_tx(smem_addr(&sh.q_full), halves * 2 * rt * 128);
+                    for (int i = 0; i < halves; ++i)
+                        for (int c = 0; c < 2; ++c)
+                            tma_load3(smem_addr(smem + S::kQ + i * kStageB + c * kHalfB), mq, 64 * c,
+                                      g.head * G, g.row0 + (g.first + i * rt) / G,
+                                      smem_addr(&sh.q_full));
+                }
+                ++nq;
+            }
+            first = false;
+            // K, then V
+            const bool mine = lane < nrun && (cur_valid >> lane & 1);
+            const int row = (g.head << shift) + ((cur * kBlk + lane * run) & ((1 << shift) - 1));
+            for (int t = 0; t < 2; ++t) {
+                constexpr int kSlots = kE4m3 ? S::kRaw : S::kStages;
+                const int st = ld % kSlots;
+                uint64_t* full_bar = kE4m3 ? &sh.raw_full[st] : &sh.kv_full[st];
+                if (!warp_wait(kE4m3 ? &sh.raw_empty[st] : &sh.kv_empty[st],
+                              ((ld / kSlots) & 1) ^ 1, ab))
+                    return;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(smem_addr(full_bar),
+                                          __popc(cur_valid) * run * (kE4m3 ? D + 1 : 2 * D));
+                __syncwarp();
+                if (mine) {
+                    const CUtensorMap* m = t ? mv : mk;
+                    if (kE4m3) {
+                        tma_load3(smem_addr(smem + S::kRawAt + st * kRawB + lane * run * D), m, 0,
+                                  row, cur_page, smem_addr(full_bar));
+                        bulk_g2s(smem_addr(smem + S::kScaleAt + st * kBlk + lane * run),
+                                 (t ? a.pool.vs : a.pool.ks) + cur_page * a.pool.scale_stride + row,
+                                 run, smem_addr(full_bar));
+                    } else {
+                        uint8_t* dst = smem + S::kKV + st * kStageB + lane * run * 128;
+                        tma_load3(smem_addr(dst), m, 0, row, cur_page, smem_addr(full_bar));
+                        tma_load3(smem_addr(dst + kHalfB), m, 64, row, cur_page, smem_addr(full_bar));
+                    }
+                }
+                ++ld;
+            }
+        }
+        ++seg;
+        x = start + b1;
+        if (b1 == nb && ++tile == nt) {
+            tile = 0;
+            ++h;
+        }
+    }
+    // the end: an entry without a segment
+    const int slot = n % kRing;
+    if (!warp_wait(&sh.info_empty[slot], ((n / kRing) & 1) ^ 1, ab)) return;
+    if (lane == 0) {
+        sh.entry[slot].flags = kEnd;
+        sh.entry[slot].block = -1;
+        arrive(&sh.info_full[slot]);
+    }
+}
+
+// ------------------------------------------------------------------------------- products
+template <bool kE4m3, int kParts>
+__device__ void mma_role(Shared& sh, uint8_t* smem, uint32_t tmem, bool inject) {
+    using S = Shape<kE4m3, kParts>;
+    constexpr uint32_t kQK = mma_desc(kBlk, false), kPV = mma_desc(D, true);
+    volatile int32_t* ab = &sh.abort;
+    uint32_t n = 0, use = 0, nq = 0, np[2] = {0, 0}, fix = 0;   // use: tiles of the ring consumed
+    int cur = 0, nxt = 0;
+    constexpr int kSome = 64;   // a block's flags are never 0
+    // flags of the next block with work, 0 at the end, -1 after a wait ran out
+    auto fetch = [&]() -> int {
+        while (true) {
+            const int slot = n % kRing;
+            if (!wait_for(&sh.info_full[slot], (n / kRing) & 1, ab)) return -1;
+            const int f = sh.entry[slot].flags, b = sh.entry[slot].block;
+            arrive(&sh.info_empty[slot]);
+            ++n;
+            if (b >= 0) return f | kSome;
+            if (f & kEnd) return 0;
+        }
+    };
+    // S of a half from Q and the K tile in stage st
+    auto qk = [&](int i, int st) {
+        const uint32_t q = smem_addr(smem + S::kQ + i * kStageB);
+        const uint32_t k = smem_addr(smem + S::kKV + st * kStageB);
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+            const uint32_t at = (j >> 2) * kHalfB + (j & 3) * 32;
+            mma_ss(tmem + S::kS + 128 * i, smem_desc(q + at, 16), smem_desc(k + at, 16), kQK, j > 0);
+        }
+        mma_commit(smem_addr(&sh.s_full[i]));
+    };
+    auto pv = [&](int i, int st, bool accumulate) {
+        const uint32_t v = smem_addr(smem + S::kKV + st * kStageB);
+#pragma unroll
+        for (int p = 0; p < kParts; ++p)
+#pragma unroll
+            for (int j = 0; j < kBlk / 16; ++j)
+                mma_ts(tmem + S::kO + 128 * i, tmem + S::kP + 128 * i + 64 * p + 8 * j,
+                       smem_desc(v + j * 16 * 128, kHalfB), kPV, accumulate || p > 0 || j > 0);
+        mma_commit(smem_addr(&sh.pv_done[i]));
+    };
+    auto k_ready = [&](int flags) -> bool {   // Q of a new tile, and the K tile `use`
+        if ((flags & kFirst) && !wait_for(&sh.q_full, nq++ & 1, ab)) return false;
+        return wait_for(&sh.kv_full[use % S::kStages], (use / S::kStages) & 1, ab);
+    };
+
+    if (inject) {   // test hook: a wait for an arrival that never comes
+        wait_for(&sh.raw_full[3], 0, ab, 1000000ull);
+        return;
+    }
+    cur = fetch();
+    if (cur <= 0) return;
+    if (!k_ready(cur)) return;
+    tc_fence_after();
+    for (int i = 0; i < (cur & kTwo ? 2 : 1); ++i) qk(i, use % S::kStages);
+    mma_commit(smem_addr(&sh.kv_empty[use % S::kStages]));
+    if (cur & kLast) mma_commit(smem_addr(&sh.q_empty));
+    ++use;
+    while (cur > 0) {
+        const int sv = use % S::kStages;
+        const uint32_t pv_parity = (use / S::kStages) & 1;
+        ++use;
+        nxt = fetch();
+        if (nxt < 0) return;
+        const int hc = cur & kTwo ? 2 : 1, hn = nxt == 0 ? 0 : nxt & kTwo ? 2 : 1;
+        for (int i = 0; i < max(hc, hn); ++i) {
+            if (i < hc) {
+                if (i == 0) {
+                    if (!wait_for(&sh.kv_full[sv], pv_parity, ab)) return;
+                    if (!kE4m3 && (cur & kFix)) {
+                        if (!wait_for(&sh.fixed[sv], fix >> sv & 1, ab)) return;
+                        fix ^= 1u << sv;
+                    }
+                }
+                if (!wait_for(&sh.p_full[i], np[i]++ & 1, ab)) return;
+                tc_fence_after();
+                pv(i, sv, !(cur & kFirst));
+                if (i == hc - 1) mma_commit(smem_addr(&sh.kv_empty[sv]));
+            }
+            if (i < hn) {
+                if (i == 0 && !k_ready(nxt)) return;
+                // the new scores go where the half's last weights are read
+                if (np[i] > 0 && !wait_for(&sh.pv_done[i], (np[i] - 1) & 1, ab)) return;
+                tc_fence_after();
+                qk(i, use % S::kStages);
+                if (i == hn - 1) {
+                    mma_commit(smem_addr(&sh.kv_empty[use % S::kStages]));
+                    if (nxt & kLast) mma_commit(smem_addr(&sh.q_empty));
+                }
+            }
+        }
+        if (nxt > 0) ++use;
+        cur = nxt;
+    }
+}
+
+// ----------------------------------------------------------------- softmax and the output
+template <bool kE4m3, int kParts, typename Out>
+__device__ void softmax_role(const AttendArgs& a, Shared& sh, uint32_t tmem, int half) {
+    using S = Shape<kE4m3, kParts>;
+    const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+    const int G = a.shape.group, R = a.shape.tile_rows, rt = R / S::kHalves;
+    const int rl = 32 * warp + lane;                            // row of the half
+    const int r = rl < rt ? half * rt + rl : INT32_MAX;         // row of the tile
+    const uint32_t ts = tmem + (warp << 21) + S::kS + 128 * half;
+    const uint32_t tp = tmem + (warp << 21) + S::kP + 128 * half;
+    const uint32_t to = tmem + (warp << 21) + S::kO + 128 * half;
+    volatile int32_t* ab = &sh.abort;
+    // scores times a positive factor c, after a sign (negative scales) or zero (scale 0)
+    const float c = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * kLog2e;
+    const float sign = a.scale > 0.0f ? 1.0f : a.scale < 0.0f ? -1.0f : 0.0f;
+
+    uint32_t n = 0, seg = 0, ns = 0;    // entries, segments, blocks of this half
+    float m = -INFINITY, l = 0.0f;      // the row's maximum (times c) as last used, and its sum
+    int lim = -1;
+    while (true) {
+        const int slot = n % kRing;
+        if (!warp_wait(&sh.info_full[slot], (n / kRing) & 1, ab)) return;
+        const int flags = sh.entry[slot].flags, block = sh.entry[slot].block;
+        if (flags & kEnd) return;
+        const Seg& g = sh.seg[seg % kRing];
+        if (flags & kFirst) {
+            lim = row_limit(g, a.shape.causal, G, r);
+            m = -INFINITY;
+            l = 0.0f;
+        }
+        const bool mine = half == 0 || (flags & kTwo);
+        if (mine && !(flags & kEmpty)) {
+            if (!warp_wait(&sh.s_full[half], ns & 1, ab)) return;
+            tc_fence_after();
+            uint32_t s[128];
+            tmem_ld32(ts, s);
+            tmem_ld32(ts + 32, s + 32);
+            tmem_ld32(ts + 64, s + 64);
+            tmem_ld32(ts + 96, s + 96);
+            tmem_wait_ld();
+            if (sign != 1.0f) {
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    s[i] = __float_as_uint(__uint_as_float(s[i]) * sign);
+            }
+            if (flags & kFix) {
+                const int left = lim - block * kBlk + 1;   // tokens up to the row's limit
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const int k = left - 32 * f;
+                    const uint32_t w = k <= 0 ? 0u
+                                              : sh.entry[slot].mask[f] &
+                                                    (k >= 32 ? ~0u : (1u << k) - 1);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (!(w >> i & 1)) s[32 * f + i] = 0xff800000u;
+                }
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 128; i += 8)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(s[i + 2 * k]),
+                                               __uint_as_float(s[i + 2 * k + 1])));
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+            const bool first = flags & kFirst;
+            bool waited = false;
+            if (first) {
+                m = top;
+            } else if (__any_sync(0xffffffffu, top > m + kRescale)) {
+                const float m1 = top > m + kRescale ? top : m;
+                const float f = m1 == -INFINITY ? 1.0f : ex2(m - m1);
+                m = m1;
+                l *= f;
+                // the last product into O has to be there before it is rescaled
+                if (!warp_wait(&sh.pv_done[half], (ns - 1) & 1, ab)) return;
+                waited = true;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t o[32];
+                    tmem_ld32(to + 32 * i, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                    tmem_st32(to + 32 * i, o);
+                }
+            }
+            if (kParts > 1 && ns > 0 && !waited) {
+                // the weights' columns are free once the last product has read them
+                if (!warp_wait(&sh.pv_done[half], (ns - 1) & 1, ab)) return;
+                tc_fence_after();
+            }
+            const float ms = m == -INFINITY ? 0.0f : m;
+            const uint64_t c2 = pack2(c, c), m2 = pack2(-ms, -ms);
+            uint64_t sum[2] = {0, 0};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float p[32];
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    const float2 y = unpack2(fma2(pack2u(s[32 * q + i], s[32 * q + i + 1]), c2, m2));
+                    p[i] = ex2(y.x);
+                    p[i + 1] = ex2(y.y);
+                    sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(p[i], p[i + 1]));
+                }
+#pragma unroll
+                for (int k = 0; k < kParts; ++k) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        w[i] = bf2(p[2 * i], p[2 * i + 1]);
+                        if (k + 1 < kParts) {
+                            p[2 * i] -= lo_f(w[i]);
+                            p[2 * i + 1] -= hi_f(w[i]);
+                        }
+                    }
+                    tmem_st16(tp + 64 * k + 16 * q, w);
+                }
+            }
+            const float2 y = unpack2(add2(sum[0], sum[1]));
+            l += y.x + y.y;
+            tmem_wait_st();
+            tc_fence_before();
+            arrive(&sh.p_full[half]);
+            ++ns;
+        }
+        if (flags & kLast) {
+            if (mine) {
+                const bool empty = flags & kEmpty;
+                if (!empty) {
+                    if (!warp_wait(&sh.pv_done[half], (ns - 1) & 1, ab)) return;
+                    tc_fence_after();
+                }
+                if (!warp_wait(&sh.bad_full[seg % kRing], (seg / kRing) & 1, ab)) return;
+                const bool bad = sh.any_bad[seg % kRing] != 0;
+                const bool live = r < g.nrow;
+                const float inv = !g.whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+                const int rr = g.first + (live ? r : 0);
+                const int64_t at = (g.row0 + rr / G) * (static_cast<int64_t>(a.heads) * G) +
+                                   g.head * G + rr % G;
+                float* part = a.work + g.part * part_floats(R);
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t o[32];
+                    if (!empty) {
+                        tmem_ld32(to + 32 * q, o);
+                        tmem_wait_ld();
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float y = empty ? 0.0f : __uint_as_float(o[i]) * inv;
+                        o[i] = __float_as_uint(y);
+                    }
+                    if (bad) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (sh.bad[seg % kRing][32 * q + i] <= lim) o[i] = 0x7fc00000u;
+                    }
+                    if (live && g.whole && sizeof(Out) == 2) {
+                        uint4* dst = reinterpret_cast<uint4*>(
+                            static_cast<__nv_bfloat16*>(a.out) + at * D + 32 * q);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t* w = o + 8 * i;
+                            dst[i] = make_uint4(
+                                bf2(__uint_as_float(w[0]), __uint_as_float(w[1])),
+                                bf2(__uint_as_float(w[2]), __uint_as_float(w[3])),
+                                bf2(__uint_as_float(w[4]), __uint_as_float(w[5])),
+                                bf2(__uint_as_float(w[6]), __uint_as_float(w[7])));
+                        }
+                    } else if (live) {
+                        uint4* dst = reinterpret_cast<uint4*>(
+                            g.whole ? static_cast<float*>(a.out) + at * D + 32 * q
+                                    : part + static_cast<size_t>(r) * D + 32 * q);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (live && g.whole && a.lse)
+                    a.lse[at] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+                if (live && !g.whole) {
+                    part[static_cast<size_t>(R) * D + r] = m;
+                    part[static_cast<size_t>(R) * D + R + r] = l;
+                }
+                tc_fence_before();
+            }
+            ++seg;
+        }
+        __syncwarp();
+        if (lane == 0) arrive(&sh.info_empty[slot]);
+        ++n;
+    }
+}
+
+// ---------------------------------------------------------------- repair, and widening
+template <bool kE4m3, int kParts>
+__device__ void aux_role(const AttendArgs& a, Shared& sh, uint8_t* smem) {
+    using S = Shape<kE4m3, kParts>;
+    constexpr int kT = S::kAuxWarps * 32;
+    const int tid = threadIdx.x - 320, lane = tid & 31;
+    volatile int32_t* ab = &sh.abort;
+    uint32_t n = 0, seg = 0, use = 0;   // use: tiles of the ring seen
+    while (true) {
+        const int slot = n % kRing;
+        if (!warp_wait(&sh.info_full[slot], (n / kRing) & 1, ab)) return;
+        const int flags = sh.entry[slot].flags, block = sh.entry[slot].block;
+        if (flags & kEnd) return;
+        const int sg = seg % kRing;
+        const int shared = sh.seg[sg].shared;
+        auto mark = [&](int d, int tok) {
+            atomicMin(&sh.bad[sg][d], tok);
+            sh.any_bad[sg] = 1;
+        };
+        if (!(flags & kEmpty)) {
+            if constexpr (kE4m3) {
+                for (int t = 0; t < 2; ++t) {
+                    const int raw = use % S::kRaw, st = use % S::kStages;
+                    if (!warp_wait(&sh.raw_full[raw], (use / S::kRaw) & 1, ab)) return;
+                    if (!warp_wait(&sh.kv_empty[st], ((use / S::kStages) & 1) ^ 1, ab)) return;
+                    const uint8_t* src = smem + S::kRawAt + raw * kRawB;
+                    const uint8_t* sc = smem + S::kScaleAt + raw * kBlk;
+                    uint8_t* dst = smem + S::kKV + st * kStageB;
+                    const bool fix = flags & kFix;
+#pragma unroll 2
+                    for (int i = tid; i < kBlk * 16; i += kT) {
+                        const int row = i >> 4, j = i & 15, tok = block * kBlk + row;
+                        const uint2 w = *reinterpret_cast<const uint2*>(src + row * D + j * 8);
+                        const int byte = sc[row];
+                        // code * 2^(byte - 127): the bf16 patterns are 2^-120 too small; the
+                        // factor 2^(byte - 7) takes two steps where it is above 2^127
+                        uint32_t f = static_cast<uint32_t>(min(byte + 120, 254)) << 7;
+                        if (byte == kNanRow) f = 0x7fc0u;
+                        bool zero = false;
+                        if (fix) {
+                            zero = !(sh.entry[slot].mask[row >> 5] >> (row & 31) & 1);
+                            if (t == 1 && !zero && byte == kNanRow && tok > shared) {
+                                for (int k = 0; k < 8; ++k) mark(8 * j + k, tok);
+                                zero = true;
+                            }
+                        }
+                        const uint32_t ff = f | f << 16;
+                        uint32_t y[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t x = k & 1 ? prmt_i<0x3424>(k < 2 ? w.x : w.y, 0)
+                                                     : prmt_i<0x1404>(k < 2 ? w.x : w.y, 0);
+                            y[k] = mul_bf2((x & 0x80008000u) | ((x >> 4) & 0x07f007f0u), ff);
+                        }
+                        if (byte > 134 && byte != kNanRow) {
+                            const uint32_t f2 = static_cast<uint32_t>(byte - 134 + 127) << 7;
+                            for (int k = 0; k < 4; ++k) y[k] = mul_bf2(y[k], f2 | f2 << 16);
+                        }
+                        if (zero) y[0] = y[1] = y[2] = y[3] = 0;
+                        *reinterpret_cast<uint4*>(dst + (j >> 3) * kHalfB + row * 128 +
+                                                  (((j & 7) ^ (row & 7)) << 4)) =
+                            make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        arrive(&sh.kv_full[st]);
+                        arrive(&sh.raw_empty[raw]);
+                    }
+                    ++use;
+                }
+            } else {
+                const int st = (use + 1) % S::kStages;
+                if (flags & kFix) {
+                    if (!warp_wait(&sh.kv_full[st], ((use + 1) / S::kStages) & 1, ab)) return;
+                    for (int row = tid; row < kBlk; row += kT) {
+                        const int tok = block * kBlk + row;
+                        const bool there = sh.entry[slot].mask[row >> 5] >> (row & 31) & 1;
+                        if (there && tok <= shared) continue;
+                        for (int i = 0; i < 16; ++i) {
+                            const int ch = (i + row) & 7;     // piece as stored
+                            uint4* p = reinterpret_cast<uint4*>(
+                                smem + S::kKV + st * kStageB + (i >> 3) * kHalfB + row * 128 +
+                                (ch << 4));
+                            if (!there) {
+                                *p = make_uint4(0, 0, 0, 0);
+                                continue;
+                            }
+                            const uint4 v = *p;
+                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            bool odd = false;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                odd = odd || (w[k] & 0x7f80u) == 0x7f80u ||
+                                      (w[k] & 0x7f800000u) == 0x7f800000u;
+                            if (!odd) continue;
+                            const int d = (i >> 3) * 64 + (ch ^ (row & 7)) * 8;
+                            for (int k = 0; k < 4; ++k) {
+                                if ((w[k] & 0x7f80u) == 0x7f80u) {
+                                    mark(d + 2 * k, tok);
+                                    w[k] &= 0xffff0000u;
+                                }
+                                if ((w[k] & 0x7f800000u) == 0x7f800000u) {
+                                    mark(d + 2 * k + 1, tok);
+                                    w[k] &= 0xffffu;
+                                }
+                            }
+                            *p = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive(&sh.fixed[st]);
+                }
+                use += 2;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) {
+            if (flags & kLast) arrive(&sh.bad_full[sg]);
+            arrive(&sh.info_empty[slot]);
+        }
+        if (flags & kLast) ++seg;
+        ++n;
+    }
+}
+
+template <bool kE4m3, int kParts, typename Out>
+__global__ void __launch_bounds__(Shape<kE4m3, kParts>::kThreads, 1)
+attend_chunk_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap mq,
+                    const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    using S = Shape<kE4m3, kParts>;
+    extern __shared__ uint8_t raw_smem[];
+    __shared__ __align__(16) Shared sh;
+    uint8_t* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
+    const int warp = threadIdx.x >> 5;
+    const int nt = *a.plan.ntiles;
+    const int64_t per_head = a.plan.pre[nt], total = per_head * a.heads;
+    if (total == 0) return;
+    const int64_t x = cut(total, gridDim.x, blockIdx.x), hi = cut(total, gridDim.x, blockIdx.x + 1);
+    if (x >= hi) return;
+
+    if (threadIdx.x == 0) {
+        sh.abort = 0;
+        auto init = [&](uint64_t* b, uint32_t count) { mbar_init(smem_addr(b), count); };
+        for (int i = 0; i < kRing; ++i) {
+            init(&sh.info_full[i], 1);
+            init(&sh.info_empty[i], 4 * S::kHalves + 1 + S::kAuxWarps);
+            init(&sh.bad_full[i], S::kAuxWarps);
+        }
+        init(&sh.q_full, 1);
+        init(&sh.q_empty, 1);
+        init(&sh.drain, 1);
+        for (int i = 0; i < 2; ++i) {
+            init(&sh.s_full[i], 1);
+            init(&sh.p_full[i], 128);
+            init(&sh.pv_done[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            init(&sh.kv_full[i], kE4m3 ? S::kAuxWarps : 1);
+            init(&sh.kv_empty[i], 1);
+            init(&sh.fixed[i], S::kAuxWarps);
+            init(&sh.raw_full[i], 1);
+            init(&sh.raw_empty[i], S::kAuxWarps);
+        }
+        mbar_fence_init();
+        tma_prefetch_map(&mq);
+        tma_prefetch_map(&mk);
+        tma_prefetch_map(&mv);
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_addr(&sh.tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
+
+    if (warp < 8) {
+        regs_up<S::kSoftRegs>();
+        if (warp < 4 * S::kHalves) softmax_role<kE4m3, kParts, Out>(a, sh, tmem, warp >> 2);
+    } else {
+        regs_down<S::kOtherRegs>();
+        if (warp == 8) {
+            load_role<kE4m3, kParts>(a, &mq, &mk, &mv, sh, smem, x, hi, per_head, nt);
+        } else if (warp == 9) {
+            if ((threadIdx.x & 31) == 0) {
+                mma_role<kE4m3, kParts>(sh, smem, tmem, a.inject_wait);
+                // nothing may be under way in tensor memory when it is given back
+                mma_commit(smem_addr(&sh.drain));
+                int32_t no = 0;
+                wait_for(&sh.drain, 0, &no);
+            }
+            __syncwarp();
+        } else {
+            aux_role<kE4m3, kParts>(a, sh, smem);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (sh.abort && warp == 8 && (threadIdx.x & 31) == 0) {
+        // copies that were under way when a wait ran out write into this CTA's memory: give them
+        // the time that any of them takes before the CTA ends
+        const uint64_t t0 = now_ns();
+        while (now_ns() - t0 < 10000000ull) {}
+    }
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <bool kE4m3, int kParts, typename Out>
+cudaError_t launch_chunk(const AttendArgs& a, const CUtensorMap maps[3], int ctas, cudaStream_t st) {
+    using S = Shape<kE4m3, kParts>;
+    static std::atomic<uint64_t> done{0};
+    auto kernel = attend_chunk_kernel<kE4m3, kParts, Out>;
+    const cudaError_t e = raise_smem_limit(kernel, S::kSmem, done);
+    if (e != cudaSuccess) return e;
+    kernel<<<ctas, S::kThreads, S::kSmem, st>>>(a, maps[0], maps[1], maps[2]);
+    return cudaGetLastError();
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// a 3-d tensor of rows of 128 elements; boxes of `cols` x r1 x r2
+bool encode(CUtensorMap* m, const void* base, bool bytes, uint64_t n1, uint64_t n2, uint64_t s1,
+            uint64_t s2, uint32_t cols, uint32_t r1, uint32_t r2) {
+    const EncodeTiled fn = encode_tiled();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), n1, n2}, strides[2] = {s1, s2};
+    const cuuint32_t box[3] = {cols, r1, r2}, step[3] = {1, 1, 1};
+    return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+              const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+int chunk_tile_rows(int group, bool f32_out) { return (f32_out ? 1 : 2) * (128 / group) * group; }
+
+cudaError_t launch_attend_chunk(const AttendArgs& a, int format, bool f32_out, int ctas,
+                                cudaStream_t st) {
+    const bool e4 = format == PARISKV_PAGES_E4M3;
+    const int G = a.shape.group;
+    const uint64_t rows = static_cast<uint64_t>(a.heads) << a.pool.shift;
+    const uint32_t run = min(1 << a.pool.shift, kBlk);
+    const uint64_t el = e4 ? 1 : 2;
+    CUtensorMap maps[3];
+    if (!encode(&maps[0], a.q, false, static_cast<uint64_t>(a.heads) * G, a.seqs.total_q, 2 * D,
+                a.q_ld * 2, 64, G, 128 / G))
+        return cudaErrorInvalidValue;
+    for (int t = 0; t < 2; ++t)
+        if (!encode(&maps[1 + t], t ? a.pool.v : a.pool.k, e4, rows, a.pool.num_pages, el * D,
+                    a.pool.page_bytes, e4 ? D : 64, run, 1))
+            return cudaErrorInvalidValue;
+    if (e4)
+        return f32_out ? launch_chunk<true, 3, float>(a, maps, ctas, st)
+                       : launch_chunk<true, 1, __nv_bfloat16>(a, maps, ctas, st);
+    return f32_out ? launch_chunk<false, 3, float>(a, maps, ctas, st)
+                   : launch_chunk<false, 1, __nv_bfloat16>(a, maps, ctas, st);
+}
+
+// The status word of the current device, read and cleared after `st`'s work is done.
+cudaError_t take_chunk_status(int* status, cudaStream_t st) {
+    cudaError_t e = cudaMemcpyFromSymbolAsync(status, g_chunk_status, sizeof(int), 0,
+                                              cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e != cudaSuccess || *status == ST_OK) return e;
+    const int ok = ST_OK;
+    e = cudaMemcpyToSymbolAsync(g_chunk_status, &ok, sizeof(int), 0, cudaMemcpyHostToDevice, st);
+    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
+}
+
+}  // namespace pkv

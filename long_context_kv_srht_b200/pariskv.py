@@ -134,6 +134,8 @@ _SIGS = {
     "pariskv_paged_attend": (_S, [ctypes.POINTER(Config), ctypes.POINTER(_Pages),
                                   ctypes.POINTER(_Chunk), _P, _I64, ctypes.c_float, _I32, _P,
                                   _I32, _P, _P]),
+    "pariskv_paged_sync": (_S, [_P]),
+    "pariskv_debug_inject_paged_timeout": (_S, []),
 }
 
 STAGES = ("query_prep", "vote", "threshold", "compact", "rerank", "topk")
@@ -692,3 +694,14 @@ def paged_attend(cfg: Config, pages: Pages, chunk: Chunk, q, scale: float, causa
                                     lse.data_ptr() if lse is not None else None,
                                     _stream(stream)), where)
     return out, lse
+
+
+def paged_sync(stream=None) -> None:
+    """pariskv_paged_sync: waits for the stream; raises (ETIMEOUT) if a device-side wait of a
+    paged attention on the current device ran out since the last call."""
+    _check(lib.pariskv_paged_sync(_stream(stream)), "pariskv_paged_sync")
+
+
+def inject_paged_timeout() -> None:
+    """pariskv_debug_inject_paged_timeout (test hook, consumed by the next chunk attention)."""
+    _check(lib.pariskv_debug_inject_paged_timeout(), "pariskv_debug_inject_paged_timeout")

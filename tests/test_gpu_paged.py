@@ -401,3 +401,17 @@ def test_injected_failures_leave_outputs_alone(monkeypatch, kind, status):
     monkeypatch.delenv("PARISKV_FAULT")
     assert (out == 5.0).all()
     pk.paged_attend(c.cfg, c.pool(), c.chunk, _bf(c.q), SCALE, out=out)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_a_wait_that_runs_out_reaches_the_caller(fmt):
+    c = Case(8, fmt, [200], [300], heads=2, group=4, page=16)
+    pk.paged_sync()
+    pk.inject_paged_timeout()
+    _attend(c)
+    with pytest.raises(pk.PariskvError) as e:
+        pk.paged_sync()
+    assert e.value.status == pk.ETIMEOUT
+    out, lse = _attend(c)                  # reported once; the next call is whole again
+    pk.paged_sync()
+    c.check(out, lse, True)
