@@ -7,7 +7,7 @@
 // tensor cores and the exponential units busy at the same time:
 //  - a tile is 2 x 128 query rows (tokens x heads of one KV head's group) against blocks of 128
 //    tokens, so a K or V block that has come to shared memory serves 256 rows;
-//  - one thread issues all products; S of both halves (2 x 128 columns) and O of both halves (2 x
+//  - one thread a half issues its products; S of both halves (2 x 128 columns) and O of both halves (2 x
 //    128 columns) fill the 512 columns of tensor memory; P overwrites S as bf16 and is the second
 //    product's operand from there, so neither S nor P ever touches shared memory;
 //  - two warpgroups do the softmax, one a half, a thread a row (no shuffles): while one half's
@@ -15,7 +15,7 @@
 //  - O is rescaled only when a row's maximum has grown by more than 2^8 since the last time (P is
 //    then at most 2^8, which costs bf16 nothing), so tensor memory is not read back each block;
 //  - K, V and Q tiles come by TMA through a ring of 32 KB stages, one copy a page and 64 columns;
-//    with 8-bit pages they come as bytes, and six warps widen them into the ring, scale and all
+//    with 8-bit pages they come as bytes, and five warps widen them into the ring, scale and all
 //    (a power of two: the bf16 values are exact);
 //  - blocks in which some token must not reach some row (the causal edge, the end of the cache,
 //    pages that are not there) are marked: their scores are masked, and their V rows are made
@@ -26,8 +26,8 @@
 // fp32 output takes P in three bf16 parts (24 bits, three products); the parts of one half then
 // take the other half's columns, and a tile is 128 rows.
 //
-// Roles, by warp: 0-3 and 4-7 softmax and output of the halves, 8 loads, 9 products, 10 and up
-// repair (bf16) or widening (8-bit). They meet in mbarriers; every wait gives up after
+// Roles, by warp: 0-3 and 4-7 softmax and output of the halves, 8 loads, 9 and 10 the halves'
+// products, 11 and up repair (bf16) or widening (8-bit). They meet in mbarriers; every wait gives up after
 // kWaitLimitNs, which ends the whole CTA in order and reaches the caller as a status.
 #include "paged.cuh"
 #include "tcgen05.cuh"
@@ -37,27 +37,26 @@ namespace pkv {
 namespace {
 
 constexpr int kBlk = 128;                      // tokens of a block
+constexpr int kTurn = 64;                      // tokens whose scores are worked on at a time
+constexpr int kPoly = 0;                       // of 16 exponentials, those on the FMA units
 constexpr int kHalfB = kBlk * 128;             // 64 columns x 128 rows of bf16: one swizzled tile
 constexpr int kStageB = 2 * kHalfB;            // a K, V or Q tile: 32 KB
 constexpr int kRawB = kBlk * D;                // a tile of codes: 16 KB
 constexpr int kRing = 8;                       // block entries between the loads and the others
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint32_t kNapNs = 20000;
 constexpr float kRescale = 8.0f;               // growth of a maximum (base 2) that rescales O
 
 template <bool kE4m3, int kParts> struct Shape {
     static constexpr int kHalves = kParts == 1 ? 2 : 1;
     static constexpr int kStages = kE4m3 ? 3 : 4;
     static constexpr int kRaw = kE4m3 ? 3 : 0;
-    static constexpr int kAuxWarps = kE4m3 ? 6 : 2;
-    static constexpr int kThreads = (10 + kAuxWarps) * 32;
-    // registers: what the softmax threads give and take must stay within the launch's total
-    static constexpr int kSoftRegs = kE4m3 ? 200 : 216, kOtherRegs = kE4m3 ? 56 : 72;
-    static constexpr int kLaunchRegs = kE4m3 ? 128 : 168;
-    static_assert(256 * kSoftRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs,
-                  "register shares");
+    static constexpr int kAuxWarps = kE4m3 ? 5 : 1;
+    static constexpr int kThreads = (11 + kAuxWarps) * 32;
     // tensor memory columns
-    static constexpr int kS = 0;                              // + 128 half
-    static constexpr int kP = kParts == 1 ? 0 : 128;          // + 128 half, + 64 part
+    static constexpr int kS = 0;                              // + 128 half + 64 turn
+    static constexpr int kP = kParts == 1 ? 0 : 128;          // + 128 half, + kPTurn turn, + 32 part
+    static constexpr int kPTurn = kParts == 1 ? 64 : 32 * kParts;
     static constexpr int kO = kParts == 1 ? 256 : 320;        // + 128 half
     // shared memory
     static constexpr int kQ = 0;
@@ -87,7 +86,8 @@ struct Seg {
 
 struct Shared {
     uint64_t info_full[kRing], info_empty[kRing], bad_full[kRing];
-    uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], drain;
+    uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], pv_done[2], o_full[2], drain[2];
+    uint64_t exp_turn[2][4];   // whose turn at the exponential units, by a half's 32 rows
     uint64_t kv_full[4], kv_empty[4], fixed[4], raw_full[4], raw_empty[4];
     Entry entry[kRing];
     Seg seg[kRing];
@@ -105,14 +105,24 @@ __device__ __forceinline__ uint64_t now_ns() {
     return t;
 }
 
-// Waits for the phase of `parity` to complete; false once a wait of this CTA has run out.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int32_t* abort,
-                                         uint64_t limit = kWaitLimitNs) {
-    const uint32_t b = smem_addr(bar);
-    for (int i = 0; i < 32; ++i)
-        if (mbar_try_wait(b, parity)) return true;
+// Waits for the phase of `parity` to complete; false once a wait of this CTA has run out. The
+// thread sleeps in the instruction for up to kNapNs at a time (or until the phase is complete): a
+// spinning warp would take issue slots from the softmax.
+__device__ __forceinline__ bool try_wait_nap(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok) : "r"(bar), "r"(parity), "r"(kNapNs) : "memory");
+    return ok != 0;
+}
+// (out of line: the roles' loops have to share the instruction caches)
+__device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, volatile int32_t* abort,
+                                       uint64_t limit) {
     const uint64_t t0 = now_ns();
-    while (!mbar_try_wait(b, parity)) {
+#pragma unroll 1
+    while (!try_wait_nap(bar, parity)) {
         if (*abort) return false;
         if (now_ns() - t0 > limit) {
             *abort = 1;
@@ -121,6 +131,11 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatil
         }
     }
     return true;
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int32_t* abort,
+                                         uint64_t limit = kWaitLimitNs) {
+    const uint32_t b = smem_addr(bar);
+    return try_wait_nap(b, parity) || wait_more(b, parity, abort, limit);
 }
 // the same by a whole warp, which goes on together
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
@@ -133,6 +148,33 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+// 2^x of a pair on the FMA units (the exponential units are the softmax's bottleneck), for x
+// that is not masked: x = n + f, |f| <= 1/2, by adding and taking away 1.5 * 2^23 + 127, 2^f by a
+// polynomial of degree 4 (fitted for the least relative error over the range: 2.6e-6, far below
+// the half step of a bf16 weight), and 2^n from the sum's low bits, which are n + 127. Below
+// 2^-126 it stays there; NaN stays NaN.
+__device__ __forceinline__ float2 ex2_fma(float2 x) {
+    const uint64_t z = pack2(max_nan(x.x, -126.0f), max_nan(x.y, -126.0f));
+    const uint64_t t = add2(z, pack2(12583039.0f, 12583039.0f));
+    const uint64_t f = fma2(add2(t, pack2(-12583039.0f, -12583039.0f)), pack2(-1.0f, -1.0f), z);
+    uint64_t p = pack2(0.00957010128f, 0.00957010128f);
+    p = fma2(p, f, pack2(0.0559178591f, 0.0559178591f));
+    p = fma2(p, f, pack2(0.240247443f, 0.240247443f));
+    p = fma2(p, f, pack2(0.693121791f, 0.693121791f));
+    p = fma2(p, f, pack2(0.999999285f, 0.999999285f));
+    const uint64_t n = pack2u(static_cast<uint32_t>(t) << 23, static_cast<uint32_t>(t >> 32) << 23);
+    return unpack2(fma2(p, n, 0));
 }
 __device__ __forceinline__ uint32_t bf2(float lo, float hi) {
     uint32_t r;
@@ -164,7 +206,8 @@ __device__ void load_role(const AttendArgs& a, const CUtensorMap* mq, const CUte
     const int lane = threadIdx.x & 31;
     const int G = a.shape.group, shift = a.pool.shift, causal = a.shape.causal;
     const int rt = a.shape.tile_rows / S::kHalves;             // rows of a half
-    const int run = min(1 << shift, kBlk), nrun = kBlk / run;  // tokens a copy, copies a block
+    const int rs = min(shift, 7), run = 1 << rs, nrun = kBlk >> rs;  // tokens a copy, copies a block
+    const int ns = 7 - rs;                                     // log2(nrun)
     int64_t h = x / per_head;
     int tile = warp_search(a.plan.pre, nt, x - h * per_head);
     uint32_t n = 0, seg = 0, ld = 0, nq = 0;   // entries, segments, tiles loaded, Q tiles loaded
@@ -191,11 +234,11 @@ __device__ void load_role(const AttendArgs& a, const CUtensorMap* mq, const CUte
         const int32_t* table = a.seqs.table + static_cast<int64_t>(s) * a.seqs.stride;
 
         // page ids come 32 at a time, a lane a run, one window ahead
-        const int per_win = 32 / nrun;                  // blocks of a window
+        const int per_win = 32 >> ns;                   // blocks of a window
         int win = b0, id = -1, id_next = -1;
         auto fetch = [&](int w) -> int {
             const int64_t tok = static_cast<int64_t>(w) * kBlk + lane * run;
-            return w + lane / nrun < b1 && tok < end ? table[tok >> shift] : -1;
+            return w + (lane >> ns) < b1 && tok < end ? table[tok >> shift] : -1;
         };
         id = fetch(win);
         id_next = fetch(win + per_win);
@@ -209,7 +252,7 @@ __device__ void load_role(const AttendArgs& a, const CUtensorMap* mq, const CUte
                 }
                 const uint32_t ok = __ballot_sync(
                     0xffffffffu, static_cast<uint32_t>(id) < static_cast<uint32_t>(a.pool.num_pages));
-                const int at = (b - win) * nrun;
+                const int at = (b - win) << ns;
                 *valid = (ok >> at) & (nrun == 32 ? ~0u : (1u << nrun) - 1);
                 *page = __shfl_sync(0xffffffffu, id, (at + lane) & 31);
                 if (*valid) return b;
@@ -234,8 +277,8 @@ __device__ void load_role(const AttendArgs& a, const CUtensorMap* mq, const CUte
             bool full = cur >= 0;
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
-                const uint32_t l = cur_valid >> (32 * f / run) & 1,
-                               u = cur_valid >> ((32 * f + 16) / run) & 1;
+                const uint32_t l = cur_valid >> (32 * f >> rs) & 1,
+                               u = cur_valid >> ((32 * f + 16) >> rs) & 1;
                 const int left = end - (cur * kBlk + 32 * f);
                 e.mask[f] = cur < 0 || left <= 0
                                 ? 0u
@@ -321,121 +364,172 @@ __device__ void load_role(const AttendArgs& a, const CUtensorMap* mq, const CUte
 }
 
 // ------------------------------------------------------------------------------- products
+// A warp a half, so that the books of one are kept while the other's products run. The whole warp
+// keeps them (the compiler then sees uniform values); one elected thread issues. A block is taken
+// in two turns of 64 tokens, each with its own columns of S and P, and the scores of the next turn
+// are issued before the weights of this one are there: the softmax never waits for the products'
+// latency. (Scores of 64 tokens cost 1.5 times their share of 128 tokens' - Q is read from shared
+// memory for half as many columns - which is less than the waits were.)
 template <bool kE4m3, int kParts>
-__device__ void mma_role(Shared& sh, uint8_t* smem, uint32_t tmem, bool inject) {
+__device__ void mma_role(Shared& sh, uint8_t* smem, uint32_t tmem, int half, bool inject) {
     using S = Shape<kE4m3, kParts>;
-    constexpr uint32_t kQK = mma_desc(kBlk, false), kPV = mma_desc(D, true);
+    constexpr uint32_t kQK = mma_desc(kTurn, false), kPV = mma_desc(D, true);
     volatile int32_t* ab = &sh.abort;
-    uint32_t n = 0, use = 0, nq = 0, np[2] = {0, 0}, fix = 0;   // use: tiles of the ring consumed
-    int cur = 0, nxt = 0;
+    const bool leader = elect_one();
+    uint32_t n = 0, nq = 0, nt = 0, fix = 0;   // nt: turns of the half
     constexpr int kSome = 64;   // a block's flags are never 0
     // flags of the next block with work, 0 at the end, -1 after a wait ran out
     auto fetch = [&]() -> int {
         while (true) {
             const int slot = n % kRing;
-            if (!wait_for(&sh.info_full[slot], (n / kRing) & 1, ab)) return -1;
+            if (!warp_wait(&sh.info_full[slot], (n / kRing) & 1, ab)) return -1;
             const int f = sh.entry[slot].flags, b = sh.entry[slot].block;
-            arrive(&sh.info_empty[slot]);
+            __syncwarp();
+            if (leader) arrive(&sh.info_empty[slot]);
             ++n;
             if (b >= 0) return f | kSome;
             if (f & kEnd) return 0;
         }
     };
-    // S of a half from Q and the K tile in stage st
-    auto qk = [&](int i, int st) {
-        const uint32_t q = smem_addr(smem + S::kQ + i * kStageB);
-        const uint32_t k = smem_addr(smem + S::kKV + st * kStageB);
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-            const uint32_t at = (j >> 2) * kHalfB + (j & 3) * 32;
-            mma_ss(tmem + S::kS + 128 * i, smem_desc(q + at, 16), smem_desc(k + at, 16), kQK, j > 0);
+    const uint64_t q_desc = smem_desc(uniform(smem_addr(smem + S::kQ + half * kStageB)), 16);
+    const uint64_t k_desc = smem_desc(uniform(smem_addr(smem + S::kKV)), 16);
+    const uint64_t v_desc = smem_desc(uniform(smem_addr(smem + S::kKV)), kHalfB);
+    const uint32_t s_at = uniform(tmem + S::kS + 128 * half),
+                   o_at = uniform(tmem + S::kO + 128 * half),
+                   p_at = uniform(tmem + S::kP + 128 * half);
+    auto tile_ready = [&](uint32_t u) -> bool {
+        return warp_wait(&sh.kv_full[u % S::kStages], (u / S::kStages) & 1, ab);
+    };
+    auto has_rows = [&](int flags) -> bool { return half == 0 || (flags & kTwo); };
+    // scores of turn `nt + ahead` from the K tile u
+    auto qk = [&](int flags, uint32_t u, int w, int ahead) -> bool {
+        if (w == 0) {
+            if ((flags & kFirst) && !warp_wait(&sh.q_full, nq++ & 1, ab)) return false;
+            if (!tile_ready(u)) return false;
         }
-        mma_commit(smem_addr(&sh.s_full[i]));
-    };
-    auto pv = [&](int i, int st, bool accumulate) {
-        const uint32_t v = smem_addr(smem + S::kKV + st * kStageB);
+        const uint32_t turn = nt + ahead;
+        if (has_rows(flags)) {
+            // they go where the weights of two turns ago were read
+            if (turn >= 2 && !warp_wait(&sh.pv_done[half], turn & 1, ab)) return false;
+            tc_fence_after();
+            const uint64_t k = uniform(k_desc + (u % S::kStages) * (kStageB >> 4) + w * (kTurn * 128 >> 4));
+            const uint32_t d = uniform(s_at + kTurn * (turn & 1));
+            if (leader) {
 #pragma unroll
-        for (int p = 0; p < kParts; ++p)
-#pragma unroll
-            for (int j = 0; j < kBlk / 16; ++j)
-                mma_ts(tmem + S::kO + 128 * i, tmem + S::kP + 128 * i + 64 * p + 8 * j,
-                       smem_desc(v + j * 16 * 128, kHalfB), kPV, accumulate || p > 0 || j > 0);
-        mma_commit(smem_addr(&sh.pv_done[i]));
+                for (int j = 0; j < D / 16; ++j) {
+                    const uint32_t at = ((j >> 2) * kHalfB + (j & 3) * 32) >> 4;
+                    mma_ss(d, q_desc + at, k + at, kQK, j > 0);
+                }
+                mma_commit(smem_addr(&sh.s_full[half][turn & 1]));
+            }
+        }
+        if (w == 1 && leader) {
+            mma_commit(smem_addr(&sh.kv_empty[u % S::kStages]));
+            if (flags & kLast) mma_commit(smem_addr(&sh.q_empty));
+        }
+        __syncwarp();
+        return true;
     };
-    auto k_ready = [&](int flags) -> bool {   // Q of a new tile, and the K tile `use`
-        if ((flags & kFirst) && !wait_for(&sh.q_full, nq++ & 1, ab)) return false;
-        return wait_for(&sh.kv_full[use % S::kStages], (use / S::kStages) & 1, ab);
+    // O += P V of turn `nt` with the V tile u
+    auto pv = [&](int flags, uint32_t u, int w) -> bool {
+        const int st = u % S::kStages;
+        if (w == 0) {
+            if (!tile_ready(u)) return false;
+            if (!kE4m3 && (flags & kFix)) {
+                if (!warp_wait(&sh.fixed[st], fix >> st & 1, ab)) return false;
+                fix ^= 1u << st;
+            }
+        }
+        if (has_rows(flags)) {
+            if (!warp_wait(&sh.p_full[half][nt & 1], nt >> 1 & 1, ab)) return false;
+            tc_fence_after();
+            const uint64_t v = uniform(v_desc + st * (kStageB >> 4) + w * (kTurn * 128 >> 4));
+            const uint32_t p0 = uniform(p_at + S::kPTurn * (nt & 1));
+            if (leader) {
+#pragma unroll
+                for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                    for (int j = 0; j < kTurn / 16; ++j)
+                        mma_ts(o_at, p0 + 32 * p + 8 * j, v + ((j * 16 * 128) >> 4), kPV,
+                               !(flags & kFirst) || w > 0 || p > 0 || j > 0);
+                mma_commit(smem_addr(&sh.pv_done[half]));
+                if ((flags & kLast) && w == 1) mma_commit(smem_addr(&sh.o_full[half]));
+            }
+            ++nt;
+        }
+        if (w == 1 && leader) mma_commit(smem_addr(&sh.kv_empty[st]));
+        __syncwarp();
+        return true;
     };
 
     if (inject) {   // test hook: a wait for an arrival that never comes
         wait_for(&sh.raw_full[3], 0, ab, 1000000ull);
         return;
     }
-    cur = fetch();
-    if (cur <= 0) return;
-    if (!k_ready(cur)) return;
-    tc_fence_after();
-    for (int i = 0; i < (cur & kTwo ? 2 : 1); ++i) qk(i, use % S::kStages);
-    mma_commit(smem_addr(&sh.kv_empty[use % S::kStages]));
-    if (cur & kLast) mma_commit(smem_addr(&sh.q_empty));
-    ++use;
-    while (cur > 0) {
-        const int sv = use % S::kStages;
-        const uint32_t pv_parity = (use / S::kStages) & 1;
-        ++use;
-        nxt = fetch();
-        if (nxt < 0) return;
-        const int hc = cur & kTwo ? 2 : 1, hn = nxt == 0 ? 0 : nxt & kTwo ? 2 : 1;
-        for (int i = 0; i < max(hc, hn); ++i) {
-            if (i < hc) {
-                if (i == 0) {
-                    if (!wait_for(&sh.kv_full[sv], pv_parity, ab)) return;
-                    if (!kE4m3 && (cur & kFix)) {
-                        if (!wait_for(&sh.fixed[sv], fix >> sv & 1, ab)) return;
-                        fix ^= 1u << sv;
-                    }
-                }
-                if (!wait_for(&sh.p_full[i], np[i]++ & 1, ab)) return;
-                tc_fence_after();
-                pv(i, sv, !(cur & kFirst));
-                if (i == hc - 1) mma_commit(smem_addr(&sh.kv_empty[sv]));
-            }
-            if (i < hn) {
-                if (i == 0 && !k_ready(nxt)) return;
-                // the new scores go where the half's last weights are read
-                if (np[i] > 0 && !wait_for(&sh.pv_done[i], (np[i] - 1) & 1, ab)) return;
-                tc_fence_after();
-                qk(i, use % S::kStages);
-                if (i == hn - 1) {
-                    mma_commit(smem_addr(&sh.kv_empty[use % S::kStages]));
-                    if (nxt & kLast) mma_commit(smem_addr(&sh.q_empty));
-                }
+    // the turn whose scores come next (flags of its block, its K tile, which half of it), and the
+    // one behind it whose weights come next
+    int fq = fetch(), wq = 0, fp = fq, wp = 0;
+    uint32_t uq = 0, up = 1;
+    if (fq <= 0) return;
+    bool ahead = false;
+#pragma unroll 1
+    while (true) {
+        if (fq > 0) {
+            if (!qk(fq, uq, wq, ahead && has_rows(fp) ? 1 : 0)) return;
+            if (wq == 0) {
+                wq = 1;
+            } else {
+                // (the ring holds a tile's V behind its K, and the next K behind that; none of
+                // them waits for the products issued here to make room)
+                fq = fetch();
+                if (fq < 0) return;
+                uq += 2;
+                wq = 0;
             }
         }
-        if (nxt > 0) ++use;
-        cur = nxt;
+        if (!ahead) {
+            ahead = true;
+            continue;
+        }
+        if (!pv(fp, up, wp)) return;
+        if (wp == 0) {
+            wp = 1;
+        } else {
+            fp = fq;
+            wp = 0;
+            up += 2;
+            if (fp == 0) return;
+        }
     }
 }
 
 // ----------------------------------------------------------------- softmax and the output
+// A warpgroup a half, a thread a row.
 template <bool kE4m3, int kParts, typename Out>
 __device__ void softmax_role(const AttendArgs& a, Shared& sh, uint32_t tmem, int half) {
     using S = Shape<kE4m3, kParts>;
-    const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+    const int quad = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const int G = a.shape.group, R = a.shape.tile_rows, rt = R / S::kHalves;
-    const int rl = 32 * warp + lane;                            // row of the half
+    const int rl = 32 * quad + lane;                            // row of the half
     const int r = rl < rt ? half * rt + rl : INT32_MAX;         // row of the tile
-    const uint32_t ts = tmem + (warp << 21) + S::kS + 128 * half;
-    const uint32_t tp = tmem + (warp << 21) + S::kP + 128 * half;
-    const uint32_t to = tmem + (warp << 21) + S::kO + 128 * half;
+    const uint32_t at0 = tmem + (quad << 21) + 128 * half;
     volatile int32_t* ab = &sh.abort;
     // scores times a positive factor c, after a sign (negative scales) or zero (scale 0)
     const float c = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * kLog2e;
     const float sign = a.scale > 0.0f ? 1.0f : a.scale < 0.0f ? -1.0f : 0.0f;
 
-    uint32_t n = 0, seg = 0, ns = 0;    // entries, segments, blocks of this half
+    uint32_t n = 0, seg = 0, nt = 0, no = 0;   // entries, segments; turns, outputs of this half
+    uint32_t nx = 0;                    // turns at the exponential units
     float m = -INFINITY, l = 0.0f;      // the row's maximum (times c) as last used, and its sum
     int lim = -1;
+    auto exp_wait = [&]() -> bool {
+        return S::kHalves == 1 ||
+               warp_wait(&sh.exp_turn[half][quad], (nx & 1) ^ (half == 0 ? 1 : 0), ab);
+    };
+    auto exp_done = [&]() {
+        ++nx;
+        if (S::kHalves == 2 && lane == 0) arrive(&sh.exp_turn[half ^ 1][quad]);
+    };
     while (true) {
         const int slot = n % kRing;
         if (!warp_wait(&sh.info_full[slot], (n / kRing) & 1, ab)) return;
@@ -449,108 +543,125 @@ __device__ void softmax_role(const AttendArgs& a, Shared& sh, uint32_t tmem, int
         }
         const bool mine = half == 0 || (flags & kTwo);
         if (mine && !(flags & kEmpty)) {
-            if (!warp_wait(&sh.s_full[half], ns & 1, ab)) return;
-            tc_fence_after();
-            uint32_t s[128];
-            tmem_ld32(ts, s);
-            tmem_ld32(ts + 32, s + 32);
-            tmem_ld32(ts + 64, s + 64);
-            tmem_ld32(ts + 96, s + 96);
-            tmem_wait_ld();
-            if (sign != 1.0f) {
-#pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    s[i] = __float_as_uint(__uint_as_float(s[i]) * sign);
-            }
-            if (flags & kFix) {
-                const int left = lim - block * kBlk + 1;   // tokens up to the row's limit
-#pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    const int k = left - 32 * f;
-                    const uint32_t w = k <= 0 ? 0u
-                                              : sh.entry[slot].mask[f] &
-                                                    (k >= 32 ? ~0u : (1u << k) - 1);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (!(w >> i & 1)) s[32 * f + i] = 0xff800000u;
-                }
-            }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < 128; i += 8)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(s[i + 2 * k]),
-                                               __uint_as_float(s[i + 2 * k + 1])));
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-            const bool first = flags & kFirst;
-            bool waited = false;
-            if (first) {
-                m = top;
-            } else if (__any_sync(0xffffffffu, top > m + kRescale)) {
-                const float m1 = top > m + kRescale ? top : m;
-                const float f = m1 == -INFINITY ? 1.0f : ex2(m - m1);
-                m = m1;
-                l *= f;
-                // the last product into O has to be there before it is rescaled
-                if (!warp_wait(&sh.pv_done[half], (ns - 1) & 1, ab)) return;
-                waited = true;
+#pragma unroll 1
+            for (int w = 0; w < 2; ++w, ++nt) {
+                const int turn = nt & 1;
+                if (!warp_wait(&sh.s_full[half][turn], nt >> 1 & 1, ab)) return;
                 tc_fence_after();
+                uint32_t s[kTurn];
+                tmem_ld32(at0 + S::kS + kTurn * turn, s);
+                tmem_ld32(at0 + S::kS + kTurn * turn + 32, s + 32);
+                tmem_wait_ld();
+                if (__builtin_expect(sign != 1.0f, 0)) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t o[32];
-                    tmem_ld32(to + 32 * i, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                    tmem_st32(to + 32 * i, o);
+                    for (int i = 0; i < kTurn; ++i)
+                        s[i] = __float_as_uint(__uint_as_float(s[i]) * sign);
                 }
-            }
-            if (kParts > 1 && ns > 0 && !waited) {
-                // the weights' columns are free once the last product has read them
-                if (!warp_wait(&sh.pv_done[half], (ns - 1) & 1, ab)) return;
-                tc_fence_after();
-            }
-            const float ms = m == -INFINITY ? 0.0f : m;
-            const uint64_t c2 = pack2(c, c), m2 = pack2(-ms, -ms);
-            uint64_t sum[2] = {0, 0};
+                if (__builtin_expect(flags & kFix, 0)) {
+                    const int left = lim - block * kBlk - kTurn * w + 1;   // up to the row's limit
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float p[32];
+                    for (int f = 0; f < 2; ++f) {
+                        const int k = left - 32 * f;
+                        const uint32_t seen = k <= 0 ? 0u
+                                                     : sh.entry[slot].mask[2 * w + f] &
+                                                           (k >= 32 ? ~0u : (1u << k) - 1);
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    const float2 y = unpack2(fma2(pack2u(s[32 * q + i], s[32 * q + i + 1]), c2, m2));
-                    p[i] = ex2(y.x);
-                    p[i + 1] = ex2(y.y);
-                    sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(p[i], p[i + 1]));
-                }
-#pragma unroll
-                for (int k = 0; k < kParts; ++k) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        w[i] = bf2(p[2 * i], p[2 * i + 1]);
-                        if (k + 1 < kParts) {
-                            p[2 * i] -= lo_f(w[i]);
-                            p[2 * i + 1] -= hi_f(w[i]);
-                        }
+                        for (int i = 0; i < 32; ++i)
+                            if (!(seen >> i & 1)) s[32 * f + i] = 0xff800000u;
                     }
-                    tmem_st16(tp + 64 * k + 16 * q, w);
                 }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < kTurn; i += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mx[k] = max3(mx[k], __uint_as_float(s[i + 2 * k]),
+                                     __uint_as_float(s[i + 2 * k + 1]));
+                const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * c;
+                if ((flags & kFirst) && w == 0) {
+                    m = top;
+                } else if (__builtin_expect(__any_sync(0xffffffffu, top > m + kRescale), 0)) {
+                    const float m1 = top > m + kRescale ? top : m;
+                    const float f = m1 == -INFINITY ? 1.0f : ex2(m - m1);
+                    m = m1;
+                    l *= f;
+                    // the last product into O has to be there before it is rescaled (the one
+                    // before it is: its weights' columns hold these scores)
+                    if (!warp_wait(&sh.pv_done[half], (nt - 1) & 1, ab)) return;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {
+                        uint32_t o[16];
+                        tmem_ld16(at0 + S::kO + 16 * i, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tmem_st16(at0 + S::kO + 16 * i, o);
+                    }
+                }
+                float ms = m == -INFINITY ? 0.0f : m;
+                // the two warps of an SM quarter (one of each half) take turns at its exponential
+                // units: left alone they run in step, and the units idle while both do the rest
+                if (!exp_wait()) return;
+                asm volatile("" : "+f"(ms));   // (not before the wait)
+                const uint64_t c2 = pack2(c, c), m2 = pack2(-ms, -ms);
+                uint64_t sum[2] = {0, 0};
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float p[32];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 y = unpack2(
+                            fma2(pack2u(s[32 * q + i], s[32 * q + i + 1]), c2, m2));
+                        if (kParts == 1 && i % 16 < kPoly) {
+                            const float2 z = ex2_fma(y);
+                            p[i] = z.x;
+                            p[i + 1] = z.y;
+                            if (flags & kFix) {   // what is masked must be 0
+                                if (y.x == -INFINITY) p[i] = 0.0f;
+                                if (y.y == -INFINITY) p[i + 1] = 0.0f;
+                            }
+                        } else {
+                            p[i] = ex2(y.x);
+                            p[i + 1] = ex2(y.y);
+                        }
+                        sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(p[i], p[i + 1]));
+                    }
+#pragma unroll
+                    for (int k = 0; k < kParts; ++k) {
+                        uint32_t x[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            x[i] = bf2(p[2 * i], p[2 * i + 1]);
+                            if (k + 1 < kParts) {
+                                p[2 * i] -= lo_f(x[i]);
+                                p[2 * i + 1] -= hi_f(x[i]);
+                            }
+                        }
+                        tmem_st16(at0 + S::kP + S::kPTurn * turn + 32 * k + 16 * q, x);
+                    }
+                }
+                exp_done();
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(&sh.p_full[half][turn]);
+                const float2 y = unpack2(add2(sum[0], sum[1]));
+                l += y.x + y.y;
             }
-            const float2 y = unpack2(add2(sum[0], sum[1]));
-            l += y.x + y.y;
-            tmem_wait_st();
-            tc_fence_before();
-            arrive(&sh.p_full[half]);
-            ++ns;
+        }
+        if (!mine && !(flags & kEmpty)) {   // (both halves count the same turns)
+            for (int w = 0; w < 2; ++w) {
+                if (!exp_wait()) return;
+                exp_done();
+            }
         }
         if (flags & kLast) {
             if (mine) {
                 const bool empty = flags & kEmpty;
                 if (!empty) {
-                    if (!warp_wait(&sh.pv_done[half], (ns - 1) & 1, ab)) return;
+                    if (!warp_wait(&sh.o_full[half], no++ & 1, ab)) return;
                     tc_fence_after();
                 }
                 if (!warp_wait(&sh.bad_full[seg % kRing], (seg / kRing) & 1, ab)) return;
@@ -561,40 +672,42 @@ __device__ void softmax_role(const AttendArgs& a, Shared& sh, uint32_t tmem, int
                 const int64_t at = (g.row0 + rr / G) * (static_cast<int64_t>(a.heads) * G) +
                                    g.head * G + rr % G;
                 float* part = a.work + g.part * part_floats(R);
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t o[32];
+#pragma unroll 1
+                for (int q = 0; q < 8; ++q) {
+                    const int col = 16 * q;
+                    uint32_t o[16];
                     if (!empty) {
-                        tmem_ld32(to + 32 * q, o);
+                        tmem_ld16(at0 + S::kO + col, o);
                         tmem_wait_ld();
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
+                    for (int i = 0; i < 16; ++i) {
                         const float y = empty ? 0.0f : __uint_as_float(o[i]) * inv;
                         o[i] = __float_as_uint(y);
                     }
                     if (bad) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (sh.bad[seg % kRing][32 * q + i] <= lim) o[i] = 0x7fc00000u;
+                        for (int i = 0; i < 16; ++i)
+                            if (sh.bad[seg % kRing][col + i] <= lim) o[i] = 0x7fc00000u;
                     }
                     if (live && g.whole && sizeof(Out) == 2) {
                         uint4* dst = reinterpret_cast<uint4*>(
-                            static_cast<__nv_bfloat16*>(a.out) + at * D + 32 * q);
+                            static_cast<__nv_bfloat16*>(a.out) + at * D + col);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t* w = o + 8 * i;
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t* u = o + 8 * i;
                             dst[i] = make_uint4(
-                                bf2(__uint_as_float(w[0]), __uint_as_float(w[1])),
-                                bf2(__uint_as_float(w[2]), __uint_as_float(w[3])),
-                                bf2(__uint_as_float(w[4]), __uint_as_float(w[5])),
-                                bf2(__uint_as_float(w[6]), __uint_as_float(w[7])));
+                                bf2(__uint_as_float(u[0]), __uint_as_float(u[1])),
+                                bf2(__uint_as_float(u[2]), __uint_as_float(u[3])),
+                                bf2(__uint_as_float(u[4]), __uint_as_float(u[5])),
+                                bf2(__uint_as_float(u[6]), __uint_as_float(u[7])));
                         }
                     } else if (live) {
                         uint4* dst = reinterpret_cast<uint4*>(
-                            g.whole ? static_cast<float*>(a.out) + at * D + 32 * q
-                                    : part + static_cast<size_t>(r) * D + 32 * q);
+                            g.whole ? static_cast<float*>(a.out) + at * D + col
+                                    : part + static_cast<size_t>(r) * D + col);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
+                        for (int i = 0; i < 4; ++i)
                             dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                     __syncwarp();
@@ -620,7 +733,7 @@ template <bool kE4m3, int kParts>
 __device__ void aux_role(const AttendArgs& a, Shared& sh, uint8_t* smem) {
     using S = Shape<kE4m3, kParts>;
     constexpr int kT = S::kAuxWarps * 32;
-    const int tid = threadIdx.x - 320, lane = tid & 31;
+    const int tid = threadIdx.x - 11 * 32, lane = tid & 31;
     volatile int32_t* ab = &sh.abort;
     uint32_t n = 0, seg = 0, use = 0;   // use: tiles of the ring seen
     while (true) {
@@ -762,20 +875,24 @@ attend_chunk_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap mq,
         auto init = [&](uint64_t* b, uint32_t count) { mbar_init(smem_addr(b), count); };
         for (int i = 0; i < kRing; ++i) {
             init(&sh.info_full[i], 1);
-            init(&sh.info_empty[i], 4 * S::kHalves + 1 + S::kAuxWarps);
+            init(&sh.info_empty[i], 5 * S::kHalves + S::kAuxWarps);
             init(&sh.bad_full[i], S::kAuxWarps);
         }
         init(&sh.q_full, 1);
-        init(&sh.q_empty, 1);
-        init(&sh.drain, 1);
+        init(&sh.q_empty, S::kHalves);
         for (int i = 0; i < 2; ++i) {
-            init(&sh.s_full[i], 1);
-            init(&sh.p_full[i], 128);
+            for (int k = 0; k < 2; ++k) {
+                init(&sh.s_full[i][k], 1);
+                init(&sh.p_full[i][k], 4);
+            }
             init(&sh.pv_done[i], 1);
+            init(&sh.o_full[i], 1);
+            for (int k = 0; k < 4; ++k) init(&sh.exp_turn[i][k], 1);
+            init(&sh.drain[i], 1);
         }
         for (int i = 0; i < 4; ++i) {
             init(&sh.kv_full[i], kE4m3 ? S::kAuxWarps : 1);
-            init(&sh.kv_empty[i], 1);
+            init(&sh.kv_empty[i], S::kHalves);
             init(&sh.fixed[i], S::kAuxWarps);
             init(&sh.raw_full[i], 1);
             init(&sh.raw_empty[i], S::kAuxWarps);
@@ -795,24 +912,21 @@ attend_chunk_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap mq,
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
 
     if (warp < 8) {
-        regs_up<S::kSoftRegs>();
         if (warp < 4 * S::kHalves) softmax_role<kE4m3, kParts, Out>(a, sh, tmem, warp >> 2);
-    } else {
-        regs_down<S::kOtherRegs>();
-        if (warp == 8) {
-            load_role<kE4m3, kParts>(a, &mq, &mk, &mv, sh, smem, x, hi, per_head, nt);
-        } else if (warp == 9) {
-            if ((threadIdx.x & 31) == 0) {
-                mma_role<kE4m3, kParts>(sh, smem, tmem, a.inject_wait);
-                // nothing may be under way in tensor memory when it is given back
-                mma_commit(smem_addr(&sh.drain));
-                int32_t no = 0;
-                wait_for(&sh.drain, 0, &no);
-            }
+    } else if (warp == 8) {
+        load_role<kE4m3, kParts>(a, &mq, &mk, &mv, sh, smem, x, hi, per_head, nt);
+    } else if (warp < 11) {
+        const int half = warp - 9;
+        if (half < S::kHalves) {
+            mma_role<kE4m3, kParts>(sh, smem, tmem, half, a.inject_wait);
+            // nothing may be under way in tensor memory when it is given back
             __syncwarp();
-        } else {
-            aux_role<kE4m3, kParts>(a, sh, smem);
+            if (elect_one()) mma_commit(smem_addr(&sh.drain[half]));
+            int32_t no = 0;
+            warp_wait(&sh.drain[half], 0, &no);
         }
+    } else {
+        aux_role<kE4m3, kParts>(a, sh, smem);
     }
     tc_fence_before();
     __syncthreads();

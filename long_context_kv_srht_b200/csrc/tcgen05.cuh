@@ -45,6 +45,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
           "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr) : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr) : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -68,6 +77,20 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
 }
 
 // ---- matrix products, issued by one thread ----
+// one thread of a converged warp, the same one every time
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok));
+    return ok != 0;
+}
+// a value that all lanes share, told to the compiler (the operands of the instructions below
+// live in uniform registers)
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ uint64_t uniform(uint64_t x) {
+    return static_cast<uint64_t>(uniform(static_cast<uint32_t>(x >> 32))) << 32 |
+           uniform(static_cast<uint32_t>(x));
+}
 // bf16 x bf16 -> fp32, M = 128, K = 16 a step. Bits: 4-5 D fp32, 7-9 A bf16, 10-12 B bf16,
 // 16 B is MN-major, 17-22 N / 8, 24-28 M / 16.
 constexpr uint32_t mma_desc(uint32_t n, bool b_mn_major) {
