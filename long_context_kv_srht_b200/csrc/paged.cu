@@ -234,6 +234,8 @@ plan_kernel(const Seqs c, int shift, const PlanShape p, const Plan plan) {
     __shared__ int64_t s_warp[kPlanT / 32];
     __shared__ int32_t s_first[kPlanT], s_count[kPlanT];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_launch_dependents();
     int64_t tiles = 0;
     for (int s0 = 0; s0 < c.batch; s0 += kPlanT) {
         const int s = s0 + threadIdx.x;
@@ -251,10 +253,18 @@ plan_kernel(const Seqs c, int shift, const PlanShape p, const Plan plan) {
             if (n == 0) continue;
             const SeqView v = seq_view(c, shift, s0 + i);
             for (int t = lane; t < n; t += 32) {
-                const int at2 = s_first[i] + t;
-                plan.seq[at2] = s0 + i;
-                plan.row[at2] = t * p.tile_rows;
-                plan.pre[at2 + 1] = tile_blocks(v, p, t * p.tile_rows);
+                Tile x;
+                x.first = t * p.tile_rows;
+                x.pre = tile_blocks(v, p, x.first);   // (its own, until they are summed)
+                x.pos0 = v.pos0;
+                x.seq = s0 + i;
+                x.row0 = v.row0;
+                x.nrow = static_cast<int32_t>(
+                    min64(p.tile_rows, static_cast<int64_t>(v.rows) * p.group - x.first));
+                x.end = tile_end(v, p, x.first);
+                x.kv = v.kv;
+                x.pad[0] = x.pad[1] = 0;
+                plan.tile[s_first[i] + t] = x;
             }
         }
         tiles = min64(tiles + all, plan.max_tiles);
@@ -262,67 +272,91 @@ plan_kernel(const Seqs c, int shift, const PlanShape p, const Plan plan) {
     }
     const int nt = static_cast<int>(tiles);
     int64_t sum = 0;
-    if (threadIdx.x == 0) {
-        plan.pre[0] = 0;
-        *plan.ntiles = nt;
-    }
     for (int t0 = 0; t0 < nt; t0 += kPlanT) {
         const int t = t0 + threadIdx.x;
         int64_t all;
-        const int64_t x = block_scan(t < nt ? plan.pre[t + 1] : 0, s_warp, &all);
-        if (t < nt) plan.pre[t + 1] = sum + x;
+        const int64_t own = t < nt ? plan.tile[t].pre : 0;
+        const int64_t x = block_scan(own, s_warp, &all);
+        if (t < nt) plan.tile[t].pre = sum + x - own;
         sum += all;
+    }
+    if (threadIdx.x == 0) {
+        plan.tile[nt].pre = sum;
+        *plan.ntiles = nt;
     }
 }
 
 // ------------------------------------------------------------------------------------- join
 // The tile that the cut before CTA c = blockIdx.x + 1 goes through, if that cut is the tile's
 // first: its parts, from the CTA of its first block to the CTA of its last, are rescaled to the
-// common maximum and summed in that order. One warp a row, 4 elements a lane.
+// common maximum and summed. A warp a row, 4 elements a lane; with many parts (few rows, a long
+// token axis) the CTA's warps share a row's parts and add their sums up in order.
 constexpr int kJoinWarps = 4;
+constexpr int kJoinShared = 8;    // parts from which on the warps share a row
 
 template <typename Out>
 __global__ void __launch_bounds__(kJoinWarps * 32)
 join_kernel(const AttendArgs a, int ctas) {
+    __shared__ float s_sum[kJoinWarps][D + 2];
+    pdl_wait();
+    pdl_launch_dependents();
     const int nt = *a.plan.ntiles;
-    const int64_t per_head = a.plan.pre[nt], total = per_head * a.heads;
-    if (total == 0) return;
-    const int lane = threadIdx.x & 31;
-    const int64_t lo = cut(total, ctas, blockIdx.x + 1);
-    if (lo >= total) return;
+    const int64_t per_head = a.plan.tile[nt].pre, total = per_head * a.heads;
+    const int64_t n = cuts(total, ctas);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (static_cast<int64_t>(blockIdx.x) + 1 >= n) return;
+    const int64_t lo = cut(total, n, blockIdx.x + 1);
     const int64_t h = lo / per_head;
-    const int tile = warp_search(a.plan.pre, nt, lo - h * per_head);
-    const int64_t start = h * per_head + a.plan.pre[tile];
-    const int64_t end = h * per_head + a.plan.pre[tile + 1];
-    const int64_t c0 = cut_of(total, ctas, start);
-    if (start == lo || c0 != blockIdx.x) return;
-    const int64_t c1 = cut_of(total, ctas, end - 1);
+    const int at_tile = find_tile(a.plan.tile, nt, lo - h * per_head);
+    const Tile t = a.plan.tile[at_tile];
+    const int64_t start = h * per_head + t.pre;
+    const int64_t end = h * per_head + a.plan.tile[at_tile + 1].pre;
+    if (start == lo) return;
+    const int c0 = static_cast<int>(cut_of(total, n, start));
+    if (c0 != static_cast<int>(blockIdx.x)) return;
+    const int parts = static_cast<int>(cut_of(total, n, end - 1)) - c0 + 1;
     const int R = a.shape.tile_rows, G = a.shape.group;
-    const SeqView v = seq_view(a.seqs, a.pool.shift, a.plan.seq[tile]);
-    const int64_t first = a.plan.row[tile];
-    const int64_t rows = min64(R, static_cast<int64_t>(v.rows) * G - first);
-    for (int64_t r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < rows;
-         r += gridDim.y * kJoinWarps) {
+    const bool shared = parts >= kJoinShared;
+    const size_t step = 2 * part_floats(R);
+    // part i: slot 2 (c0 + i), the first one 2 c0 + 1
+    const float* base = a.work + 2 * static_cast<size_t>(c0) * part_floats(R);
+    auto part = [&](int i) { return base + i * step + (i == 0 ? part_floats(R) : 0); };
+    const int i0 = shared ? warp : 0, istep = shared ? kJoinWarps : 1;
+    const int r0 = shared ? blockIdx.y : blockIdx.y * kJoinWarps + warp;
+    for (int r = r0; r < t.nrow; r += gridDim.y * (shared ? 1 : kJoinWarps)) {
         float M = -INFINITY;
-        for (int64_t c = c0; c <= c1; ++c) {
-            if (cut(total, ctas, c) == cut(total, ctas, c + 1)) continue;
-            M = fmaxf(M, a.work[(2 * c + (c == c0)) * part_floats(R) + R * D + r]);
-        }
+        for (int i = lane; i < parts; i += 32) M = fmaxf(M, part(i)[R * D + r]);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
         const float m = M == -INFINITY ? 0.0f : M;
         float den = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-        for (int64_t c = c0; c <= c1; ++c) {
-            if (cut(total, ctas, c) == cut(total, ctas, c + 1)) continue;
-            const float* w = a.work + (2 * c + (c == c0)) * part_floats(R);
+        for (int i = i0; i < parts; i += istep) {
+            const float* w = part(i);
             const float f = exp2f(w[R * D + r] - m);
             den += w[R * D + R + r] * f;
             const float4 x = *reinterpret_cast<const float4*>(w + r * D + 4 * lane);
             o[0] += x.x * f; o[1] += x.y * f; o[2] += x.z * f; o[3] += x.w * f;
         }
+        if (shared) {
+            *reinterpret_cast<float2*>(&s_sum[warp][4 * lane]) = make_float2(o[0], o[1]);
+            *reinterpret_cast<float2*>(&s_sum[warp][4 * lane + 2]) = make_float2(o[2], o[3]);
+            if (lane == 0) s_sum[warp][D] = den;
+            __syncthreads();
+            if (warp == 0) {
+                for (int w = 1; w < kJoinWarps; ++w) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[k] += s_sum[w][4 * lane + k];
+                    den += s_sum[w][D];
+                }
+            }
+            __syncthreads();
+            if (warp != 0) continue;
+        }
         // a row without tokens has den == 0 (a NaN must come through)
         const float inv = den == 0.0f ? 0.0f : 1.0f / den;
-        const int64_t rr = first + r, tok = v.row0 + rr / G;
-        const int64_t at = tok * (static_cast<int64_t>(a.heads) * G) + h * G + rr % G;
+        const int rr = t.first + r;
+        const int64_t at = (t.row0 + rr / G) * (static_cast<int64_t>(a.heads) * G) + h * G + rr % G;
         Out* dst = static_cast<Out*>(a.out) + at * D + 4 * lane;
         if constexpr (sizeof(Out) == 2)
             *reinterpret_cast<uint2*>(dst) = make_uint2(bf16_pair(o[0] * inv, o[1] * inv),
@@ -337,18 +371,15 @@ join_kernel(const AttendArgs a, int ctas) {
 }  // namespace
 
 cudaError_t launch_plan(const AttendArgs& a, cudaStream_t st) {
-    plan_kernel<<<1, kPlanT, 0, st>>>(a.seqs, a.pool.shift, a.shape, a.plan);
-    return cudaGetLastError();
+    return launch_pdl(plan_kernel, dim3(1), dim3(kPlanT), 0, st, a.seqs, a.pool.shift, a.shape,
+                      a.plan);
 }
 
 cudaError_t launch_join(const AttendArgs& a, int ctas, bool f32_out, cudaStream_t st) {
     if (ctas < 2) return cudaSuccess;
-    const dim3 grid(ctas - 1, static_cast<unsigned>(ceil_div(a.shape.tile_rows, 4 * kJoinWarps)));
-    if (f32_out)
-        join_kernel<float><<<grid, kJoinWarps * 32, 0, st>>>(a, ctas);
-    else
-        join_kernel<__nv_bfloat16><<<grid, kJoinWarps * 32, 0, st>>>(a, ctas);
-    return cudaGetLastError();
+    const dim3 grid(ctas - 1, min(16, a.shape.tile_rows));
+    return launch_pdl(f32_out ? join_kernel<float> : join_kernel<__nv_bfloat16>, grid,
+                      dim3(kJoinWarps * 32), 0, st, a, ctas);
 }
 
 namespace {
@@ -576,17 +607,15 @@ pariskv_status pariskv_paged_attend(const pariskv_config* cfg, const pariskv_pag
     const int64_t tiles = min64(cfg->batch * ceil_div(most, a.shape.tile_rows),
                                 chunk->total_q * cfg->group / a.shape.tile_rows + cfg->batch);
     if (tiles > (1 << 28)) return fail(PARISKV_EINVAL, "too many query rows for one call");
-    const size_t pre = round_up((tiles + 1) * 8, 256), ids = round_up(tiles * 4, 256);
+    const size_t plan = round_up((tiles + 1) * sizeof(Tile), 256);
     const size_t parts = round_up(2 * ctas * part_floats(a.shape.tile_rows) * 4, 256);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     void* ws = nullptr;
-    if ((s = take_workspace(&ws, parts + pre + 2 * ids + 256, st)) != PARISKV_OK) return s;
+    if ((s = take_workspace(&ws, parts + plan + 256, st)) != PARISKV_OK) return s;
     uint8_t* w = static_cast<uint8_t*>(ws);
     a.work = reinterpret_cast<float*>(w);
-    a.plan.pre = reinterpret_cast<int64_t*>(w + parts);
-    a.plan.seq = reinterpret_cast<int32_t*>(w + parts + pre);
-    a.plan.row = reinterpret_cast<int32_t*>(w + parts + pre + ids);
-    a.plan.ntiles = reinterpret_cast<int32_t*>(w + parts + pre + 2 * ids);
+    a.plan.tile = reinterpret_cast<Tile*>(w + parts);
+    a.plan.ntiles = reinterpret_cast<int32_t*>(w + parts + plan);
     a.plan.max_tiles = static_cast<int32_t>(tiles);
     cudaError_t e = launch_plan(a, st);
     if (e == cudaSuccess)

@@ -77,10 +77,19 @@ __device__ __forceinline__ SeqView seq_view(const Seqs& c, int shift, int s) {
 // of `heads * blocks` blocks which is cut into equal ranges, one per CTA, whatever the lengths
 // of the sequences are. A tile that a cut goes through is computed in parts (unnormalised
 // accumulators, maxima and sums in the workspace) which a second kernel joins in order.
+struct __align__(16) Tile {
+    int64_t pre;       // blocks of the tiles before this one (entry ntiles: of all)
+    int64_t pos0;      // position of the sequence's first new token
+    int32_t seq;
+    int32_t row0;      // its row in the per-token arrays
+    int32_t first;     // first row of the tile within the sequence (row = token * group + head)
+    int32_t nrow;      // rows of the tile
+    int32_t end;       // tokens [0, end) are all that its rows may see
+    int32_t kv;        // tokens of the sequence
+    int32_t pad[2];
+};
 struct Plan {
-    int64_t* pre;      // [max_tiles + 1] blocks before each tile
-    int32_t* seq;      // [max_tiles]
-    int32_t* row;      // [max_tiles] first row of the tile within its sequence
+    Tile* tile;        // [max_tiles + 1]
     int32_t* ntiles;   // [1]
     int32_t max_tiles;
 };
@@ -100,27 +109,26 @@ __device__ __forceinline__ int32_t tile_blocks(const SeqView& v, const PlanShape
     return max(1, static_cast<int32_t>(ceil_div(tile_end(v, p, row), p.block)));
 }
 
-// CTA c of n works on blocks [cut(c), cut(c + 1)) of `total`; cut_of is the CTA of a block.
-__host__ __device__ __forceinline__ int64_t cut(int64_t total, int64_t n, int64_t c) {
+// Of `ctas` CTAs, cuts(total, ctas) have work (one block each at least); CTA c of n works on blocks
+// [cut(c), cut(c + 1)) of `total`; cut_of is the CTA of a block.
+__device__ __forceinline__ int64_t cuts(int64_t total, int64_t ctas) { return min64(total, ctas); }
+__device__ __forceinline__ int64_t cut(int64_t total, int64_t n, int64_t c) {
     return total * c / n;
 }
-__host__ __device__ __forceinline__ int64_t cut_of(int64_t total, int64_t n, int64_t x) {
+__device__ __forceinline__ int64_t cut_of(int64_t total, int64_t n, int64_t x) {
     return ((x + 1) * n - 1) / total;
 }
 
-// Index of the last entry <= x of an ascending array of n entries with a[0] <= x, by a whole
-// warp: 32 probes a round.
-__device__ __forceinline__ int warp_search(const int64_t* a, int n, int64_t x) {
+// The last tile of n with pre <= x, by a whole warp: 32 probes a round.
+__device__ __forceinline__ int find_tile(const Tile* t, int n, int64_t x) {
     const int lane = threadIdx.x & 31;
     int lo = 0, len = n;
     while (len > 1) {
         const int step = (len + 31) / 32;
-        const int i = lo + lane * step;
-        const bool le = lane * step < len && a[i] <= x;
-        const int cnt = __popc(__ballot_sync(0xffffffffu, le));
-        lo += (cnt - 1) * step;
-        len = min(step, n - lo);
-        if (step == 1) break;
+        const bool le = lane * step < len && t[lo + lane * step].pre <= x;
+        const int end = lo + len;
+        lo += (__popc(__ballot_sync(0xffffffffu, le)) - 1) * step;
+        len = min(step, end - lo);
     }
     return lo;
 }

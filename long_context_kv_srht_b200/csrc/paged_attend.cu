@@ -112,26 +112,26 @@ attend_few_kernel(const AttendArgs a) {
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
+    pdl_wait();
+    pdl_launch_dependents();
     const int nt = *a.plan.ntiles;
-    const int64_t per_head = a.plan.pre[nt], total = per_head * a.heads;
-    if (total == 0) return;
-    const int64_t hi = cut(total, gridDim.x, blockIdx.x + 1);
-    int64_t x = cut(total, gridDim.x, blockIdx.x);
-    if (x >= hi) return;
+    const int64_t per_head = a.plan.tile[nt].pre, total = per_head * a.heads;
+    const int64_t ncut = cuts(total, gridDim.x);
+    if (blockIdx.x >= ncut) return;
+    const int64_t hi = cut(total, ncut, blockIdx.x + 1);
+    int64_t x = cut(total, ncut, blockIdx.x);
     int64_t h = x / per_head;
-    int tile = warp_search(a.plan.pre, nt, x - h * per_head);
+    int tile = find_tile(a.plan.tile, nt, x - h * per_head);
     const int G = a.shape.group, shift = a.pool.shift;
     const float qs = a.scale * kLog2e;
 
     while (x < hi) {
-        const int64_t start = h * per_head + a.plan.pre[tile];
-        const int64_t nb = a.plan.pre[tile + 1] - a.plan.pre[tile];
+        const Tile v = a.plan.tile[tile];
+        const int64_t start = h * per_head + v.pre;
+        const int64_t nb = a.plan.tile[tile + 1].pre - v.pre;
         const int b0 = static_cast<int>(x - start);
         const int b1 = static_cast<int>(min64(nb, hi - start));
-        const int s = a.plan.seq[tile], first = a.plan.row[tile];
-        const SeqView v = seq_view(a.seqs, shift, s);
-        const int end = tile_end(v, a.shape, first);
-        const int nrow = static_cast<int>(min64(R, static_cast<int64_t>(v.rows) * G - first));
+        const int s = v.seq, first = v.first, end = v.end, nrow = v.nrow;
         const int32_t* table = a.seqs.table + static_cast<int64_t>(s) * a.seqs.stride;
         // the last token a row may attend
         auto limit = [&](int r) -> int {

@@ -209,29 +209,30 @@ __device__ void load_role(const AttendArgs& a, const CUtensorMap* mq, const CUte
     const int rs = min(shift, 7), run = 1 << rs, nrun = kBlk >> rs;  // tokens a copy, copies a block
     const int ns = 7 - rs;                                     // log2(nrun)
     int64_t h = x / per_head;
-    int tile = warp_search(a.plan.pre, nt, x - h * per_head);
+    int tile = find_tile(a.plan.tile, nt, x - h * per_head);
+    Tile v = a.plan.tile[tile];
     uint32_t n = 0, seg = 0, ld = 0, nq = 0;   // entries, segments, tiles loaded, Q tiles loaded
     volatile int32_t* ab = &sh.abort;
 
     while (x < hi) {
-        const int64_t start = h * per_head + a.plan.pre[tile];
-        const int64_t nb = a.plan.pre[tile + 1] - a.plan.pre[tile];
+        // the next tile's record is under way while this one is worked on
+        const int64_t after = a.plan.tile[tile + 1].pre;
+        const int next = tile + 1 == nt ? 0 : tile + 1;
+        const Tile ahead = a.plan.tile[next];
+        const int64_t start = h * per_head + v.pre, nb = after - v.pre;
         const int b0 = static_cast<int>(x - start), b1 = static_cast<int>(min64(nb, hi - start));
-        const int s = a.plan.seq[tile];
-        const SeqView v = seq_view(a.seqs, shift, s);
         Seg g;
-        g.first = a.plan.row[tile];
+        g.first = v.first;
         g.pos0 = v.pos0;
         g.row0 = v.row0;
-        g.nrow = static_cast<int>(min64(a.shape.tile_rows,
-                                        static_cast<int64_t>(v.rows) * G - g.first));
+        g.nrow = v.nrow;
         g.head = static_cast<int>(h);
         g.kv = v.kv;
         g.whole = b0 == 0 && b1 == nb;
         g.part = 2 * static_cast<int>(blockIdx.x) + (b0 == 0);
         g.shared = row_limit(g, causal, G, 0);
-        const int end = tile_end(v, a.shape, g.first);
-        const int32_t* table = a.seqs.table + static_cast<int64_t>(s) * a.seqs.stride;
+        const int end = v.end;
+        const int32_t* table = a.seqs.table + static_cast<int64_t>(v.seq) * a.seqs.stride;
 
         // page ids come 32 at a time, a lane a run, one window ahead
         const int per_win = 32 >> ns;                   // blocks of a window
@@ -348,10 +349,9 @@ __device__ void load_role(const AttendArgs& a, const CUtensorMap* mq, const CUte
         }
         ++seg;
         x = start + b1;
-        if (b1 == nb && ++tile == nt) {
-            tile = 0;
-            ++h;
-        }
+        h += next == 0 ? 1 : 0;   // (a range that ends inside the tile is the last)
+        tile = next;
+        v = ahead;
     }
     // the end: an entry without a segment
     const int slot = n % kRing;
@@ -803,39 +803,53 @@ __device__ void aux_role(const AttendArgs& a, Shared& sh, uint8_t* smem) {
                 const int st = (use + 1) % S::kStages;
                 if (flags & kFix) {
                     if (!warp_wait(&sh.kv_full[st], ((use + 1) / S::kStages) & 1, ab)) return;
-                    for (int row = tid; row < kBlk; row += kT) {
-                        const int tok = block * kBlk + row;
-                        const bool there = sh.entry[slot].mask[row >> 5] >> (row & 31) & 1;
-                        if (there && tok <= shared) continue;
-                        for (int i = 0; i < 16; ++i) {
-                            const int ch = (i + row) & 7;     // piece as stored
-                            uint4* p = reinterpret_cast<uint4*>(
-                                smem + S::kKV + st * kStageB + (i >> 3) * kHalfB + row * 128 +
-                                (ch << 4));
-                            if (!there) {
-                                *p = make_uint4(0, 0, 0, 0);
+                    // rows from the first one that needs a look: all past `shared`, and all of a
+                    // block that is not whole; a warp takes 4 rows of 64 columns at a time, 4
+                    // such pieces in flight
+                    bool full = true;
+                    for (int f = 0; f < 4; ++f) full = full && sh.entry[slot].mask[f] == ~0u;
+                    const int row0 = full ? max(0, shared + 1 - block * kBlk) & ~3 : 0;
+                    uint8_t* tile = smem + S::kKV + st * kStageB;
+                    const int warp = tid >> 5, npc = 2 * (kBlk - row0) / 4;
+                    for (int pc = warp; pc < npc; pc += 4 * S::kAuxWarps) {
+                        uint4 v[4];
+                        uint4* at[4];
+                        int tok[4], d[4];
+                        bool there[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int p = pc + u * S::kAuxWarps;
+                            const int half = p & 1, row = row0 + 4 * (p >> 1) + (lane >> 3);
+                            const bool in = p < npc;
+                            at[u] = reinterpret_cast<uint4*>(tile + half * kHalfB +
+                                                             (in ? row : 0) * 128 + (lane & 7) * 16);
+                            tok[u] = in ? block * kBlk + row : -1;
+                            d[u] = half * 64 + ((lane & 7) ^ (row & 7)) * 8;
+                            there[u] = !in || (sh.entry[slot].mask[row >> 5] >> (row & 31) & 1);
+                            v[u] = *at[u];
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            if (!there[u]) {
+                                *at[u] = make_uint4(0, 0, 0, 0);
                                 continue;
                             }
-                            const uint4 v = *p;
-                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                            bool odd = false;
+                            // an exponent of all ones carries into the (cleared) sign bit
+                            uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w}, odd = 0;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                odd = odd || (w[k] & 0x7f80u) == 0x7f80u ||
-                                      (w[k] & 0x7f800000u) == 0x7f800000u;
-                            if (!odd) continue;
-                            const int d = (i >> 3) * 64 + (ch ^ (row & 7)) * 8;
+                            for (int k = 0; k < 4; ++k) odd |= (w[k] & 0x7f807f80u) + 0x00800080u;
+                            if (!(odd & 0x80008000u) || tok[u] <= shared) continue;
                             for (int k = 0; k < 4; ++k) {
                                 if ((w[k] & 0x7f80u) == 0x7f80u) {
-                                    mark(d + 2 * k, tok);
+                                    mark(d[u] + 2 * k, tok[u]);
                                     w[k] &= 0xffff0000u;
                                 }
                                 if ((w[k] & 0x7f800000u) == 0x7f800000u) {
-                                    mark(d + 2 * k + 1, tok);
+                                    mark(d[u] + 2 * k + 1, tok[u]);
                                     w[k] &= 0xffffu;
                                 }
                             }
-                            *p = make_uint4(w[0], w[1], w[2], w[3]);
+                            *at[u] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
                     fence_async_smem();
@@ -864,12 +878,6 @@ attend_chunk_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap mq,
     __shared__ __align__(16) Shared sh;
     uint8_t* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
     const int warp = threadIdx.x >> 5;
-    const int nt = *a.plan.ntiles;
-    const int64_t per_head = a.plan.pre[nt], total = per_head * a.heads;
-    if (total == 0) return;
-    const int64_t x = cut(total, gridDim.x, blockIdx.x), hi = cut(total, gridDim.x, blockIdx.x + 1);
-    if (x >= hi) return;
-
     if (threadIdx.x == 0) {
         sh.abort = 0;
         auto init = [&](uint64_t* b, uint32_t count) { mbar_init(smem_addr(b), count); };
@@ -906,12 +914,23 @@ attend_chunk_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap mq,
         tmem_alloc(smem_addr(&sh.tmem), 512);
         tmem_relinquish();
     }
+    // (everything up to here needs nothing of the plan)
+    pdl_wait();
+    pdl_launch_dependents();
+    const int nt = *a.plan.ntiles;
+    const int64_t per_head = a.plan.tile[nt].pre, total = per_head * a.heads;
+    const int64_t ncut = cuts(total, gridDim.x);
+    const bool work = blockIdx.x < ncut;
+    const int64_t x = work ? cut(total, ncut, blockIdx.x) : 0;
+    const int64_t hi = work ? cut(total, ncut, blockIdx.x + 1) : 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
 
-    if (warp < 8) {
+    if (!work) {
+        // nothing to do but to give the tensor memory back
+    } else if (warp < 8) {
         if (warp < 4 * S::kHalves) softmax_role<kE4m3, kParts, Out>(a, sh, tmem, warp >> 2);
     } else if (warp == 8) {
         load_role<kE4m3, kParts>(a, &mq, &mk, &mv, sh, smem, x, hi, per_head, nt);
@@ -950,8 +969,8 @@ cudaError_t launch_chunk(const AttendArgs& a, const CUtensorMap maps[3], int cta
     auto kernel = attend_chunk_kernel<kE4m3, kParts, Out>;
     const cudaError_t e = raise_smem_limit(kernel, S::kSmem, done);
     if (e != cudaSuccess) return e;
-    kernel<<<ctas, S::kThreads, S::kSmem, st>>>(a, maps[0], maps[1], maps[2]);
-    return cudaGetLastError();
+    return launch_pdl(kernel, dim3(ctas), dim3(S::kThreads), S::kSmem, st, a, maps[0], maps[1],
+                      maps[2]);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
