@@ -599,9 +599,10 @@ pariskv_status pariskv_paged_attend(const pariskv_config* cfg, const pariskv_pag
     // up to one tile of the streaming kernel a sequence: it reads each K/V row once
     const int64_t most = static_cast<int64_t>(chunk->max_q) * cfg->group;
     const bool few = most <= kFewRows;
-    a.shape.tile_rows = few ? kFewRows : chunk_tile_rows(cfg->group, f32);
+    a.shape.tile_rows = few ? (most <= 8 ? 8 : kFewRows) : chunk_tile_rows(cfg->group, f32);
     a.shape.block = few ? kFewBlock : kChunkBlock;
-    const int ctas = few ? few_ctas(sms) : sms;
+    const int ctas = few ? few_ctas(sms, pages->format, a.shape.tile_rows) : sms;
+    const bool plan_first = !few || !few_plans_inline(cfg->batch);
     a.inject_wait = !few && g_inject_wait.exchange(0);
     // tiles: every sequence may end in a part of one
     const int64_t tiles = min64(cfg->batch * ceil_div(most, a.shape.tile_rows),
@@ -617,22 +618,24 @@ pariskv_status pariskv_paged_attend(const pariskv_config* cfg, const pariskv_pag
     a.plan.tile = reinterpret_cast<Tile*>(w + parts);
     a.plan.ntiles = reinterpret_cast<int32_t*>(w + parts + plan);
     a.plan.max_tiles = static_cast<int32_t>(tiles);
-    cudaError_t e = launch_plan(a, st);
+    cudaError_t e = plan_first ? launch_plan(a, st) : cudaSuccess;
     if (e == cudaSuccess)
         e = few ? launch_attend_few(a, pages->format, f32, ctas, st)
                 : launch_attend_chunk(a, pages->format, f32, ctas, st);
     if (e == cudaSuccess) e = launch_join(a, ctas, f32, st);
     cudaFreeAsync(ws, st);
     if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
-    set_last_launches(3);
+    set_last_launches(plan_first ? 3 : 2);
     return PARISKV_OK;
 }
 
 pariskv_status pariskv_paged_sync(void* stream) {
     int status = ST_OK;
-    const cudaError_t e = take_chunk_status(&status, static_cast<cudaStream_t>(stream));
+    int other = ST_OK;
+    cudaError_t e = take_chunk_status(&status, static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) e = take_few_status(&other, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "paged attention");
-    if (status == ST_TIMEOUT)
+    if (status == ST_TIMEOUT || other == ST_TIMEOUT)
         return fail(PARISKV_ETIMEOUT, "a bounded device-side wait of the paged attention expired");
     return PARISKV_OK;
 }

@@ -158,12 +158,14 @@ struct AttendArgs {
 // paged.cu
 cudaError_t launch_plan(const AttendArgs& a, cudaStream_t st);
 cudaError_t launch_join(const AttendArgs& a, int ctas, bool f32_out, cudaStream_t st);
-// paged_attend.cu: few rows a sequence (mma.sync, K/V streamed once)
-constexpr int kFewBlock = 64;
-constexpr int kFewRows = 16;    // rows of a tile
-int few_ctas(int sms);
+// paged_attend.cu: up to kFewRows rows a sequence (mma.sync, K/V streamed once), in tiles of 8 or
+// 16. It plans for itself where few_plans_inline says so (no launch_plan then).
+constexpr int kFewBlock = 64, kFewRows = 16;
+int few_ctas(int sms, int format, int tile_rows);
+bool few_plans_inline(int batch);
 cudaError_t launch_attend_few(const AttendArgs& a, int format, bool f32_out, int ctas,
                               cudaStream_t st);
+cudaError_t take_few_status(int* status, cudaStream_t st);     // read and clear
 // paged_chunk.cu: many rows a sequence (tcgen05); one CTA an SM
 constexpr int kChunkBlock = 128;
 int chunk_tile_rows(int group, bool f32_out);

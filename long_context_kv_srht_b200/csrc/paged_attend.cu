@@ -3,25 +3,26 @@
 //     o_r = sum_t softmax_t(scale * <q_r, K_t>) V_t,   rows r = (token, head of the group).
 //
 // With a handful of rows the call is a stream over the K and V rows (512 bytes a token and KV
-// head in bf16, 258 in 8 bits), bound by HBM; the aim is to read each of them once and to spend
-// few instructions a token:
-//  - all rows of a tile (up to 16: tokens x heads of the KV head's group) share one pass over
-//    K and V;
+// head in bf16, 258 in 8 bits), bound by HBM; the aim is to read each of them once, to keep enough
+// copies under way, and to spend few instructions a token:
+//  - all rows of a tile (up to 8 or 16: tokens x heads of the KV head's group) share one pass
+//    over K and V;
 //  - the (head, sequence) streams of a batch form one axis of 64-token blocks that is cut into
-//    equal ranges, two CTAs an SM, so ragged lengths leave no SM idle (see Plan);
-//  - blocks are staged by a cp.async ring (16-byte copies; page ids ride in the same ring ahead
-//    of the rows that need them), rows that are not there are zero-filled and masked;
-//  - both products run on mma.sync (m16n8k16, bf16, fp32 accumulators), each warp taking 16
-//    tokens of a block: S^T = K Q^T and O^T += V^T P^T, so a lane's softmax state and its
-//    accumulators belong to the same two rows of each 8-row group;
+//    equal ranges, two or three CTAs an SM, so ragged lengths leave no SM idle (see Plan);
+//  - one warp walks the range and brings the pages by TMA into rings of K and of V tiles, across
+//    the ends of sequences; four warps take 16 tokens of a block each, held together by mbarriers
+//    only (no barrier of the CTA in the loop);
+//  - both products run on mma.sync (m16n8k16, bf16, fp32 accumulators): S^T = K Q^T and O^T +=
+//    V^T P^T, so a lane's softmax state and its accumulators belong to the same two rows of each
+//    8-row group. K and V are read once, so tcgen05 tiles of 128 rows would be 1/16 full;
 //  - bf16 rows come as fragments by ldmatrix. 8-bit rows are widened in registers: which element
-//    of the head dimension stands at which position of a fragment is free as long as both
-//    factors agree, so a lane reads 16 consecutive codes and uses them for four MMAs;
+//    of the head dimension, and which token, stands at which position of a fragment is free as
+//    long as both factors agree, so a lane reads 16 consecutive codes and uses them for four MMAs;
 //  - the 8-bit rows' scales are powers of two and multiply the scores (K) and the weights (V);
 //  - P enters the second product as two bf16 parts (16 bits), or three (24) for fp32 output;
-//  - base-2 online softmax over 16-token blocks per warp; the four warps merge at the end of a
-//    range.
-#include "paged.cuh"
+//  - a row's maximum is only brought up to date (three shuffles, O rescaled) when a score exceeds
+//    it by more than 2^8; sums stay per lane until the end of a range, where the warps merge.
+#include "paged_async.cuh"
 
 namespace pkv {
 
@@ -29,17 +30,39 @@ namespace {
 
 constexpr int kFW = 4;                        // warps, 16 tokens of a block each
 static_assert(kFewBlock == 16 * kFW, "a warp takes 16 tokens of a block");
-constexpr int kIdRing = 16;                   // blocks whose page ids are held
-constexpr int kRuns = kFewBlock / 16;         // page ids a block: 16 tokens lie in one page
+constexpr int kInline = 256;                  // sequences that every CTA plans for itself
+constexpr int kSegs = 8;                      // segment records between the loads and the others
+constexpr float kGrow = 8.0f;                 // growth of a maximum (base 2) that rescales O
 
 template <bool kE4m3> struct FewShape {
     static constexpr int kRowB = kE4m3 ? D : 2 * D;          // bytes of a row
-    static constexpr int kStages = kE4m3 ? 6 : 3;            // 96 KB either way: 2 CTAs an SM
-    static constexpr int kTensor = kFewBlock * kRowB;
-    static constexpr int kStage = 2 * kTensor + (kE4m3 ? 2 * kFewBlock : 0);
-    static constexpr int kSmem = kStages * kStage;
+    static constexpr int kTile = kFewBlock * kRowB;          // a K or V tile: 16 or 8 KB
+    static constexpr int kNK = 3, kNV = kE4m3 ? 3 : 2;
+    static constexpr int kScales = (kNK + kNV) * kTile;      // 64 scale bytes a tile (8-bit)
+    static constexpr int kScratch = kScales + (kE4m3 ? (kNK + kNV) * kFewBlock : 0);
+    static constexpr int kPart = D + 4;                      // a row's partial in the scratch
+    static constexpr int kSmem = kScratch + kFW * 8 * kPart * 4 + 1024;   // + alignment
 };
-static_assert(2 * FewShape<true>::kStages - 1 <= kIdRing, "ids of loaded and computed blocks");
+static_assert(FewShape<true>::kNK < kSegs, "a record outlives the entries behind it");
+
+enum : int { kFirst = 1, kLast = 2, kEnd = 4 };
+struct Meta {
+    int32_t block, flags;
+    uint32_t runs;         // 16-token runs that hold something a row may see
+};
+struct Seg {
+    int64_t pos0;
+    int32_t row0, first, nrow, head, end, kv, whole, part;
+};
+struct Control {
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], met;
+    Meta meta[4];
+    Seg seg[kSegs];
+    int64_t pre[kInline + 1];
+    int64_t warp_sum[8];
+    int32_t bad[2][D];     // first token whose V is not finite in this element, by segment
+    int32_t abort;
+};
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t r[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -89,310 +112,484 @@ __device__ __forceinline__ uint32_t widen2(uint32_t r) {
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                 :: "r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+// The last of n + 1 sums with pre[i] <= x.
+__device__ __forceinline__ int find_pre(const int64_t* pre, int n, int64_t x) {
+    int lo = 0, len = n;
+    while (len > 1) {
+        const int half = len >> 1;
+        if (pre[lo + half] <= x) {
+            lo += half;
+            len -= half;
+        } else {
+            len = half;
+        }
+    }
+    return lo;
 }
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
+
+// Where a CTA's range lies. Up to kInline sequences (a tile each, the host sees to that) are
+// planned here, by every CTA for itself; CTA 0 leaves the records that the join reads.
+struct Range {
+    int64_t x, hi, per_head;
+    int32_t nt;
+    bool inline_plan;
+};
+
+__device__ __forceinline__ Tile tile_record(const AttendArgs& a, int s, int64_t pre) {
+    const SeqView v = seq_view(a.seqs, a.pool.shift, s);
+    Tile t;
+    t.pre = pre;
+    t.pos0 = v.pos0;
+    t.seq = s;
+    t.row0 = v.row0;
+    t.first = 0;
+    t.nrow = static_cast<int32_t>(min64(a.shape.tile_rows, static_cast<int64_t>(v.rows) * a.shape.group));
+    t.end = tile_end(v, a.shape, 0);
+    t.kv = v.kv;
+    t.pad[0] = t.pad[1] = 0;
+    return t;
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+__device__ __forceinline__ Range make_range(const AttendArgs& a, Control& c, bool inline_plan) {
+    Range r;
+    r.inline_plan = inline_plan;
+    if (inline_plan) {
+        r.nt = a.seqs.batch;
+        // a thread sums up consecutive sequences, then the threads' sums are scanned
+        constexpr int kT = (kFW + 1) * 32;
+        const int per = (r.nt + kT - 1) / kT, s0 = threadIdx.x * per;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        int64_t sum = 0;
+        for (int i = 0; i < per && s0 + i < r.nt; ++i) {
+            const SeqView v = seq_view(a.seqs, a.pool.shift, s0 + i);
+            c.pre[s0 + i] = sum;
+            sum += v.rows > 0 ? tile_blocks(v, a.shape, 0) : 0;
+        }
+        int64_t scan = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, scan, o);
+            if (lane >= o) scan += y;
+        }
+        if (lane == 31) c.warp_sum[warp] = scan;
+        __syncthreads();
+        int64_t before = scan - sum, all = 0;
+        for (int w = 0; w <= kFW; ++w) {
+            if (w < warp) before += c.warp_sum[w];
+            all += c.warp_sum[w];
+        }
+        for (int i = 0; i < per && s0 + i < r.nt; ++i) {
+            c.pre[s0 + i] += before;
+            if (blockIdx.x == 0) a.plan.tile[s0 + i] = tile_record(a, s0 + i, c.pre[s0 + i]);
+        }
+        if (threadIdx.x == 0) {
+            c.pre[r.nt] = all;
+            if (blockIdx.x == 0) {
+                a.plan.tile[r.nt].pre = all;
+                *a.plan.ntiles = r.nt;
+            }
+        }
+        r.per_head = all;
+        __syncthreads();
+    } else {
+        r.nt = *a.plan.ntiles;
+        r.per_head = a.plan.tile[r.nt].pre;
+    }
+    const int64_t total = r.per_head * a.heads, n = cuts(total, gridDim.x);
+    const bool work = blockIdx.x < n;
+    r.x = work ? cut(total, n, blockIdx.x) : 0;
+    r.hi = work ? cut(total, n, blockIdx.x + 1) : 0;
+    return r;
+}
+
+// ---------------------------------------------------------------------------------- loads
+template <bool kE4m3>
+__device__ void few_loads(const AttendArgs& a, const CUtensorMap* mk, const CUtensorMap* mv,
+                          Control& c, uint8_t* smem, const Range& range) {
+    using S = FewShape<kE4m3>;
+    const int lane = threadIdx.x & 31, shift = a.pool.shift;
+    const int rs = min(shift, 6), run = 1 << rs, ns = 6 - rs, nrun = 1 << ns;
+    const int per_win = 32 >> ns;
+    volatile int32_t* ab = &c.abort;
+    int64_t x = range.x, h = 0;
+    uint32_t n = 0, seg = 0;
+    int tile = 0;
+    if (x < range.hi) {
+        h = x / range.per_head;
+        const int64_t rest = x - h * range.per_head;
+        tile = range.inline_plan ? find_pre(c.pre, range.nt, rest)
+                                 : find_tile(a.plan.tile, range.nt, rest);
+    }
+    while (x < range.hi) {
+        const Tile t = range.inline_plan ? tile_record(a, tile, c.pre[tile]) : a.plan.tile[tile];
+        const int64_t nb = (range.inline_plan ? c.pre[tile + 1] : a.plan.tile[tile + 1].pre) - t.pre;
+        const int64_t start = h * range.per_head + t.pre;
+        const int b0 = static_cast<int>(x - start);
+        const int b1 = static_cast<int>(min64(nb, range.hi - start));
+        const int32_t* table = a.seqs.table + static_cast<int64_t>(t.seq) * a.seqs.stride;
+        // page ids come 32 at a time, a lane a run, one window ahead
+        auto fetch = [&](int w) -> int {
+            const int tok = w * kFewBlock + lane * run;
+            return w + (lane >> ns) < b1 && tok < t.end ? table[tok >> shift] : -1;
+        };
+        int win = b0, id = fetch(b0), id_next = fetch(b0 + per_win);
+        uint32_t valid = 0;
+        int page = 0;
+        // the next block with a page that is there, from b on
+        auto live = [&](int b) -> int {
+            for (; b < b1; ++b) {
+                if (b >= win + per_win) {
+                    win += per_win;
+                    id = id_next;
+                    id_next = fetch(win + per_win);
+                }
+                const uint32_t ok = __ballot_sync(
+                    0xffffffffu, static_cast<uint32_t>(id) < static_cast<uint32_t>(a.pool.num_pages));
+                const int at = (b - win) << ns;
+                valid = (ok >> at) & ((1u << nrun) - 1);
+                page = __shfl_sync(0xffffffffu, id, (at + lane) & 31);
+                if (valid) return b;
+            }
+            valid = 0;
+            return -1;
+        };
+        bool first = true;
+        int b = live(b0);
+        while (first || b >= 0) {
+            const uint32_t cur_valid = valid;
+            const int cur_page = page, cur = b;
+            if (b >= 0) b = live(b + 1);
+            const int ks = n % S::kNK, vs = n % S::kNV;
+            const bool mine = lane < nrun && (cur_valid >> lane & 1);
+            const int tok = cur * kFewBlock + lane * run;
+            const int row = (static_cast<int>(h) << shift) + (tok & ((1 << shift) - 1));
+            if (!warp_wait(&c.k_empty[ks], ((n / S::kNK) & 1) ^ 1, ab)) return;
+            const uint32_t bytes = __popc(cur_valid) * run * (kE4m3 ? D + 1 : 2 * D);
+            if (lane == 0) {
+                if (first) {
+                    Seg g;
+                    g.pos0 = t.pos0;
+                    g.row0 = t.row0;
+                    g.first = t.first;
+                    g.nrow = t.nrow;
+                    g.head = static_cast<int>(h);
+                    g.end = t.end;
+                    g.kv = t.kv;
+                    g.whole = b0 == 0 && b1 == nb;
+                    g.part = 2 * static_cast<int>(blockIdx.x) + (b0 == 0);
+                    c.seg[seg % kSegs] = g;
+                }
+                Meta m;
+                m.block = cur;
+                m.flags = (first ? kFirst : 0) | (b < 0 ? kLast : 0);
+                m.runs = 0;
+                for (int i = 0; i < kFW; ++i)
+                    if ((cur_valid >> (16 * i >> rs) & 1) && cur * kFewBlock + 16 * i < t.end)
+                        m.runs |= 1u << i;
+                c.meta[ks] = m;
+                mbar_arrive_expect_tx(smem_addr(&c.k_full[ks]), bytes);
+            }
+            __syncwarp();
+            auto bring = [&](int slot, int of, uint64_t* bar) {
+                uint8_t* dst = smem + slot * S::kTile + lane * run * 128;
+                const CUtensorMap* m = of ? mv : mk;
+                tma_load3(smem_addr(dst), m, 0, row, cur_page, smem_addr(bar));
+                if (kE4m3)
+                    bulk_g2s(smem_addr(smem + S::kScales + slot * kFewBlock + lane * run),
+                             (of ? a.pool.vs : a.pool.ks) + cur_page * a.pool.scale_stride + row,
+                             run, smem_addr(bar));
+                else
+                    tma_load3(smem_addr(dst + S::kTile / 2), m, 64, row, cur_page, smem_addr(bar));
+            };
+            if (mine) bring(ks, 0, &c.k_full[ks]);
+            if (!warp_wait(&c.v_empty[vs], ((n / S::kNV) & 1) ^ 1, ab)) return;
+            if (lane == 0) mbar_arrive_expect_tx(smem_addr(&c.v_full[vs]), bytes);
+            __syncwarp();
+            if (mine) bring(S::kNK + vs, 1, &c.v_full[vs]);
+            first = false;
+            ++n;
+        }
+        ++seg;
+        x = start + b1;
+        if (b1 == nb) {
+            // (sequences without rows have no blocks)
+            do {
+                if (++tile == range.nt) {
+                    tile = 0;
+                    ++h;
+                }
+            } while (range.inline_plan && x < range.hi && c.pre[tile + 1] == c.pre[tile]);
+        }
+    }
+    const int ks = n % S::kNK;
+    if (!warp_wait(&c.k_empty[ks], ((n / S::kNK) & 1) ^ 1, ab)) return;
+    if (lane == 0) {
+        c.meta[ks].flags = kEnd;
+        arrive(&c.k_full[ks]);
+    }
+}
 
 // NT groups of 8 rows; kParts bf16 parts of P.
 template <bool kE4m3, int NT, int kParts, typename Out>
-__global__ void __launch_bounds__(kFW * 32, 2)
-attend_few_kernel(const AttendArgs a) {
+__device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
     using S = FewShape<kE4m3>;
-    constexpr int R = 8 * NT;
-    constexpr int kPart = D + 4;     // a row's partial in the merge scratch
-    static_assert(kFW * R * kPart * 4 <= S::kSmem, "the merge scratch fits in the stages");
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int32_t s_page[kIdRing][kRuns];
-    __shared__ int32_t s_bad[D];     // first token whose V is not finite in this element
-
+    constexpr int R = 8 * NT, kPart = S::kPart;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int g = lane >> 2, t = lane & 3;
-    pdl_wait();
-    pdl_launch_dependents();
-    const int nt = *a.plan.ntiles;
-    const int64_t per_head = a.plan.tile[nt].pre, total = per_head * a.heads;
-    const int64_t ncut = cuts(total, gridDim.x);
-    if (blockIdx.x >= ncut) return;
-    const int64_t hi = cut(total, ncut, blockIdx.x + 1);
-    int64_t x = cut(total, ncut, blockIdx.x);
-    int64_t h = x / per_head;
-    int tile = find_tile(a.plan.tile, nt, x - h * per_head);
-    const int G = a.shape.group, shift = a.pool.shift;
+    const int g = lane >> 2, t = lane & 3, mi = lane >> 3, j8 = lane & 7;
+    // the token of a lane's first row of S (the second is 8 on), and the 16-byte piece of a V row
+    // that it reads: orders in which 8 lanes' reads of swizzled 8-bit rows meet no bank twice
+    const int pg = kE4m3 ? (g >> 1) | (g & 1) << 2 : g;
+    const int G = a.shape.group;
     const float qs = a.scale * kLog2e;
+    volatile int32_t* ab = &c.abort;
+    float* scr = reinterpret_cast<float*>(smem + S::kScratch);
 
-    while (x < hi) {
-        const Tile v = a.plan.tile[tile];
-        const int64_t start = h * per_head + v.pre;
-        const int64_t nb = a.plan.tile[tile + 1].pre - v.pre;
-        const int b0 = static_cast<int>(x - start);
-        const int b1 = static_cast<int>(min64(nb, hi - start));
-        const int s = v.seq, first = v.first, end = v.end, nrow = v.nrow;
-        const int32_t* table = a.seqs.table + static_cast<int64_t>(s) * a.seqs.stride;
-        // the last token a row may attend
-        auto limit = [&](int r) -> int {
-            if (r >= nrow) return -1;
-            const int64_t lim = a.shape.causal ? v.pos0 + (first + r) / G : v.kv - 1;
-            return static_cast<int>(max64(-1, min64(lim, v.kv - 1)));
-        };
-        // tokens past this one (and before `end`) are seen by some rows of the tile and not by
-        // others
-        const int shared = limit(0);
-
-        s_bad[tid] = INT32_MAX;
-        // page ids of block b, run i: -1 where the run holds nothing that is attended
-        auto id_source = [&](int b, int i, const int32_t** src) -> bool {
-            const int tok = b * kFewBlock + 16 * i;
-            *src = table + (tok >> shift);
-            return b < b1 && tok < end;
-        };
-        if (tid < (S::kStages - 1) * kRuns) {
-            const int b = b0 + tid / kRuns, i = tid % kRuns;
-            const int32_t* src;
-            s_page[b % kIdRing][i] = id_source(b, i, &src) ? *src : -1;
-        }
-        __syncthreads();
-
-        auto load_ids = [&](int b) {
-            if (tid < kRuns) {
-                const int32_t* src;
-                int32_t* dst = &s_page[b % kIdRing][tid];
-                if (id_source(b, tid, &src))
-                    cp4(smem_addr(dst), src);
-                else
-                    *dst = -1;
-            }
-        };
-        auto load_block = [&](int b, int stage) {
-            uint8_t* st = smem + stage * S::kStage;
-            constexpr int kChunks = S::kRowB / 16;
-            constexpr int kLoads = 2 * kFewBlock * kChunks / (kFW * 32);
-            constexpr int kRowsPass = kFW * 32 / kChunks;
-            const int c = tid % kChunks;
+    uint32_t n = 0, seg = 0, nm = 0;      // entries, segments, meetings
+    Seg sg = {};
+    uint32_t qb[NT][8][2];
+    int lim[NT][2], shared = 0;
+    float mx[NT][2], den[NT][2], o[NT][8][4];
+    // the last token a row may attend
+    auto limit = [&](int r) -> int {
+        if (r >= sg.nrow) return -1;
+        const int64_t l = a.shape.causal ? sg.pos0 + (sg.first + r) / G : sg.kv - 1;
+        return static_cast<int>(max64(-1, min64(l, sg.kv - 1)));
+    };
+    auto meet = [&]() -> bool {           // of the four warps
+        __syncwarp();
+        if (lane == 0) arrive(&c.met);
+        return warp_wait(&c.met, nm++ & 1, ab);
+    };
+#pragma unroll 1
+    while (true) {
+        const int ks = n % S::kNK, vs = n % S::kNV;
+        if (!warp_wait(&c.k_full[ks], (n / S::kNK) & 1, ab)) return;
+        const Meta m = c.meta[ks];
+        if (m.flags & kEnd) return;
+        if (m.flags & kFirst) {
+            sg = c.seg[seg % kSegs];
+            shared = limit(0);
+            // B fragments of Q^T: row 8 j + g of the tile; with 8-bit pages, position k of MMA m
+            // is element 64 (m / 4) + 16 t + 4 (m % 4) + ... of the row, as the K codes are read
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                const int id = tid / kChunks + kRowsPass * j;
-                const int is_v = id / kFewBlock, row = id % kFewBlock;
-                const int tok = b * kFewBlock + row;
-                const int32_t page = s_page[b % kIdRing][row >> 4];
-                const bool ok = tok < end && static_cast<uint32_t>(page) <
-                                                 static_cast<uint32_t>(a.pool.num_pages);
-                const int64_t slot = (h << shift) + (tok & ((1 << shift) - 1));
-                const uint8_t* src = (is_v ? a.pool.v : a.pool.k) +
-                                     (ok ? page * a.pool.page_bytes + slot * S::kRowB : 0) + c * 16;
-                // 16-byte pieces of a row change places so that the fragment reads below hit
-                // different banks
-                const int sw = !kE4m3 ? (row & 7) : is_v ? ((row >> 1) & 3) << 1 : (row & 1) << 2;
-                cp16(smem_addr(st + is_v * S::kTensor + row * S::kRowB + ((c ^ sw) << 4)), src, ok);
-            }
-            if (kE4m3 && tid < 2 * kRuns) {
-                const int is_v = tid / kRuns, i = tid % kRuns;
-                const int tok = b * kFewBlock + 16 * i;
-                const int32_t page = s_page[b % kIdRing][i];
-                const bool ok = tok < end && static_cast<uint32_t>(page) <
-                                                 static_cast<uint32_t>(a.pool.num_pages);
-                const int64_t slot = (h << shift) + (tok & ((1 << shift) - 1));
-                const uint8_t* src = (is_v ? a.pool.vs : a.pool.ks) +
-                                     (ok ? page * a.pool.scale_stride + slot : 0);
-                cp16(smem_addr(st + 2 * S::kTensor + is_v * kFewBlock + 16 * i), src, ok);
-            }
-        };
+            for (int j = 0; j < NT; ++j) {
+                const int r = 8 * j + g;
+                const bool ok = r < sg.nrow;
+                const int rr = sg.first + (ok ? r : 0);
+                const uint32_t* qr = reinterpret_cast<const uint32_t*>(
+                    a.q + (sg.row0 + rr / G) * a.q_ld + (static_cast<int64_t>(sg.head) * G + rr % G) * D);
 #pragma unroll
-        for (int i = 0; i < S::kStages - 1; ++i) {
-            if (b0 + i < b1) load_block(b0 + i, i);
-            load_ids(b0 + i + S::kStages - 1);
-            cp_commit();
-        }
-
-        // B fragments of Q^T: row 8 j + g of the tile; with 8-bit pages, position k of MMA m is
-        // element 64 (m / 4) + 16 t + 4 (m % 4) + ... of the row, as the K codes are read below
-        uint32_t qb[NT][8][2];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int r = 8 * j + g;
-            const bool ok = r < nrow;
-            const int rr = first + (ok ? r : 0);
-            const uint32_t* qr = reinterpret_cast<const uint32_t*>(
-                a.q + (v.row0 + rr / G) * a.q_ld + (h * G + rr % G) * D);
-#pragma unroll
-            for (int m = 0; m < 8; ++m) {
-                const int i0 = kE4m3 ? 32 * (m >> 2) + 8 * t + 2 * (m & 3) : 8 * m + t;
-                const int i1 = kE4m3 ? i0 + 1 : i0 + 4;
-                qb[j][m][0] = ok ? qr[i0] : 0u;
-                qb[j][m][1] = ok ? qr[i1] : 0u;
-            }
-        }
-        int lim[NT][2];
-        float mx[NT][2], den[NT][2], o[NT][8][4];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                lim[j][e] = limit(8 * j + 2 * t + e);
-                mx[j][e] = -INFINITY;
-                den[j][e] = 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.0f;
-        }
-
-        const int mi = lane >> 3, j8 = lane & 7;
-        for (int b = b0; b < b1; ++b) {
-            asm volatile("cp.async.wait_group %0;" :: "n"(S::kStages - 2) : "memory");
-            __syncthreads();
-            const int it = b - b0, ahead = it + S::kStages - 1;
-            if (b0 + ahead < b1) load_block(b0 + ahead, ahead % S::kStages);
-            load_ids(b0 + ahead + S::kStages - 1);
-            cp_commit();
-            uint8_t* st = smem + (it % S::kStages) * S::kStage;
-            const int32_t page = s_page[b % kIdRing][warp];
-            if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.pool.num_pages)) continue;
-            const int tok = b * kFewBlock + 16 * warp + g;    // this lane's tokens: tok, tok + 8
-
-            float ka = 1.0f, kb = 1.0f, va = 1.0f, vb = 1.0f;
-            if (kE4m3) {
-                const uint8_t* sc = st + 2 * S::kTensor + 16 * warp + g;
-                ka = scale_value(sc[0]);
-                kb = scale_value(sc[8]);
-                va = scale_value(sc[kFewBlock]);
-                vb = scale_value(sc[kFewBlock + 8]);
-            }
-            // V of a token that some rows may not see must not reach them: 0 * NaN is NaN, so
-            // what is not finite is taken out here and put back into the rows that see it
-            const int tok15 = b * kFewBlock + 16 * warp + 15;
-            if (end - 1 > shared && tok15 > shared) {
-                if (kE4m3) {
-                    int bad = INT32_MAX;
-                    if (tok + 8 > shared && vb != vb) { bad = tok + 8; vb = 0.0f; }
-                    if (tok > shared && va != va) { bad = tok; va = 0.0f; }
-                    bad = __reduce_min_sync(0xffffffffu, bad);
-                    if (bad < end)
-                        for (int i = 0; i < 4; ++i) atomicMin(&s_bad[4 * lane + i], bad);
-                } else {
-                    for (int i = lane; i < 16 * D; i += 32) {
-                        const int row = 16 * warp + i / D, d = i % D, tk = b * kFewBlock + row;
-                        uint16_t* e = reinterpret_cast<uint16_t*>(
-                            st + S::kTensor + row * S::kRowB +
-                            (((d >> 3) ^ (row & 7)) << 4) + (d & 7) * 2);
-                        if (tk > shared && (*e & 0x7f80u) == 0x7f80u) {
-                            atomicMin(&s_bad[d], tk);
-                            *e = 0;
-                        }
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    const int i0 = kE4m3 ? 32 * (i >> 2) + 8 * t + 2 * (i & 3) : 8 * i + t;
+                    const int i1 = kE4m3 ? i0 + 1 : i0 + 4;
+                    qb[j][i][0] = ok ? qr[i0] : 0u;
+                    qb[j][i][1] = ok ? qr[i1] : 0u;
                 }
-                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    lim[j][e] = limit(8 * j + 2 * t + e);
+                    mx[j][e] = -INFINITY;
+                    den[j][e] = 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.0f;
             }
+        }
+        const bool live = m.runs >> warp & 1;
+        const int tok = m.block * kFewBlock + 16 * warp + pg;    // this lane's: tok, tok + 8
 
-            // S^T: 16 tokens x R rows
-            float sc[NT][4];
+        // S^T: 16 tokens x R rows
+        float sc[NT][4];
+        float ka = 1.0f, kb = 1.0f;
+        if (live) {
 #pragma unroll
             for (int j = 0; j < NT; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.0f;
+            const uint8_t* kt = smem + ks * S::kTile;
             if (kE4m3) {
-                const uint32_t base = smem_addr(st + (16 * warp + g) * S::kRowB);
+                const uint8_t* sp = smem + S::kScales + ks * kFewBlock + 16 * warp + pg;
+                ka = scale_value(sp[0]);
+                kb = scale_value(sp[8]);
+                const uint32_t base = smem_addr(kt + (16 * warp + pg) * 128);
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
-                    const uint32_t at = base + (((4 * hh + t) ^ ((g & 1) << 2)) << 4);
-                    const uint4 lo = lds128(at), up = lds128(at + 8 * S::kRowB);
+                    const uint32_t at = base + (((4 * hh + t) ^ pg) << 4);
+                    const uint4 lo = lds128(at), up = lds128(at + 8 * 128);
                     const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w};
                     const uint32_t wu[4] = {up.x, up.y, up.z, up.w};
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const uint32_t f[4] = {widen2(prmt_i<0x1404>(wl[m], 0)),
-                                               widen2(prmt_i<0x1404>(wu[m], 0)),
-                                               widen2(prmt_i<0x3424>(wl[m], 0)),
-                                               widen2(prmt_i<0x3424>(wu[m], 0))};
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t f[4] = {widen2(prmt_i<0x1404>(wl[i], 0)),
+                                               widen2(prmt_i<0x1404>(wu[i], 0)),
+                                               widen2(prmt_i<0x3424>(wl[i], 0)),
+                                               widen2(prmt_i<0x3424>(wu[i], 0))};
 #pragma unroll
                         for (int j = 0; j < NT; ++j)
-                            mma_bf16(sc[j], f, qb[j][4 * hh + m][0], qb[j][4 * hh + m][1]);
+                            mma_bf16(sc[j], f, qb[j][4 * hh + i][0], qb[j][4 * hh + i][1]);
                     }
                 }
             } else {
-                const int krow = 16 * warp + j8 + 8 * (mi & 1), kc = mi >> 1;
-                const uint32_t base = smem_addr(st + krow * S::kRowB);
+                const int row = 16 * warp + j8 + 8 * (mi & 1), kc = mi >> 1;
+                const uint32_t base = smem_addr(kt + row * 128);
 #pragma unroll
-                for (int m = 0; m < 8; ++m) {
+                for (int i = 0; i < 8; ++i) {
                     uint32_t f[4];
-                    ldsm_x4(base + (((2 * m + kc) ^ (krow & 7)) << 4), f);
+                    const int ch = 2 * i + kc;
+                    ldsm_x4(base + (ch >> 3) * (S::kTile / 2) + (((ch & 7) ^ (row & 7)) << 4), f);
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) mma_bf16(sc[j], f, qb[j][m][0], qb[j][m][1]);
+                    for (int j = 0; j < NT; ++j) mma_bf16(sc[j], f, qb[j][i][0], qb[j][i][1]);
                 }
             }
+        }
+        __syncwarp();
+        if (lane == 0) arrive(&c.k_empty[ks]);
 
-            // softmax; the weights as B fragments (k = tokens, n = rows)
-            uint32_t pb[NT][kParts][2];
+        // softmax: weights with the maxima as they are, unless a score is far above
+        uint32_t pb[NT][kParts][2];
+        float w[NT][4];
+        if (live) {
             const float fa = qs * ka, fb = qs * kb;
+            bool grown = false;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                float w[4];
-                float co[2];
+            for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float s0 = tok <= lim[j][e] ? sc[j][e] * fa : -INFINITY;
-                    const float s1 = tok + 8 <= lim[j][e] ? sc[j][2 + e] * fb : -INFINITY;
-                    float bm = fmaxf(s0, s1);
-#pragma unroll
-                    for (int k = 4; k < 32; k <<= 1)
-                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, k));
-                    const float m1 = fmaxf(mx[j][e], bm);
-                    const float ms = m1 == -INFINITY ? 0.0f : m1;
-                    co[e] = exp2f(mx[j][e] - ms);
-                    const float p0 = exp2f(s0 - ms), p1 = exp2f(s1 - ms);
-                    float sum = p0 + p1;
-#pragma unroll
-                    for (int k = 4; k < 32; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-                    den[j][e] = den[j][e] * co[e] + sum;
-                    mx[j][e] = m1;
-                    // (a masked token's scale may be anything)
-                    w[e] = tok <= lim[j][e] ? p0 * va : 0.0f;
-                    w[2 + e] = tok + 8 <= lim[j][e] ? p1 * vb : 0.0f;
+                    sc[j][e] = tok <= lim[j][e] ? sc[j][e] * fa : -INFINITY;
+                    sc[j][2 + e] = tok + 8 <= lim[j][e] ? sc[j][2 + e] * fb : -INFINITY;
+                    grown = grown || fmaxf(sc[j][e], sc[j][2 + e]) > mx[j][e] + kGrow;
                 }
-                if (!__all_sync(0xffffffffu, co[0] == 1.0f && co[1] == 1.0f)) {
+            if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    float co[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float bm = fmaxf(sc[j][e], sc[j][2 + e]);
+#pragma unroll
+                        for (int k = 4; k < 32; k <<= 1)
+                            bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, k));
+                        const float m1 = fmaxf(mx[j][e], bm);
+                        co[e] = exp2f(mx[j][e] - (m1 == -INFINITY ? 0.0f : m1));
+                        mx[j][e] = m1;
+                        den[j][e] *= co[e];
+                    }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         o[j][i][0] *= co[0]; o[j][i][1] *= co[1];
                         o[j][i][2] *= co[0]; o[j][i][3] *= co[1];
                     }
                 }
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float ms = mx[j][e] == -INFINITY ? 0.0f : mx[j][e];
+                    w[j][e] = exp2f(sc[j][e] - ms);
+                    w[j][2 + e] = exp2f(sc[j][2 + e] - ms);
+                    den[j][e] += w[j][e] + w[j][2 + e];
+                }
+        }
+        if (!warp_wait(&c.v_full[vs], (n / S::kNV) & 1, ab)) return;
+        if (live) {
+            uint8_t* vt = smem + (S::kNK + vs) * S::kTile;
+            const int t0 = m.block * kFewBlock + 16 * warp;
+            float va = 1.0f, vb = 1.0f;
+            if (kE4m3) {
+                const uint8_t* sp = smem + S::kScales + (S::kNK + vs) * kFewBlock + 16 * warp + pg;
+                va = scale_value(sp[0]);
+                vb = scale_value(sp[8]);
+            }
+            // What no row or not every row may see must not reach them: 0 * NaN is NaN. Codes
+            // are finite whatever they are and the weights below select; a NaN row of the chunk
+            // itself, or what is not finite in a bf16 row, is taken out and put back at the end
+            // into the rows that see it; rows behind the end of the sequence are cleared.
+            if (t0 + 15 > shared && (sg.end - 1 > shared || t0 + 15 >= sg.end)) {
+                int32_t* bad_at = c.bad[seg & 1];
+                if (kE4m3) {
+                    int bad = INT32_MAX;
+                    if (tok + 8 > shared && tok + 8 < sg.end && vb != vb) { bad = tok + 8; vb = 0.0f; }
+                    if (tok > shared && tok < sg.end && va != va) { bad = tok; va = 0.0f; }
+                    bad = __reduce_min_sync(0xffffffffu, bad);
+                    if (bad != INT32_MAX)
+                        for (int i = 0; i < 4; ++i) atomicMin(&bad_at[4 * lane + i], bad);
+                } else {
+#pragma unroll 1
+                    for (int i = lane; i < 16 * 16; i += 32) {      // 16 rows of 16 pieces
+                        const int row = 16 * warp + (i >> 4), ch = i & 15, tk = t0 + (i >> 4);
+                        if (tk <= shared) continue;
+                        uint4* e = reinterpret_cast<uint4*>(vt + (ch >> 3) * (S::kTile / 2) +
+                                                            row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+                        if (tk >= sg.end) {
+                            *e = make_uint4(0, 0, 0, 0);
+                            continue;
+                        }
+                        const uint4 y = *e;
+                        uint32_t u[4] = {y.x, y.y, y.z, y.w};
+                        bool odd = false;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if ((u[k] & 0x7f80u) == 0x7f80u) {
+                                atomicMin(&bad_at[8 * ch + 2 * k], tk);
+                                u[k] &= 0xffff0000u;
+                                odd = true;
+                            }
+                            if ((u[k] & 0x7f800000u) == 0x7f800000u) {
+                                atomicMin(&bad_at[8 * ch + 2 * k + 1], tk);
+                                u[k] &= 0xffffu;
+                                odd = true;
+                            }
+                        }
+                        if (odd) *e = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                }
+            }
+            // the weights as B fragments (k = tokens, n = rows)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                if (kE4m3) {   // (a masked token's scale may be anything)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        w[j][e] = tok <= lim[j][e] ? w[j][e] * va : 0.0f;
+                        w[j][2 + e] = tok + 8 <= lim[j][e] ? w[j][2 + e] * vb : 0.0f;
+                    }
+                }
 #pragma unroll
                 for (int k = 0; k < kParts; ++k) {
-                    const uint32_t h01 = bf2(w[0], w[1]), h23 = bf2(w[2], w[3]);
+                    const uint32_t h01 = bf2(w[j][0], w[j][1]), h23 = bf2(w[j][2], w[j][3]);
                     pb[j][k][0] = movm_t(h01);
                     pb[j][k][1] = movm_t(h23);
                     const float2 f01 = bf2_f(h01), f23 = bf2_f(h23);
-                    w[0] -= f01.x; w[1] -= f01.y; w[2] -= f23.x; w[3] -= f23.y;
+                    w[j][0] -= f01.x; w[j][1] -= f01.y; w[j][2] -= f23.x; w[j][3] -= f23.y;
                 }
             }
-
             // O^T += V^T P^T. MMA i covers elements 16 i + g and 16 i + g + 8 of a row (bf16),
-            // or 16 g + 2 i and 16 g + 2 i + 1 (8-bit)
+            // or 16 pg + 2 i and 16 pg + 2 i + 1 (8-bit)
             if (kE4m3) {
-                uint32_t wv[4][4];   // rows 2t, 2t+1, 2t+8, 2t+9: 16 codes from element 16 g on
+                uint32_t wv[4][4];   // S rows 2t, 2t+1, 2t+8, 2t+9 are tokens t, t+4, t+8, t+12
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int row = 16 * warp + 2 * t + (k & 1) + 8 * (k >> 1);
-                    const uint4 q4 = lds128(smem_addr(st + S::kTensor + row * S::kRowB) +
-                                            ((g ^ (((row >> 1) & 3) << 1)) << 4));
+                    const int row = 16 * warp + t + 4 * k;
+                    const uint4 q4 = lds128(smem_addr(vt + row * 128) + ((pg ^ (row & 7)) << 4));
                     wv[k][0] = q4.x; wv[k][1] = q4.y; wv[k][2] = q4.z; wv[k][3] = q4.w;
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int w = i >> 1;
+                    const int u = i >> 1;
                     // the same element of two neighbouring tokens, side by side
                     uint32_t f[4];
                     if (i & 1) {
-                        f[0] = widen2(prmt_i<0x6020>(wv[0][w], wv[1][w]));
-                        f[1] = widen2(prmt_i<0x7030>(wv[0][w], wv[1][w]));
-                        f[2] = widen2(prmt_i<0x6020>(wv[2][w], wv[3][w]));
-                        f[3] = widen2(prmt_i<0x7030>(wv[2][w], wv[3][w]));
+                        f[0] = widen2(prmt_i<0x6020>(wv[0][u], wv[1][u]));
+                        f[1] = widen2(prmt_i<0x7030>(wv[0][u], wv[1][u]));
+                        f[2] = widen2(prmt_i<0x6020>(wv[2][u], wv[3][u]));
+                        f[3] = widen2(prmt_i<0x7030>(wv[2][u], wv[3][u]));
                     } else {
-                        f[0] = widen2(prmt_i<0x4000>(wv[0][w], wv[1][w]));
-                        f[1] = widen2(prmt_i<0x5010>(wv[0][w], wv[1][w]));
-                        f[2] = widen2(prmt_i<0x4000>(wv[2][w], wv[3][w]));
-                        f[3] = widen2(prmt_i<0x5010>(wv[2][w], wv[3][w]));
+                        f[0] = widen2(prmt_i<0x4000>(wv[0][u], wv[1][u]));
+                        f[1] = widen2(prmt_i<0x5010>(wv[0][u], wv[1][u]));
+                        f[2] = widen2(prmt_i<0x4000>(wv[2][u], wv[3][u]));
+                        f[3] = widen2(prmt_i<0x5010>(wv[2][u], wv[3][u]));
                     }
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
@@ -401,12 +598,13 @@ attend_few_kernel(const AttendArgs a) {
                             mma_bf16(o[j][i], f, pb[j][k][0], pb[j][k][1]);
                 }
             } else {
-                const int vrow = 16 * warp + j8 + 8 * (mi >> 1), vc = mi & 1;
-                const uint32_t base = smem_addr(st + S::kTensor + vrow * S::kRowB);
+                const int row = 16 * warp + j8 + 8 * (mi >> 1), vc = mi & 1;
+                const uint32_t base = smem_addr(vt + row * 128);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     uint32_t f[4];
-                    ldsm_x4_t(base + (((2 * i + vc) ^ (vrow & 7)) << 4), f);
+                    const int ch = 2 * i + vc;
+                    ldsm_x4_t(base + (ch >> 3) * (S::kTile / 2) + (((ch & 7) ^ (row & 7)) << 4), f);
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -415,99 +613,168 @@ attend_few_kernel(const AttendArgs a) {
                 }
             }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        __syncthreads();   // the stages become the merge scratch
+        __syncwarp();
+        if (lane == 0) arrive(&c.v_empty[vs]);
+        ++n;
+        if (!(m.flags & kLast)) continue;
 
-        float* scr = reinterpret_cast<float*>(smem);
+        // the warps' partials of 8 rows at a time, merged
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < NT; ++j) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float* w = scr + (warp * R + 8 * j + 2 * t + e) * kPart;
+#pragma unroll
+                for (int k = 4; k < 32; k <<= 1)
+                    den[j][e] += __shfl_xor_sync(0xffffffffu, den[j][e], k);
+                float* p = scr + (warp * 8 + 2 * t + e) * kPart;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    w[kE4m3 ? 16 * g + 2 * i : 16 * i + g] = o[j][i][e];
-                    w[kE4m3 ? 16 * g + 2 * i + 1 : 16 * i + g + 8] = o[j][i][2 + e];
+                    p[kE4m3 ? 16 * pg + 2 * i : 16 * i + g] = o[j][i][e];
+                    p[kE4m3 ? 16 * pg + 2 * i + 1 : 16 * i + g + 8] = o[j][i][2 + e];
                 }
                 if (g == 0) {
-                    w[D] = mx[j][e];
-                    w[D + 1] = den[j][e];
+                    p[D] = mx[j][e];
+                    p[D + 1] = den[j][e];
                 }
             }
-        __syncthreads();
-        const bool whole = b0 == 0 && b1 == nb;
-        float* part = a.work + (2 * static_cast<int64_t>(blockIdx.x) + (b0 == 0)) * part_floats(R);
-        for (int r = warp; r < nrow; r += kFW) {
-            float M = -INFINITY;
+            if (!meet()) return;
+            float* part = a.work + static_cast<int64_t>(sg.part) * part_floats(R);
+            for (int r8 = warp; r8 < 8 && 8 * j + r8 < sg.nrow; r8 += kFW) {
+                const int r = 8 * j + r8;
+                float M = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kFW; ++w) M = fmaxf(M, scr[(w * R + r) * kPart + D]);
-            const float ms = M == -INFINITY ? 0.0f : M;
-            float dn = 0.0f, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int x = 0; x < kFW; ++x) M = fmaxf(M, scr[(x * 8 + r8) * kPart + D]);
+                const float ms = M == -INFINITY ? 0.0f : M;
+                float dn = 0.0f, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int w = 0; w < kFW; ++w) {
-                const float* src = scr + (w * R + r) * kPart;
-                const float f = exp2f(src[D] - ms);
-                dn += src[D + 1] * f;
-                const float4 z = *reinterpret_cast<const float4*>(src + 4 * lane);
-                y[0] += z.x * f; y[1] += z.y * f; y[2] += z.z * f; y[3] += z.w * f;
-            }
-            const int lr = limit(r);
+                for (int x = 0; x < kFW; ++x) {
+                    const float* src = scr + (x * 8 + r8) * kPart;
+                    const float f = exp2f(src[D] - ms);
+                    dn += src[D + 1] * f;
+                    const float4 z = *reinterpret_cast<const float4*>(src + 4 * lane);
+                    y[0] += z.x * f; y[1] += z.y * f; y[2] += z.z * f; y[3] += z.w * f;
+                }
+                const int lr = limit(r);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (s_bad[4 * lane + i] <= lr) y[i] = __uint_as_float(0x7fc00000u);
-            if (whole) {
-                const float inv = dn == 0.0f ? 0.0f : 1.0f / dn;
-                const int rr = first + r;
-                const int64_t at = (v.row0 + rr / G) * (static_cast<int64_t>(a.heads) * G) +
-                                   h * G + rr % G;
-                Out* dst = static_cast<Out*>(a.out) + at * D + 4 * lane;
-                if constexpr (sizeof(Out) == 2)
-                    *reinterpret_cast<uint2*>(dst) =
-                        make_uint2(bf2(y[0] * inv, y[1] * inv), bf2(y[2] * inv, y[3] * inv));
-                else
-                    *reinterpret_cast<float4*>(dst) =
-                        make_float4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
-                if (a.lse && lane == 0) a.lse[at] = dn == 0.0f ? -INFINITY : M * kLn2 + logf(dn);
-            } else {
-                *reinterpret_cast<float4*>(part + r * D + 4 * lane) =
-                    make_float4(y[0], y[1], y[2], y[3]);
-                if (lane == 0) {
-                    part[R * D + r] = M;
-                    part[R * D + R + r] = dn;
+                for (int i = 0; i < 4; ++i)
+                    if (c.bad[seg & 1][4 * lane + i] <= lr) y[i] = __uint_as_float(0x7fc00000u);
+                if (sg.whole) {
+                    const float inv = dn == 0.0f ? 0.0f : 1.0f / dn;
+                    const int rr = sg.first + r;
+                    const int64_t at = (sg.row0 + rr / G) * (static_cast<int64_t>(a.heads) * G) +
+                                       static_cast<int64_t>(sg.head) * G + rr % G;
+                    Out* dst = static_cast<Out*>(a.out) + at * D + 4 * lane;
+                    if constexpr (sizeof(Out) == 2)
+                        *reinterpret_cast<uint2*>(dst) =
+                            make_uint2(bf2(y[0] * inv, y[1] * inv), bf2(y[2] * inv, y[3] * inv));
+                    else
+                        *reinterpret_cast<float4*>(dst) =
+                            make_float4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+                    if (a.lse && lane == 0)
+                        a.lse[at] = dn == 0.0f ? -INFINITY : M * kLn2 + logf(dn);
+                } else {
+                    *reinterpret_cast<float4*>(part + r * D + 4 * lane) =
+                        make_float4(y[0], y[1], y[2], y[3]);
+                    if (lane == 0) {
+                        part[R * D + r] = M;
+                        part[R * D + R + r] = dn;
+                    }
                 }
             }
+            if (j == NT - 1) c.bad[(seg + 1) & 1][tid] = INT32_MAX;
+            if (!meet()) return;   // the scratch is free again
         }
-        __syncthreads();   // the scratch becomes the stages again
-        x = start + b1;
-        if (b1 == nb && ++tile == nt) {
-            tile = 0;
-            ++h;
-        }
+        ++seg;
     }
 }
 
-template <bool kE4m3, int kParts, typename Out>
-cudaError_t launch_few(const AttendArgs& a, int ctas, cudaStream_t st) {
+constexpr int few_per_sm(bool e4m3, int nt) { return e4m3 && nt == 1 ? 3 : 2; }
+
+template <bool kE4m3, int NT, int kParts, typename Out>
+__global__ void __launch_bounds__((kFW + 1) * 32, few_per_sm(kE4m3, NT))
+attend_few_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap mk,
+                  const __grid_constant__ CUtensorMap mv, int inline_plan) {
+    using S = FewShape<kE4m3>;
+    extern __shared__ uint8_t raw_smem[];
+    __shared__ __align__(16) Control c;
+    uint8_t* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        c.abort = 0;
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(smem_addr(&c.k_full[i]), 1);
+            mbar_init(smem_addr(&c.k_empty[i]), kFW);
+            mbar_init(smem_addr(&c.v_full[i]), 1);
+            mbar_init(smem_addr(&c.v_empty[i]), kFW);
+        }
+        mbar_init(smem_addr(&c.met), kFW);
+        mbar_fence_init();
+        tma_prefetch_map(&mk);
+        tma_prefetch_map(&mv);
+    }
+    if (threadIdx.x < D) c.bad[0][threadIdx.x] = c.bad[1][threadIdx.x] = INT32_MAX;
+    pdl_wait();
+    pdl_launch_dependents();
+    const Range range = make_range(a, c, inline_plan != 0);
+    __syncthreads();
+    if (warp == kFW) {
+        few_loads<kE4m3>(a, &mk, &mv, c, smem, range);
+        if (*reinterpret_cast<volatile int32_t*>(&c.abort)) {
+            // copies that were under way when a wait ran out write into this CTA's memory: give
+            // them the time that any of them takes before the CTA ends
+            const uint64_t t0 = now_ns();
+            while (now_ns() - t0 < 10000000ull) {}
+        }
+    } else {
+        few_consume<kE4m3, NT, kParts, Out>(a, c, smem);
+    }
+}
+
+template <bool kE4m3, int NT, int kParts, typename Out>
+cudaError_t launch_few(const AttendArgs& a, const CUtensorMap maps[2], int ctas, bool inline_plan,
+                       cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     constexpr int smem = FewShape<kE4m3>::kSmem;
-    auto kernel = attend_few_kernel<kE4m3, 2, kParts, Out>;
+    auto kernel = attend_few_kernel<kE4m3, NT, kParts, Out>;
     const cudaError_t e = raise_smem_limit(kernel, smem, done);
     if (e != cudaSuccess) return e;
-    kernel<<<ctas, kFW * 32, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(kernel, dim3(ctas), dim3((kFW + 1) * 32), smem, st, a, maps[0], maps[1],
+                      inline_plan ? 1 : 0);
+}
+
+template <bool kE4m3, int NT>
+cudaError_t launch_few_out(const AttendArgs& a, const CUtensorMap maps[2], bool f32_out, int ctas,
+                           bool inline_plan, cudaStream_t st) {
+    return f32_out ? launch_few<kE4m3, NT, 3, float>(a, maps, ctas, inline_plan, st)
+                   : launch_few<kE4m3, NT, 2, __nv_bfloat16>(a, maps, ctas, inline_plan, st);
 }
 
 }  // namespace
 
-int few_ctas(int sms) { return 2 * sms; }
+int few_ctas(int sms, int format, int tile_rows) {
+    return sms * few_per_sm(format == PARISKV_PAGES_E4M3, tile_rows / 8);
+}
+
+bool few_plans_inline(int batch) { return batch <= kInline; }
 
 cudaError_t launch_attend_few(const AttendArgs& a, int format, bool f32_out, int ctas,
                               cudaStream_t st) {
-    if (format == PARISKV_PAGES_E4M3)
-        return f32_out ? launch_few<true, 3, float>(a, ctas, st)
-                       : launch_few<true, 2, __nv_bfloat16>(a, ctas, st);
-    return f32_out ? launch_few<false, 3, float>(a, ctas, st)
-                   : launch_few<false, 2, __nv_bfloat16>(a, ctas, st);
+    const bool e4 = format == PARISKV_PAGES_E4M3, in = few_plans_inline(a.seqs.batch);
+    const uint64_t el = e4 ? 1 : 2;
+    CUtensorMap maps[2];
+    for (int t = 0; t < 2; ++t)
+        if (!encode_rows(&maps[t], t ? a.pool.v : a.pool.k, e4, true,
+                         static_cast<uint64_t>(a.heads) << a.pool.shift, a.pool.num_pages, el * D,
+                         a.pool.page_bytes, e4 ? D : 64, min(1 << a.pool.shift, kFewBlock), 1))
+            return cudaErrorInvalidValue;
+    const bool one = a.shape.tile_rows == 8;
+    if (e4)
+        return one ? launch_few_out<true, 1>(a, maps, f32_out, ctas, in, st)
+                   : launch_few_out<true, 2>(a, maps, f32_out, ctas, in, st);
+    return one ? launch_few_out<false, 1>(a, maps, f32_out, ctas, in, st)
+               : launch_few_out<false, 2>(a, maps, f32_out, ctas, in, st);
 }
+
+cudaError_t take_few_status(int* status, cudaStream_t st) { return take_wait_status(status, st); }
 
 }  // namespace pkv

@@ -29,8 +29,7 @@
 // Roles, by warp: 0-3 and 4-7 softmax and output of the halves, 8 loads, 9 and 10 the halves'
 // products, 11 and up repair (bf16) or widening (8-bit). They meet in mbarriers; every wait gives up after
 // kWaitLimitNs, which ends the whole CTA in order and reaches the caller as a status.
-#include "paged.cuh"
-#include "tcgen05.cuh"
+#include "paged_async.cuh"
 
 namespace pkv {
 
@@ -43,8 +42,6 @@ constexpr int kHalfB = kBlk * 128;             // 64 columns x 128 rows of bf16:
 constexpr int kStageB = 2 * kHalfB;            // a K, V or Q tile: 32 KB
 constexpr int kRawB = kBlk * D;                // a tile of codes: 16 KB
 constexpr int kRing = 8;                       // block entries between the loads and the others
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
-constexpr uint32_t kNapNs = 20000;
 constexpr float kRescale = 8.0f;               // growth of a maximum (base 2) that rescales O
 
 template <bool kE4m3, int kParts> struct Shape {
@@ -96,53 +93,6 @@ struct Shared {
     uint32_t tmem;
     int32_t abort;
 };
-
-__device__ int g_chunk_status;   // ST_TIMEOUT after a wait ran out
-
-__device__ __forceinline__ uint64_t now_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-// Waits for the phase of `parity` to complete; false once a wait of this CTA has run out. The
-// thread sleeps in the instruction for up to kNapNs at a time (or until the phase is complete): a
-// spinning warp would take issue slots from the softmax.
-__device__ __forceinline__ bool try_wait_nap(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok) : "r"(bar), "r"(parity), "r"(kNapNs) : "memory");
-    return ok != 0;
-}
-// (out of line: the roles' loops have to share the instruction caches)
-__device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, volatile int32_t* abort,
-                                       uint64_t limit) {
-    const uint64_t t0 = now_ns();
-#pragma unroll 1
-    while (!try_wait_nap(bar, parity)) {
-        if (*abort) return false;
-        if (now_ns() - t0 > limit) {
-            *abort = 1;
-            atomicExch(&g_chunk_status, ST_TIMEOUT);
-            return false;
-        }
-    }
-    return true;
-}
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int32_t* abort,
-                                         uint64_t limit = kWaitLimitNs) {
-    const uint32_t b = smem_addr(bar);
-    return try_wait_nap(b, parity) || wait_more(b, parity, abort, limit);
-}
-// the same by a whole warp, which goes on together
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
-                                          volatile int32_t* abort) {
-    return __all_sync(0xffffffffu, wait_for(bar, parity, abort));
-}
-__device__ __forceinline__ void arrive(uint64_t* bar) { mbar_arrive(smem_addr(bar)); }
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -973,38 +923,6 @@ cudaError_t launch_chunk(const AttendArgs& a, const CUtensorMap maps[3], int cta
                       maps[2]);
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-    static const EncodeTiled fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &r) != cudaSuccess ||
-            r != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return fn;
-}
-
-// a 3-d tensor of rows of 128 elements; boxes of `cols` x r1 x r2
-bool encode(CUtensorMap* m, const void* base, bool bytes, uint64_t n1, uint64_t n2, uint64_t s1,
-            uint64_t s2, uint32_t cols, uint32_t r1, uint32_t r2) {
-    const EncodeTiled fn = encode_tiled();
-    if (!fn) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), n1, n2}, strides[2] = {s1, s2};
-    const cuuint32_t box[3] = {cols, r1, r2}, step[3] = {1, 1, 1};
-    return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-              const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace
 
 int chunk_tile_rows(int group, bool f32_out) { return (f32_out ? 1 : 2) * (128 / group) * group; }
@@ -1017,12 +935,12 @@ cudaError_t launch_attend_chunk(const AttendArgs& a, int format, bool f32_out, i
     const uint32_t run = min(1 << a.pool.shift, kBlk);
     const uint64_t el = e4 ? 1 : 2;
     CUtensorMap maps[3];
-    if (!encode(&maps[0], a.q, false, static_cast<uint64_t>(a.heads) * G, a.seqs.total_q, 2 * D,
-                a.q_ld * 2, 64, G, 128 / G))
+    if (!encode_rows(&maps[0], a.q, false, true, static_cast<uint64_t>(a.heads) * G,
+                     a.seqs.total_q, 2 * D, a.q_ld * 2, 64, G, 128 / G))
         return cudaErrorInvalidValue;
     for (int t = 0; t < 2; ++t)
-        if (!encode(&maps[1 + t], t ? a.pool.v : a.pool.k, e4, rows, a.pool.num_pages, el * D,
-                    a.pool.page_bytes, e4 ? D : 64, run, 1))
+        if (!encode_rows(&maps[1 + t], t ? a.pool.v : a.pool.k, e4, !e4, rows, a.pool.num_pages,
+                         el * D, a.pool.page_bytes, e4 ? D : 64, run, 1))
             return cudaErrorInvalidValue;
     if (e4)
         return f32_out ? launch_chunk<true, 3, float>(a, maps, ctas, st)
@@ -1031,15 +949,6 @@ cudaError_t launch_attend_chunk(const AttendArgs& a, int format, bool f32_out, i
                    : launch_chunk<false, 1, __nv_bfloat16>(a, maps, ctas, st);
 }
 
-// The status word of the current device, read and cleared after `st`'s work is done.
-cudaError_t take_chunk_status(int* status, cudaStream_t st) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(status, g_chunk_status, sizeof(int), 0,
-                                              cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e != cudaSuccess || *status == ST_OK) return e;
-    const int ok = ST_OK;
-    e = cudaMemcpyToSymbolAsync(g_chunk_status, &ok, sizeof(int), 0, cudaMemcpyHostToDevice, st);
-    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
-}
+cudaError_t take_chunk_status(int* status, cudaStream_t st) { return take_wait_status(status, st); }
 
 }  // namespace pkv
