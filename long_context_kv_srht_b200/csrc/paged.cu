@@ -9,13 +9,6 @@ namespace pkv {
 
 namespace {
 
-// 8 consecutive elements of a row as fp32
-__device__ __forceinline__ void load8(const float* p, float v[8]) {
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    const float4 b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
 __device__ __forceinline__ void unpack8(uint4 a, float v[8]) {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -23,9 +16,6 @@ __device__ __forceinline__ void unpack8(uint4 a, float v[8]) {
         v[2 * i] = __uint_as_float(w[i] << 16);
         v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float v[8]) {
-    unpack8(*reinterpret_cast<const uint4*>(p), v);
 }
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -38,19 +28,66 @@ __device__ __forceinline__ uint4 pack8(const float v[8]) {
 
 // ------------------------------------------------------------------------------------ write
 // A warp takes one new token: 2 * heads rows of 128 elements (K of every head, then V), two at
-// a time, 16 lanes a row and 8 elements a lane, kWriteRows row pairs in flight. Bound by HBM:
-// it reads each row once and writes 256 or 129 bytes of it; neighbouring tokens are in
-// neighbouring warps of a CTA, so the 128-byte pieces of a head's rows meet in L2.
+// a time, 16 lanes a row and 8 elements a lane. The first rows are under way while the warp finds
+// out where they go (a chain of dependent loads: starts, lengths, the page's id). Bound by HBM: it
+// reads each row once and writes 256 or 129 bytes of it; neighbouring tokens are in neighbouring
+// warps of a CTA, so the 128-byte pieces of a head's rows meet in L2.
 constexpr int kWriteWarps = 8;
-constexpr int kWriteRows = 4;
+
+// 8 elements of a row, as they are in memory
+template <typename In> struct Raw8;
+template <> struct Raw8<float> {
+    float4 a, b;
+    static constexpr int kRows = 4;      // row pairs in flight
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldcs(reinterpret_cast<const float4*>(p));
+        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void clear() { a = b = make_float4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float v[8]) const {
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+    __device__ __forceinline__ uint4 bf16() const {
+        float v[8];
+        get(v);
+        return pack8(v);
+    }
+};
+template <> struct Raw8<__nv_bfloat16> {
+    uint4 a;
+    static constexpr int kRows = 8;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        a = __ldcs(reinterpret_cast<const uint4*>(p));
+    }
+    __device__ __forceinline__ void clear() { a = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float v[8]) const { unpack8(a, v); }
+    __device__ __forceinline__ uint4 bf16() const { return a; }
+};
 
 template <typename In, bool kE4m3>
 __global__ void __launch_bounds__(kWriteWarps * 32)
 paged_write_kernel(const PagePool pool, const Seqs c, int heads, const In* __restrict__ kn,
                    const In* __restrict__ vn, int64_t k_ld, int64_t v_ld) {
+    constexpr int kRows = Raw8<In>::kRows;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t tok = static_cast<int64_t>(blockIdx.x) * kWriteWarps + warp;
     if (tok >= c.total_q) return;
+    const int half = lane >> 4, l8 = (lane & 15) * 8;
+    Raw8<In> x[kRows];
+    auto load = [&](int r0) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int r = r0 + 2 * i + half;
+            const bool is_v = r >= heads;
+            if (r < 2 * heads)
+                x[i].load((is_v ? vn + tok * v_ld : kn + tok * k_ld) +
+                          static_cast<int64_t>(is_v ? r - heads : r) * D + l8);
+            else
+                x[i].clear();
+        }
+    };
+    load(0);
     // the sequence of the token: the last start <= tok
     int lo = 0;
     for (int len = c.batch + 1; len > 1;) {
@@ -68,36 +105,25 @@ paged_write_kernel(const PagePool pool, const Seqs c, int heads, const In* __res
     const int32_t page = c.table[static_cast<int64_t>(lo) * c.stride + (pos >> pool.shift)];
     if (page < 0 || page >= pool.num_pages) return;
     const int slot = static_cast<int>(pos) & ((1 << pool.shift) - 1);
-    const int half = lane >> 4, l8 = (lane & 15) * 8;
 
-    for (int r0 = 0; r0 < 2 * heads; r0 += 2 * kWriteRows) {
-        float x[kWriteRows][8];
+    for (int r0 = 0; r0 < 2 * heads; r0 += 2 * kRows) {
+        if (r0 > 0) load(r0);
 #pragma unroll
-        for (int i = 0; i < kWriteRows; ++i) {
-            const int r = r0 + 2 * i + half;
-            if (r < 2 * heads) {
-                const bool is_v = r >= heads;
-                load8((is_v ? vn + tok * v_ld : kn + tok * k_ld) +
-                          static_cast<int64_t>(is_v ? r - heads : r) * D + l8, x[i]);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) x[i][k] = 0.0f;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kWriteRows; ++i) {
+        for (int i = 0; i < kRows; ++i) {
             const int r = r0 + 2 * i + half;
             const bool live = r < 2 * heads, is_v = r >= heads;
             const int64_t row = static_cast<int64_t>(is_v ? r - heads : r) << pool.shift | slot;
             uint8_t* base = (is_v ? pool.v : pool.k) + page * pool.page_bytes;
             if (!kE4m3) {
-                if (live) *reinterpret_cast<uint4*>(base + (row * D + l8) * 2) = pack8(x[i]);
+                if (live) *reinterpret_cast<uint4*>(base + (row * D + l8) * 2) = x[i].bf16();
                 continue;
             }
+            float y[8];
+            x[i].get(y);
             // largest magnitude by its bits: a NaN's are above infinity's
             uint32_t top = 0;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(x[i][k]) & 0x7fffffffu);
+            for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(y[k]) & 0x7fffffffu);
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
             const bool finite = top < 0x7f800000u;
@@ -107,11 +133,11 @@ paged_write_kernel(const PagePool pool, const Seqs c, int heads, const In* __res
             if (finite) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const float* y = x[i] + 4 * k;
-                    code[k] = __nv_cvt_float2_to_fp8x2(make_float2(y[0] * inv, y[1] * inv),
+                    const float* z = y + 4 * k;
+                    code[k] = __nv_cvt_float2_to_fp8x2(make_float2(z[0] * inv, z[1] * inv),
                                                        __NV_SATFINITE, __NV_E4M3);
                     code[k] |= uint32_t(__nv_cvt_float2_to_fp8x2(
-                                   make_float2(y[2] * inv, y[3] * inv), __NV_SATFINITE,
+                                   make_float2(z[2] * inv, z[3] * inv), __NV_SATFINITE,
                                    __NV_E4M3)) << 16;
                 }
             }

@@ -135,9 +135,10 @@ __device__ __forceinline__ int find_tile(const Tile* t, int n, int64_t x) {
 
 // The parts of cut tiles: slot 2 * cta holds the CTA's first tile when it begins before the
 // CTA's range, slot 2 * cta + 1 its last tile when it begins inside and ends past the range.
-// A slot is tile_rows rows of 128 accumulators, then the rows' maxima (base-2 units) and sums.
+// A slot is tile_rows rows of 128 accumulators, then the rows' maxima (base-2 units) and sums; each
+// begins on 16 bytes (tile_rows may be odd).
 __host__ __device__ __forceinline__ size_t part_floats(int tile_rows) {
-    return static_cast<size_t>(tile_rows) * (D + 2);
+    return static_cast<size_t>(round_up(static_cast<int64_t>(tile_rows) * (D + 2), 4));
 }
 
 struct AttendArgs {

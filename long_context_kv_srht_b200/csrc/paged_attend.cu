@@ -15,13 +15,19 @@
 //  - both products run on mma.sync (m16n8k16, bf16, fp32 accumulators): S^T = K Q^T and O^T +=
 //    V^T P^T, so a lane's softmax state and its accumulators belong to the same two rows of each
 //    8-row group. K and V are read once, so tcgen05 tiles of 128 rows would be 1/16 full;
-//  - bf16 rows come as fragments by ldmatrix. 8-bit rows are widened in registers: which element
-//    of the head dimension, and which token, stands at which position of a fragment is free as
-//    long as both factors agree, so a lane reads 16 consecutive codes and uses them for four MMAs;
-//  - the 8-bit rows' scales are powers of two and multiply the scores (K) and the weights (V);
-//  - P enters the second product as two bf16 parts (16 bits), or three (24) for fp32 output;
+//  - bf16 rows come as fragments by ldmatrix. 8-bit rows are widened to fp16 in registers (one
+//    instruction a pair; fp16 holds every code): which element of the head dimension, and which
+//    token, stands at which position of a fragment is free as long as both factors agree, so a
+//    lane reads 16 consecutive codes and uses them for four MMAs. Q becomes fp16 too, each row
+//    times a power of two;
+//  - the 8-bit rows' scales are powers of two: K's multiply the scores, V's go into the exponents
+//    of the weights, which are then relative to maxima of their own (so that they fit fp16);
+//  - P enters the second product in parts: two of bf16 (16 bits; 8-bit pages: one of fp16, 11
+//    bits), three (24 bits and more) for fp32 output;
 //  - a row's maximum is only brought up to date (three shuffles, O rescaled) when a score exceeds
 //    it by more than 2^8; sums stay per lane until the end of a range, where the warps merge.
+#include <cuda_fp16.h>
+
 #include "paged_async.cuh"
 
 namespace pkv {
@@ -78,13 +84,21 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
-__device__ __forceinline__ void mma_bf16(float d[4], const uint32_t a[4], uint32_t b0,
-                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// d += a * b (m16n8k16, fp32 accumulators; bf16 factors, or fp16 ones)
+template <bool kF16>
+__device__ __forceinline__ void mma16(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+    if (kF16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+            "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+            "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
     uint32_t y;
@@ -99,18 +113,21 @@ __device__ __forceinline__ float2 bf2_f(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// Two e4m3 codes, in bytes 1 and 3 of r (the other bytes are ignored), as bf16 values: sign and
-// the seven bits below it, moved four places down, are a bf16 number 2^-120 times the code's
-// value (the exponent biases differ by 120; subnormal codes become subnormal bf16 numbers), and
-// the product with 2^120 is exact.
-__device__ __forceinline__ uint32_t widen2(uint32_t r) {
-    const uint32_t w = (r & 0x80008000u) | ((r >> 4) & 0x07f007f0u);
-    __nv_bfloat162 v, f;
-    *reinterpret_cast<uint32_t*>(&v) = w;
-    *reinterpret_cast<uint32_t*>(&f) = 0x7b807b80u;   // 2^120, 2^120
-    v = __hmul2(v, f);
+__device__ __forceinline__ uint32_t h2(float lo, float hi) {
+    __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
 }
+__device__ __forceinline__ float2 h2_f(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+// two e4m3 codes as fp16 values (exact: fp16 has the exponents and the bits)
+__device__ __forceinline__ uint32_t widen2(uint16_t codes) {
+    uint32_t y;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(codes));
+    return y;
+}
+__device__ __forceinline__ uint32_t widen_lo(uint32_t w) { return widen2(static_cast<uint16_t>(w)); }
+__device__ __forceinline__ uint32_t widen_hi(uint32_t w) { return widen2(static_cast<uint16_t>(w >> 16)); }
 
 // The last of n + 1 sums with pre[i] <= x.
 __device__ __forceinline__ int find_pre(const int64_t* pre, int n, int64_t x) {
@@ -348,7 +365,9 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
     Seg sg = {};
     uint32_t qb[NT][8][2];
     int lim[NT][2], shared = 0;
+    int down[NT][2];     // exponents that undo what the rows of Q were multiplied by (8-bit)
     float mx[NT][2], den[NT][2], o[NT][8][4];
+    float mw[NT][2];     // maxima of the weights that O is relative to (8-bit: mx and V's scales)
     // the last token a row may attend
     auto limit = [&](int r) -> int {
         if (r >= sg.nrow) return -1;
@@ -385,10 +404,38 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                     qb[j][i][0] = ok ? qr[i0] : 0u;
                     qb[j][i][1] = ok ? qr[i1] : 0u;
                 }
+                float up = 1.0f;
+                if (kE4m3) {
+                    // the fp16 of the row times a power of two that brings its largest magnitude
+                    // to [2^14, 2^15): exact but for what is 2^31 times smaller than that
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint32_t x = qb[j][i >> 1][i & 1];
+                        top = max(top, max(x & 0x7fffu, x >> 16 & 0x7fffu));
+                    }
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    // (in two steps: the power itself may be out of range)
+                    const int e = top >= 0x7f80u || top < 0x80u ? 0 : 127 + 14 - static_cast<int>(top >> 7);
+                    const float f0 = pow2f(e / 2), f1 = pow2f(e - e / 2);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 x = bf2_f(qb[j][i >> 1][i & 1]);
+                        qb[j][i >> 1][i & 1] = h2(x.x * f0 * f1, x.y * f0 * f1);
+                    }
+                    up = __int_as_float(e);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    // (that row's exponent is with the lanes whose g it is)
+                    const int k = __float_as_int(__shfl_sync(0xffffffffu, up, 4 * (2 * t + e)));
+                    down[j][e] = kE4m3 ? -k : 0;
+                }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     lim[j][e] = limit(8 * j + 2 * t + e);
-                    mx[j][e] = -INFINITY;
+                    mx[j][e] = mw[j][e] = -INFINITY;
                     den[j][e] = 0.0f;
                 }
 #pragma unroll
@@ -419,13 +466,11 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                     const uint32_t wu[4] = {up.x, up.y, up.z, up.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint32_t f[4] = {widen2(prmt_i<0x1404>(wl[i], 0)),
-                                               widen2(prmt_i<0x1404>(wu[i], 0)),
-                                               widen2(prmt_i<0x3424>(wl[i], 0)),
-                                               widen2(prmt_i<0x3424>(wu[i], 0))};
+                        const uint32_t f[4] = {widen_lo(wl[i]), widen_lo(wu[i]), widen_hi(wl[i]),
+                                               widen_hi(wu[i])};
 #pragma unroll
                         for (int j = 0; j < NT; ++j)
-                            mma_bf16(sc[j], f, qb[j][4 * hh + i][0], qb[j][4 * hh + i][1]);
+                            mma16<kE4m3>(sc[j], f, qb[j][4 * hh + i][0], qb[j][4 * hh + i][1]);
                     }
                 }
             } else {
@@ -437,7 +482,7 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                     const int ch = 2 * i + kc;
                     ldsm_x4(base + (ch >> 3) * (S::kTile / 2) + (((ch & 7) ^ (row & 7)) << 4), f);
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) mma_bf16(sc[j], f, qb[j][i][0], qb[j][i][1]);
+                    for (int j = 0; j < NT; ++j) mma16<kE4m3>(sc[j], f, qb[j][i][0], qb[j][i][1]);
                 }
             }
         }
@@ -447,124 +492,161 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
         // softmax: weights with the maxima as they are, unless a score is far above
         uint32_t pb[NT][kParts][2];
         float w[NT][4];
-        if (live) {
-            const float fa = qs * ka, fb = qs * kb;
+        // brings maxima up to date with the values v where one is far above; factors for the old
+        auto raise = [&](float (&top)[NT][2], const float (&v)[NT][4], float (&co)[NT][2]) -> bool {
             bool grown = false;
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    sc[j][e] = tok <= lim[j][e] ? sc[j][e] * fa : -INFINITY;
-                    sc[j][2 + e] = tok + 8 <= lim[j][e] ? sc[j][2 + e] * fb : -INFINITY;
-                    grown = grown || fmaxf(sc[j][e], sc[j][2 + e]) > mx[j][e] + kGrow;
-                }
-            if (__any_sync(0xffffffffu, grown)) {
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    float co[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float bm = fmaxf(sc[j][e], sc[j][2 + e]);
-#pragma unroll
-                        for (int k = 4; k < 32; k <<= 1)
-                            bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, k));
-                        const float m1 = fmaxf(mx[j][e], bm);
-                        co[e] = exp2f(mx[j][e] - (m1 == -INFINITY ? 0.0f : m1));
-                        mx[j][e] = m1;
-                        den[j][e] *= co[e];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        o[j][i][0] *= co[0]; o[j][i][1] *= co[1];
-                        o[j][i][2] *= co[0]; o[j][i][3] *= co[1];
-                    }
-                }
-            }
+                for (int e = 0; e < 2; ++e)
+                    grown = grown || fmaxf(v[j][e], v[j][2 + e]) > top[j][e] + kGrow;
+            if (!__any_sync(0xffffffffu, grown)) return false;
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float ms = mx[j][e] == -INFINITY ? 0.0f : mx[j][e];
+                    float bm = fmaxf(v[j][e], v[j][2 + e]);
+#pragma unroll
+                    for (int k = 4; k < 32; k <<= 1)
+                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, k));
+                    const float m1 = fmaxf(top[j][e], bm);
+                    co[j][e] = exp2f(top[j][e] - (m1 == -INFINITY ? 0.0f : m1));
+                    top[j][e] = m1;
+                }
+            return true;
+        };
+        auto rescale = [&](const float (&co)[NT][2]) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    o[j][i][0] *= co[j][0]; o[j][i][1] *= co[j][1];
+                    o[j][i][2] *= co[j][0]; o[j][i][3] *= co[j][1];
+                }
+        };
+        auto weigh = [&](const float (&top)[NT][2]) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float ms = top[j][e] == -INFINITY ? 0.0f : top[j][e];
                     w[j][e] = exp2f(sc[j][e] - ms);
                     w[j][2 + e] = exp2f(sc[j][2 + e] - ms);
-                    den[j][e] += w[j][e] + w[j][2 + e];
                 }
+        };
+        if (live) {
+            const float fa = qs * ka, fb = qs * kb;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float d0 = pow2f(down[j][e] / 2), d1 = pow2f(down[j][e] - down[j][e] / 2);
+                    const float s0 = kE4m3 ? sc[j][e] * d0 * d1 : sc[j][e];
+                    const float s1 = kE4m3 ? sc[j][2 + e] * d0 * d1 : sc[j][2 + e];
+                    sc[j][e] = tok <= lim[j][e] ? s0 * fa : -INFINITY;
+                    sc[j][2 + e] = tok + 8 <= lim[j][e] ? s1 * fb : -INFINITY;
+                }
+            float co[NT][2];
+            if (raise(mx, sc, co)) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    den[j][0] *= co[j][0];
+                    den[j][1] *= co[j][1];
+                }
+                if (!kE4m3) rescale(co);
+            }
+            weigh(mx);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                den[j][0] += w[j][0] + w[j][2];
+                den[j][1] += w[j][1] + w[j][3];
+            }
         }
         if (!warp_wait(&c.v_full[vs], (n / S::kNV) & 1, ab)) return;
         if (live) {
             uint8_t* vt = smem + (S::kNK + vs) * S::kTile;
             const int t0 = m.block * kFewBlock + 16 * warp;
-            float va = 1.0f, vb = 1.0f;
+            int ea = 0, eb = 0;    // exponents of the V rows' scales
             if (kE4m3) {
                 const uint8_t* sp = smem + S::kScales + (S::kNK + vs) * kFewBlock + 16 * warp + pg;
-                va = scale_value(sp[0]);
-                vb = scale_value(sp[8]);
+                ea = sp[0] - 127;
+                eb = sp[8] - 127;
             }
-            // What no row or not every row may see must not reach them: 0 * NaN is NaN. Codes
-            // are finite whatever they are and the weights below select; a NaN row of the chunk
-            // itself, or what is not finite in a bf16 row, is taken out and put back at the end
-            // into the rows that see it; rows behind the end of the sequence are cleared.
+            // What no row or not every row may see must not reach them: 0 * NaN is NaN. So rows
+            // behind the end of the sequence are cleared, and what is not finite in the rows of
+            // the chunk itself (8-bit: a NaN row) is taken out and put back at the end into the
+            // rows that see it.
             if (t0 + 15 > shared && (sg.end - 1 > shared || t0 + 15 >= sg.end)) {
                 int32_t* bad_at = c.bad[seg & 1];
-                if (kE4m3) {
-                    int bad = INT32_MAX;
-                    if (tok + 8 > shared && tok + 8 < sg.end && vb != vb) { bad = tok + 8; vb = 0.0f; }
-                    if (tok > shared && tok < sg.end && va != va) { bad = tok; va = 0.0f; }
-                    bad = __reduce_min_sync(0xffffffffu, bad);
-                    if (bad != INT32_MAX)
-                        for (int i = 0; i < 4; ++i) atomicMin(&bad_at[4 * lane + i], bad);
-                } else {
+                constexpr int kPieces = S::kRowB / 16;
 #pragma unroll 1
-                    for (int i = lane; i < 16 * 16; i += 32) {      // 16 rows of 16 pieces
-                        const int row = 16 * warp + (i >> 4), ch = i & 15, tk = t0 + (i >> 4);
-                        if (tk <= shared) continue;
-                        uint4* e = reinterpret_cast<uint4*>(vt + (ch >> 3) * (S::kTile / 2) +
-                                                            row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-                        if (tk >= sg.end) {
-                            *e = make_uint4(0, 0, 0, 0);
-                            continue;
-                        }
-                        const uint4 y = *e;
-                        uint32_t u[4] = {y.x, y.y, y.z, y.w};
-                        bool odd = false;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if ((u[k] & 0x7f80u) == 0x7f80u) {
-                                atomicMin(&bad_at[8 * ch + 2 * k], tk);
-                                u[k] &= 0xffff0000u;
-                                odd = true;
-                            }
-                            if ((u[k] & 0x7f800000u) == 0x7f800000u) {
-                                atomicMin(&bad_at[8 * ch + 2 * k + 1], tk);
-                                u[k] &= 0xffffu;
-                                odd = true;
-                            }
-                        }
-                        if (odd) *e = make_uint4(u[0], u[1], u[2], u[3]);
+                for (int i = lane; i < 16 * kPieces; i += 32) {
+                    const int r16 = i / kPieces, ch = i % kPieces, row = 16 * warp + r16;
+                    const int tk = t0 + r16;
+                    if (tk <= shared) continue;
+                    uint4* e = reinterpret_cast<uint4*>(vt + (ch >> 3) * (S::kTile / 2) + row * 128 +
+                                                        (((ch & 7) ^ (row & 7)) << 4));
+                    if (tk >= sg.end) {
+                        *e = make_uint4(0, 0, 0, 0);
+                        continue;
                     }
-                    fence_async_smem();
-                    __syncwarp();
-                }
-            }
-            // the weights as B fragments (k = tokens, n = rows)
+                    if (kE4m3) {
+                        if (smem[S::kScales + (S::kNK + vs) * kFewBlock + row] != kNanRow) continue;
+                        for (int k = 0; k < 16; ++k) atomicMin(&bad_at[16 * ch + k], tk);
+                        *e = make_uint4(0, 0, 0, 0);
+                        continue;
+                    }
+                    const uint4 y = *e;
+                    uint32_t u[4] = {y.x, y.y, y.z, y.w};
+                    bool odd = false;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                if (kE4m3) {   // (a masked token's scale may be anything)
+                    for (int k = 0; k < 4; ++k) {
+                        if ((u[k] & 0x7f80u) == 0x7f80u) {
+                            atomicMin(&bad_at[8 * ch + 2 * k], tk);
+                            u[k] &= 0xffff0000u;
+                            odd = true;
+                        }
+                        if ((u[k] & 0x7f800000u) == 0x7f800000u) {
+                            atomicMin(&bad_at[8 * ch + 2 * k + 1], tk);
+                            u[k] &= 0xffffu;
+                            odd = true;
+                        }
+                    }
+                    if (odd) *e = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+                if (kE4m3) {   // (a cleared NaN row weighs nothing)
+                    if (tok > shared && ea == kNanRow - 127) ea = -INT32_MAX / 2;
+                    if (tok + 8 > shared && eb == kNanRow - 127) eb = -INT32_MAX / 2;
+                }
+                fence_async_smem();
+                __syncwarp();
+            }
+            if (kE4m3) {
+                // the weights of O: with V's scales in the exponent, relative to maxima of their own
+                float co[NT][2];
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        w[j][e] = tok <= lim[j][e] ? w[j][e] * va : 0.0f;
-                        w[j][2 + e] = tok + 8 <= lim[j][e] ? w[j][2 + e] * vb : 0.0f;
+                        sc[j][e] += static_cast<float>(ea);
+                        sc[j][2 + e] += static_cast<float>(eb);
                     }
-                }
+                if (raise(mw, sc, co)) rescale(co);
+                weigh(mw);
+            }
+            // as B fragments (k = tokens, n = rows), in parts
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int k = 0; k < kParts; ++k) {
-                    const uint32_t h01 = bf2(w[j][0], w[j][1]), h23 = bf2(w[j][2], w[j][3]);
+                    const uint32_t h01 = kE4m3 ? h2(w[j][0], w[j][1]) : bf2(w[j][0], w[j][1]);
+                    const uint32_t h23 = kE4m3 ? h2(w[j][2], w[j][3]) : bf2(w[j][2], w[j][3]);
                     pb[j][k][0] = movm_t(h01);
                     pb[j][k][1] = movm_t(h23);
-                    const float2 f01 = bf2_f(h01), f23 = bf2_f(h23);
+                    const float2 f01 = kE4m3 ? h2_f(h01) : bf2_f(h01);
+                    const float2 f23 = kE4m3 ? h2_f(h23) : bf2_f(h23);
                     w[j][0] -= f01.x; w[j][1] -= f01.y; w[j][2] -= f23.x; w[j][3] -= f23.y;
                 }
-            }
             // O^T += V^T P^T. MMA i covers elements 16 i + g and 16 i + g + 8 of a row (bf16),
             // or 16 pg + 2 i and 16 pg + 2 i + 1 (8-bit)
             if (kE4m3) {
@@ -578,24 +660,20 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int u = i >> 1;
-                    // the same element of two neighbouring tokens, side by side
+                    // two elements of two neighbouring tokens: a pair a register
                     uint32_t f[4];
-                    if (i & 1) {
-                        f[0] = widen2(prmt_i<0x6020>(wv[0][u], wv[1][u]));
-                        f[1] = widen2(prmt_i<0x7030>(wv[0][u], wv[1][u]));
-                        f[2] = widen2(prmt_i<0x6020>(wv[2][u], wv[3][u]));
-                        f[3] = widen2(prmt_i<0x7030>(wv[2][u], wv[3][u]));
-                    } else {
-                        f[0] = widen2(prmt_i<0x4000>(wv[0][u], wv[1][u]));
-                        f[1] = widen2(prmt_i<0x5010>(wv[0][u], wv[1][u]));
-                        f[2] = widen2(prmt_i<0x4000>(wv[2][u], wv[3][u]));
-                        f[3] = widen2(prmt_i<0x5010>(wv[2][u], wv[3][u]));
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t y = i & 1 ? prmt_i<0x7362>(wv[2 * k][u], wv[2 * k + 1][u])
+                                                 : prmt_i<0x5140>(wv[2 * k][u], wv[2 * k + 1][u]);
+                        f[2 * k] = widen_lo(y);
+                        f[2 * k + 1] = widen_hi(y);
                     }
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
                         for (int k = 0; k < kParts; ++k)
-                            mma_bf16(o[j][i], f, pb[j][k][0], pb[j][k][1]);
+                            mma16<kE4m3>(o[j][i], f, pb[j][k][0], pb[j][k][1]);
                 }
             } else {
                 const int row = 16 * warp + j8 + 8 * (mi >> 1), vc = mi & 1;
@@ -609,7 +687,7 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
                         for (int k = 0; k < kParts; ++k)
-                            mma_bf16(o[j][i], f, pb[j][k][0], pb[j][k][1]);
+                            mma16<kE4m3>(o[j][i], f, pb[j][k][0], pb[j][k][1]);
                 }
             }
         }
@@ -635,6 +713,7 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                 if (g == 0) {
                     p[D] = mx[j][e];
                     p[D + 1] = den[j][e];
+                    p[D + 2] = kE4m3 ? mw[j][e] : mx[j][e];
                 }
             }
             if (!meet()) return;
@@ -649,8 +728,8 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
 #pragma unroll
                 for (int x = 0; x < kFW; ++x) {
                     const float* src = scr + (x * 8 + r8) * kPart;
-                    const float f = exp2f(src[D] - ms);
-                    dn += src[D + 1] * f;
+                    dn += src[D + 1] * exp2f(src[D] - ms);
+                    const float f = exp2f(src[D + 2] - ms);
                     const float4 z = *reinterpret_cast<const float4*>(src + 4 * lane);
                     y[0] += z.x * f; y[1] += z.y * f; y[2] += z.z * f; y[3] += z.w * f;
                 }
@@ -746,7 +825,7 @@ template <bool kE4m3, int NT>
 cudaError_t launch_few_out(const AttendArgs& a, const CUtensorMap maps[2], bool f32_out, int ctas,
                            bool inline_plan, cudaStream_t st) {
     return f32_out ? launch_few<kE4m3, NT, 3, float>(a, maps, ctas, inline_plan, st)
-                   : launch_few<kE4m3, NT, 2, __nv_bfloat16>(a, maps, ctas, inline_plan, st);
+                   : launch_few<kE4m3, NT, kE4m3 ? 1 : 2, __nv_bfloat16>(a, maps, ctas, inline_plan, st);
 }
 
 }  // namespace

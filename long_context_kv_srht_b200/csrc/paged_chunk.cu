@@ -359,8 +359,10 @@ __device__ void mma_role(Shared& sh, uint8_t* smem, uint32_t tmem, int half, boo
         }
         const uint32_t turn = nt + ahead;
         if (has_rows(flags)) {
-            // they go where the weights of two turns ago were read
-            if (turn >= 2 && !warp_wait(&sh.pv_done[half], turn & 1, ab)) return false;
+            // they go where the weights of two turns ago were read. (A phase may be waited for while
+            // it is the current or the last one, no longer: where blocks without rows lie between,
+            // the next product is issued too, and had waited for this one itself)
+            if (turn >= 2 && nt < turn && !warp_wait(&sh.pv_done[half], turn & 1, ab)) return false;
             tc_fence_after();
             const uint64_t k = uniform(k_desc + (u % S::kStages) * (kStageB >> 4) + w * (kTurn * 128 >> 4));
             const uint32_t d = uniform(s_at + kTurn * (turn & 1));
@@ -391,6 +393,7 @@ __device__ void mma_role(Shared& sh, uint8_t* smem, uint32_t tmem, int half, boo
             }
         }
         if (has_rows(flags)) {
+            if (nt >= 1 && !warp_wait(&sh.pv_done[half], (nt - 1) & 1, ab)) return false;
             if (!warp_wait(&sh.p_full[half][nt & 1], nt >> 1 & 1, ab)) return false;
             tc_fence_after();
             const uint64_t v = uniform(v_desc + st * (kStageB >> 4) + w * (kTurn * 128 >> 4));

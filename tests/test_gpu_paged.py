@@ -240,8 +240,9 @@ def test_attend_lengths(fmt, out_dtype, causal, q, kv):
 @pytest.mark.parametrize("page", [16, 64, 256])
 def test_attend_head_layouts_and_pages(fmt, heads, group, page):
     c = Case(group * 31 + page, fmt, [1, 4, 33], [70, 4, 290], heads=heads, group=group, page=page)
-    out, lse = _attend(c)
-    c.check(out, lse, True)
+    for out_dtype in (torch.bfloat16, torch.float32):   # (with tiles of 125 rows: group 5, fp32)
+        out, lse = _attend(c, out_dtype=out_dtype)
+        c.check(out, lse, True)
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
@@ -370,6 +371,22 @@ def test_many_sequences():
     c = Case(1, "e4m3", q, kv, heads=1, group=2, page=16)
     out, lse = _attend(c)
     c.check(out, lse, True)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+def test_many_tiles_a_cta(fmt, out_dtype, causal):
+    """A ragged batch that gives each CTA many tiles one after the other: full ones, ones with few
+    rows, ones without a single page, single blocks and long ones, in every order."""
+    rng = np.random.default_rng(3)
+    q = [int(rng.choice([1, 3, 33, 64, 70, 129])) for _ in range(48)]
+    kv = [a + int(rng.choice([0, 5, 130, 700])) for a in q]
+    holes = [(s, p) for s in range(0, 48, 5) for p in range((kv[s] + 31) // 32) if s % 10 or p % 3]
+    c = Case(5, fmt, q, kv, heads=4, group=4, page=32, holes=holes)
+    out, lse = _attend(c, causal, out_dtype)
+    pk.paged_sync()
+    c.check(out, lse, causal)
 
 
 def test_refusals_with_device_buffers():
