@@ -10,7 +10,6 @@ namespace pkv {
 namespace {
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-constexpr uint32_t kNapNs = 20000;
 
 __device__ int g_wait_status;   // ST_TIMEOUT after a wait ran out (one word a source file)
 
@@ -21,25 +20,19 @@ __device__ __forceinline__ uint64_t now_ns() {
 }
 
 // Waits for the phase of `parity` to complete; false once a wait of this CTA has run out. The
-// thread sleeps in the instruction for up to kNapNs at a time (or until the phase is complete): a
-// spinning warp would take issue slots from the softmax.
-__device__ __forceinline__ bool try_wait_nap(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok) : "r"(bar), "r"(parity), "r"(kNapNs) : "memory");
-    return ok != 0;
-}
-// (out of line: the roles' loops have to share the instruction caches)
+// instruction holds the warp for a while by itself; the rest of a longer wait is out of line (the
+// roles' loops have to share the instruction caches) and short (a spinning warp takes issue slots
+// and power from the others).
 __device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, volatile int32_t* abort,
                                        uint64_t limit) {
-    const uint64_t t0 = now_ns();
+    uint64_t t0 = 0;
 #pragma unroll 1
-    while (!try_wait_nap(bar, parity)) {
+    for (int i = 1; !mbar_try_wait(bar, parity); ++i) {
+        if (i & 127) continue;
         if (*abort) return false;
-        if (now_ns() - t0 > limit) {
+        const uint64_t t = now_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > limit) {
             *abort = 1;
             atomicExch(&g_wait_status, ST_TIMEOUT);
             return false;
@@ -50,7 +43,7 @@ __device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, volatile i
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int32_t* abort,
                                          uint64_t limit = kWaitLimitNs) {
     const uint32_t b = smem_addr(bar);
-    return try_wait_nap(b, parity) || wait_more(b, parity, abort, limit);
+    return mbar_try_wait(b, parity) || wait_more(b, parity, abort, limit);
 }
 // the same by a whole warp, which goes on together
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,

@@ -7,11 +7,11 @@
 // tensor cores and the exponential units busy at the same time:
 //  - a tile is 2 x 128 query rows (tokens x heads of one KV head's group) against blocks of 128
 //    tokens, so a K or V block that has come to shared memory serves 256 rows;
-//  - one thread a half issues its products; S of both halves (2 x 128 columns) and O of both halves (2 x
+//  - S of both halves (2 x 128 columns) and O of both halves (2 x
 //    128 columns) fill the 512 columns of tensor memory; P overwrites S as bf16 and is the second
 //    product's operand from there, so neither S nor P ever touches shared memory;
-//  - two warpgroups do the softmax, one a half, a thread a row (no shuffles): while one half's
-//    rows are in the exponentials the tensor cores work for the other half;
+//  - two warpgroups do the softmax, one a half, a thread a row (no shuffles); a block is taken in
+//    two turns of 64 tokens, and the scores of the next turn are there before this one's are done;
 //  - O is rescaled only when a row's maximum has grown by more than 2^8 since the last time (P is
 //    then at most 2^8, which costs bf16 nothing), so tensor memory is not read back each block;
 //  - K, V and Q tiles come by TMA through a ring of 32 KB stages, one copy a page and 64 columns;
@@ -26,8 +26,8 @@
 // fp32 output takes P in three bf16 parts (24 bits, three products); the parts of one half then
 // take the other half's columns, and a tile is 128 rows.
 //
-// Roles, by warp: 0-3 and 4-7 softmax and output of the halves, 8 loads, 9 and 10 the halves'
-// products, 11 and up repair (bf16) or widening (8-bit). They meet in mbarriers; every wait gives up after
+// Roles, by warp: 0-3 and 4-7 softmax and output of the halves, 8 loads, 9 to 12 the halves'
+// scores and products, 13 and up repair (bf16) or widening (8-bit). They meet in mbarriers; every wait gives up after
 // kWaitLimitNs, which ends the whole CTA in order and reaches the caller as a status.
 #include "paged_async.cuh"
 
@@ -49,7 +49,9 @@ template <bool kE4m3, int kParts> struct Shape {
     static constexpr int kStages = kE4m3 ? 3 : 4;
     static constexpr int kRaw = kE4m3 ? 3 : 0;
     static constexpr int kAuxWarps = kE4m3 ? 5 : 1;
-    static constexpr int kThreads = (11 + kAuxWarps) * 32;
+    static constexpr int kSoft = 4 * kHalves;                 // softmax warps
+    static constexpr int kAux0 = kSoft + 1 + 2 * kHalves;     // first of the others
+    static constexpr int kThreads = (kAux0 + kAuxWarps) * 32;
     // tensor memory columns
     static constexpr int kS = 0;                              // + 128 half + 64 turn
     static constexpr int kP = kParts == 1 ? 0 : 128;          // + 128 half, + kPTurn turn, + 32 part
@@ -83,8 +85,7 @@ struct Seg {
 
 struct Shared {
     uint64_t info_full[kRing], info_empty[kRing], bad_full[kRing];
-    uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], pv_done[2], o_full[2], drain[2];
-    uint64_t exp_turn[2][4];   // whose turn at the exponential units, by a half's 32 rows
+    uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], pv_done[2][2], o_full[2], drain[4];
     uint64_t kv_full[4], kv_empty[4], fixed[4], raw_full[4], raw_empty[4];
     Entry entry[kRing];
     Seg seg[kRing];
@@ -314,145 +315,122 @@ __device__ void load_role(const AttendArgs& a, const CUtensorMap* mq, const CUte
 }
 
 // ------------------------------------------------------------------------------- products
-// A warp a half, so that the books of one are kept while the other's products run. The whole warp
-// keeps them (the compiler then sees uniform values); one elected thread issues. A block is taken
-// in two turns of 64 tokens, each with its own columns of S and P, and the scores of the next turn
-// are issued before the weights of this one are there: the softmax never waits for the products'
-// latency. (Scores of 64 tokens cost 1.5 times their share of 128 tokens' - Q is read from shared
-// memory for half as many columns - which is less than the waits were.)
+// Two warps a half, one for the scores and one for the weights' product: what each waits for and
+// looks up (some 100 cycles a wait) hides behind the other three's products. A whole warp keeps
+// the books (the compiler then sees uniform values); one elected thread issues. A block is taken
+// in two turns of 64 tokens, each with its own columns of S and P, and the scores of a turn are
+// issued as soon as the weights of the turn two before it have been used: the softmax never waits
+// for the products' latency. (Scores of 64 tokens cost 1.5 times their share of 128 tokens' - Q is
+// read from shared memory for half as many columns - which is less than the waits were.)
+
+// The flags of the next block with work and kSome, 0 at the end, -1 after a wait ran out.
+constexpr int kSome = 64;
+__device__ __forceinline__ int next_block(Shared& sh, uint32_t& n, bool leader) {
+    while (true) {
+        const int slot = n % kRing;
+        if (!warp_wait(&sh.info_full[slot], (n / kRing) & 1, &sh.abort)) return -1;
+        const int f = sh.entry[slot].flags, b = sh.entry[slot].block;
+        __syncwarp();
+        if (leader) arrive(&sh.info_empty[slot]);
+        ++n;
+        if (b >= 0) return f | kSome;
+        if (f & kEnd) return 0;
+    }
+}
+
 template <bool kE4m3, int kParts>
-__device__ void mma_role(Shared& sh, uint8_t* smem, uint32_t tmem, int half, bool inject) {
+__device__ void score_role(Shared& sh, uint8_t* smem, uint32_t tmem, int half, bool inject) {
     using S = Shape<kE4m3, kParts>;
-    constexpr uint32_t kQK = mma_desc(kTurn, false), kPV = mma_desc(D, true);
+    constexpr uint32_t kQK = mma_desc(kTurn, false);
     volatile int32_t* ab = &sh.abort;
     const bool leader = elect_one();
-    uint32_t n = 0, nq = 0, nt = 0, fix = 0;   // nt: turns of the half
-    constexpr int kSome = 64;   // a block's flags are never 0
-    // flags of the next block with work, 0 at the end, -1 after a wait ran out
-    auto fetch = [&]() -> int {
-        while (true) {
-            const int slot = n % kRing;
-            if (!warp_wait(&sh.info_full[slot], (n / kRing) & 1, ab)) return -1;
-            const int f = sh.entry[slot].flags, b = sh.entry[slot].block;
-            __syncwarp();
-            if (leader) arrive(&sh.info_empty[slot]);
-            ++n;
-            if (b >= 0) return f | kSome;
-            if (f & kEnd) return 0;
-        }
-    };
     const uint64_t q_desc = smem_desc(uniform(smem_addr(smem + S::kQ + half * kStageB)), 16);
     const uint64_t k_desc = smem_desc(uniform(smem_addr(smem + S::kKV)), 16);
-    const uint64_t v_desc = smem_desc(uniform(smem_addr(smem + S::kKV)), kHalfB);
-    const uint32_t s_at = uniform(tmem + S::kS + 128 * half),
-                   o_at = uniform(tmem + S::kO + 128 * half),
-                   p_at = uniform(tmem + S::kP + 128 * half);
-    auto tile_ready = [&](uint32_t u) -> bool {
-        return warp_wait(&sh.kv_full[u % S::kStages], (u / S::kStages) & 1, ab);
-    };
-    auto has_rows = [&](int flags) -> bool { return half == 0 || (flags & kTwo); };
-    // scores of turn `nt + ahead` from the K tile u
-    auto qk = [&](int flags, uint32_t u, int w, int ahead) -> bool {
-        if (w == 0) {
-            if ((flags & kFirst) && !warp_wait(&sh.q_full, nq++ & 1, ab)) return false;
-            if (!tile_ready(u)) return false;
-        }
-        const uint32_t turn = nt + ahead;
-        if (has_rows(flags)) {
-            // they go where the weights of two turns ago were read. (A phase may be waited for while
-            // it is the current or the last one, no longer: where blocks without rows lie between,
-            // the next product is issued too, and had waited for this one itself)
-            if (turn >= 2 && nt < turn && !warp_wait(&sh.pv_done[half], turn & 1, ab)) return false;
-            tc_fence_after();
-            const uint64_t k = uniform(k_desc + (u % S::kStages) * (kStageB >> 4) + w * (kTurn * 128 >> 4));
-            const uint32_t d = uniform(s_at + kTurn * (turn & 1));
-            if (leader) {
-#pragma unroll
-                for (int j = 0; j < D / 16; ++j) {
-                    const uint32_t at = ((j >> 2) * kHalfB + (j & 3) * 32) >> 4;
-                    mma_ss(d, q_desc + at, k + at, kQK, j > 0);
-                }
-                mma_commit(smem_addr(&sh.s_full[half][turn & 1]));
-            }
-        }
-        if (w == 1 && leader) {
-            mma_commit(smem_addr(&sh.kv_empty[u % S::kStages]));
-            if (flags & kLast) mma_commit(smem_addr(&sh.q_empty));
-        }
-        __syncwarp();
-        return true;
-    };
-    // O += P V of turn `nt` with the V tile u
-    auto pv = [&](int flags, uint32_t u, int w) -> bool {
-        const int st = u % S::kStages;
-        if (w == 0) {
-            if (!tile_ready(u)) return false;
-            if (!kE4m3 && (flags & kFix)) {
-                if (!warp_wait(&sh.fixed[st], fix >> st & 1, ab)) return false;
-                fix ^= 1u << st;
-            }
-        }
-        if (has_rows(flags)) {
-            if (nt >= 1 && !warp_wait(&sh.pv_done[half], (nt - 1) & 1, ab)) return false;
-            if (!warp_wait(&sh.p_full[half][nt & 1], nt >> 1 & 1, ab)) return false;
-            tc_fence_after();
-            const uint64_t v = uniform(v_desc + st * (kStageB >> 4) + w * (kTurn * 128 >> 4));
-            const uint32_t p0 = uniform(p_at + S::kPTurn * (nt & 1));
-            if (leader) {
-#pragma unroll
-                for (int p = 0; p < kParts; ++p)
-#pragma unroll
-                    for (int j = 0; j < kTurn / 16; ++j)
-                        mma_ts(o_at, p0 + 32 * p + 8 * j, v + ((j * 16 * 128) >> 4), kPV,
-                               !(flags & kFirst) || w > 0 || p > 0 || j > 0);
-                mma_commit(smem_addr(&sh.pv_done[half]));
-                if ((flags & kLast) && w == 1) mma_commit(smem_addr(&sh.o_full[half]));
-            }
-            ++nt;
-        }
-        if (w == 1 && leader) mma_commit(smem_addr(&sh.kv_empty[st]));
-        __syncwarp();
-        return true;
-    };
-
+    const uint32_t s_at = uniform(tmem + S::kS + 128 * half);
     if (inject) {   // test hook: a wait for an arrival that never comes
         wait_for(&sh.raw_full[3], 0, ab, 1000000ull);
         return;
     }
-    // the turn whose scores come next (flags of its block, its K tile, which half of it), and the
-    // one behind it whose weights come next
-    int fq = fetch(), wq = 0, fp = fq, wp = 0;
-    uint32_t uq = 0, up = 1;
-    if (fq <= 0) return;
-    bool ahead = false;
+    uint32_t n = 0, nq = 0, nb = 0, used = 0;   // entries, Q tiles, blocks of the half, K/V tiles
 #pragma unroll 1
     while (true) {
-        if (fq > 0) {
-            if (!qk(fq, uq, wq, ahead && has_rows(fp) ? 1 : 0)) return;
-            if (wq == 0) {
-                wq = 1;
-            } else {
-                // (the ring holds a tile's V behind its K, and the next K behind that; none of
-                // them waits for the products issued here to make room)
-                fq = fetch();
-                if (fq < 0) return;
-                uq += 2;
-                wq = 0;
+        const int flags = next_block(sh, n, leader);
+        if (flags <= 0) return;
+        const int st = used % S::kStages;
+        if ((flags & kFirst) && !warp_wait(&sh.q_full, nq++ & 1, ab)) return;
+        if (!warp_wait(&sh.kv_full[st], (used / S::kStages) & 1, ab)) return;
+        const bool mine = half == 0 || (flags & kTwo);
+        const uint64_t k0 = uniform(k_desc + st * (kStageB >> 4));
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            if (mine) {
+                // they go where the weights of the same turn of the last block were read
+                if (nb > 0 && !warp_wait(&sh.pv_done[half][w], (nb - 1) & 1, ab)) return;
+                tc_fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        const uint32_t at = ((j >> 2) * kHalfB + (j & 3) * 32) >> 4;
+                        mma_ss(s_at + kTurn * w, q_desc + at, k0 + (w * kTurn * 128 >> 4) + at, kQK,
+                               j > 0);
+                    }
+                    mma_commit(smem_addr(&sh.s_full[half][w]));
+                }
             }
         }
-        if (!ahead) {
-            ahead = true;
-            continue;
+        if (leader) {
+            mma_commit(smem_addr(&sh.kv_empty[st]));
+            if (flags & kLast) mma_commit(smem_addr(&sh.q_empty));
         }
-        if (!pv(fp, up, wp)) return;
-        if (wp == 0) {
-            wp = 1;
-        } else {
-            fp = fq;
-            wp = 0;
-            up += 2;
-            if (fp == 0) return;
+        __syncwarp();
+        nb += mine ? 1 : 0;
+        used += 2;
+    }
+}
+
+template <bool kE4m3, int kParts>
+__device__ void weight_role(Shared& sh, uint8_t* smem, uint32_t tmem, int half) {
+    using S = Shape<kE4m3, kParts>;
+    constexpr uint32_t kPV = mma_desc(D, true);
+    volatile int32_t* ab = &sh.abort;
+    const bool leader = elect_one();
+    const uint64_t v_desc = smem_desc(uniform(smem_addr(smem + S::kKV)), kHalfB);
+    const uint32_t o_at = uniform(tmem + S::kO + 128 * half), p_at = uniform(tmem + S::kP + 128 * half);
+    uint32_t n = 0, nb = 0, used = 1, fix = 0;
+#pragma unroll 1
+    while (true) {
+        const int flags = next_block(sh, n, leader);
+        if (flags <= 0) return;
+        const int st = used % S::kStages;
+        if (!warp_wait(&sh.kv_full[st], (used / S::kStages) & 1, ab)) return;
+        if (!kE4m3 && (flags & kFix)) {
+            if (!warp_wait(&sh.fixed[st], fix >> st & 1, ab)) return;
+            fix ^= 1u << st;
         }
+        const bool mine = half == 0 || (flags & kTwo);
+        const uint64_t v0 = uniform(v_desc + st * (kStageB >> 4));
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            if (mine) {
+                if (!warp_wait(&sh.p_full[half][w], nb & 1, ab)) return;
+                tc_fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                        for (int j = 0; j < kTurn / 16; ++j)
+                            mma_ts(o_at, p_at + S::kPTurn * w + 32 * p + 8 * j,
+                                   v0 + ((w * kTurn * 128 + j * 16 * 128) >> 4), kPV,
+                                   !(flags & kFirst) || w > 0 || p > 0 || j > 0);
+                    mma_commit(smem_addr(&sh.pv_done[half][w]));
+                    if ((flags & kLast) && w == 1) mma_commit(smem_addr(&sh.o_full[half]));
+                }
+            }
+        }
+        if (leader) mma_commit(smem_addr(&sh.kv_empty[st]));
+        __syncwarp();
+        nb += mine ? 1 : 0;
+        used += 2;
     }
 }
 
@@ -472,17 +450,8 @@ __device__ void softmax_role(const AttendArgs& a, Shared& sh, uint32_t tmem, int
     const float sign = a.scale > 0.0f ? 1.0f : a.scale < 0.0f ? -1.0f : 0.0f;
 
     uint32_t n = 0, seg = 0, nt = 0, no = 0;   // entries, segments; turns, outputs of this half
-    uint32_t nx = 0;                    // turns at the exponential units
     float m = -INFINITY, l = 0.0f;      // the row's maximum (times c) as last used, and its sum
     int lim = -1;
-    auto exp_wait = [&]() -> bool {
-        return S::kHalves == 1 ||
-               warp_wait(&sh.exp_turn[half][quad], (nx & 1) ^ (half == 0 ? 1 : 0), ab);
-    };
-    auto exp_done = [&]() {
-        ++nx;
-        if (S::kHalves == 2 && lane == 0) arrive(&sh.exp_turn[half ^ 1][quad]);
-    };
     while (true) {
         const int slot = n % kRing;
         if (!warp_wait(&sh.info_full[slot], (n / kRing) & 1, ab)) return;
@@ -540,7 +509,7 @@ __device__ void softmax_role(const AttendArgs& a, Shared& sh, uint32_t tmem, int
                     l *= f;
                     // the last product into O has to be there before it is rescaled (the one
                     // before it is: its weights' columns hold these scores)
-                    if (!warp_wait(&sh.pv_done[half], (nt - 1) & 1, ab)) return;
+                    if (!warp_wait(&sh.pv_done[half][turn ^ 1], (nt - 1) >> 1 & 1, ab)) return;
                     tc_fence_after();
 #pragma unroll 1
                     for (int i = 0; i < 8; ++i) {
@@ -553,11 +522,7 @@ __device__ void softmax_role(const AttendArgs& a, Shared& sh, uint32_t tmem, int
                         tmem_st16(at0 + S::kO + 16 * i, o);
                     }
                 }
-                float ms = m == -INFINITY ? 0.0f : m;
-                // the two warps of an SM quarter (one of each half) take turns at its exponential
-                // units: left alone they run in step, and the units idle while both do the rest
-                if (!exp_wait()) return;
-                asm volatile("" : "+f"(ms));   // (not before the wait)
+                const float ms = m == -INFINITY ? 0.0f : m;
                 const uint64_t c2 = pack2(c, c), m2 = pack2(-ms, -ms);
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -595,19 +560,12 @@ __device__ void softmax_role(const AttendArgs& a, Shared& sh, uint32_t tmem, int
                         tmem_st16(at0 + S::kP + S::kPTurn * turn + 32 * k + 16 * q, x);
                     }
                 }
-                exp_done();
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive(&sh.p_full[half][turn]);
                 const float2 y = unpack2(add2(sum[0], sum[1]));
                 l += y.x + y.y;
-            }
-        }
-        if (!mine && !(flags & kEmpty)) {   // (both halves count the same turns)
-            for (int w = 0; w < 2; ++w) {
-                if (!exp_wait()) return;
-                exp_done();
             }
         }
         if (flags & kLast) {
@@ -686,7 +644,7 @@ template <bool kE4m3, int kParts>
 __device__ void aux_role(const AttendArgs& a, Shared& sh, uint8_t* smem) {
     using S = Shape<kE4m3, kParts>;
     constexpr int kT = S::kAuxWarps * 32;
-    const int tid = threadIdx.x - 11 * 32, lane = tid & 31;
+    const int tid = threadIdx.x - S::kAux0 * 32, lane = tid & 31;
     volatile int32_t* ab = &sh.abort;
     uint32_t n = 0, seg = 0, use = 0;   // use: tiles of the ring seen
     while (true) {
@@ -836,7 +794,7 @@ attend_chunk_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap mq,
         auto init = [&](uint64_t* b, uint32_t count) { mbar_init(smem_addr(b), count); };
         for (int i = 0; i < kRing; ++i) {
             init(&sh.info_full[i], 1);
-            init(&sh.info_empty[i], 5 * S::kHalves + S::kAuxWarps);
+            init(&sh.info_empty[i], S::kSoft + 2 * S::kHalves + S::kAuxWarps);
             init(&sh.bad_full[i], S::kAuxWarps);
         }
         init(&sh.q_full, 1);
@@ -844,12 +802,12 @@ attend_chunk_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap mq,
         for (int i = 0; i < 2; ++i) {
             for (int k = 0; k < 2; ++k) {
                 init(&sh.s_full[i][k], 1);
+                init(&sh.pv_done[i][k], 1);
                 init(&sh.p_full[i][k], 4);
             }
-            init(&sh.pv_done[i], 1);
             init(&sh.o_full[i], 1);
-            for (int k = 0; k < 4; ++k) init(&sh.exp_turn[i][k], 1);
-            init(&sh.drain[i], 1);
+            init(&sh.drain[2 * i], 1);
+            init(&sh.drain[2 * i + 1], 1);
         }
         for (int i = 0; i < 4; ++i) {
             init(&sh.kv_full[i], kE4m3 ? S::kAuxWarps : 1);
@@ -863,7 +821,7 @@ attend_chunk_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap mq,
         tma_prefetch_map(&mk);
         tma_prefetch_map(&mv);
     }
-    if (warp == 9) {
+    if (warp == S::kSoft + 1) {
         tmem_alloc(smem_addr(&sh.tmem), 512);
         tmem_relinquish();
     }
@@ -883,33 +841,34 @@ attend_chunk_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap mq,
 
     if (!work) {
         // nothing to do but to give the tensor memory back
-    } else if (warp < 8) {
-        if (warp < 4 * S::kHalves) softmax_role<kE4m3, kParts, Out>(a, sh, tmem, warp >> 2);
-    } else if (warp == 8) {
+    } else if (warp < S::kSoft) {
+        softmax_role<kE4m3, kParts, Out>(a, sh, tmem, warp >> 2);
+    } else if (warp == S::kSoft) {
         load_role<kE4m3, kParts>(a, &mq, &mk, &mv, sh, smem, x, hi, per_head, nt);
-    } else if (warp < 11) {
-        const int half = warp - 9;
-        if (half < S::kHalves) {
-            mma_role<kE4m3, kParts>(sh, smem, tmem, half, a.inject_wait);
-            // nothing may be under way in tensor memory when it is given back
-            __syncwarp();
-            if (elect_one()) mma_commit(smem_addr(&sh.drain[half]));
-            int32_t no = 0;
-            warp_wait(&sh.drain[half], 0, &no);
-        }
+    } else if (warp < S::kAux0) {
+        const int i = warp - S::kSoft - 1, half = i >> 1;
+        if (i & 1)
+            weight_role<kE4m3, kParts>(sh, smem, tmem, half);
+        else
+            score_role<kE4m3, kParts>(sh, smem, tmem, half, a.inject_wait);
+        // nothing may be under way in tensor memory when it is given back
+        __syncwarp();
+        if (elect_one()) mma_commit(smem_addr(&sh.drain[i]));
+        int32_t no = 0;
+        warp_wait(&sh.drain[i], 0, &no);
     } else {
         aux_role<kE4m3, kParts>(a, sh, smem);
     }
     tc_fence_before();
     __syncthreads();
-    if (sh.abort && warp == 8 && (threadIdx.x & 31) == 0) {
+    if (sh.abort && warp == S::kSoft && (threadIdx.x & 31) == 0) {
         // copies that were under way when a wait ran out write into this CTA's memory: give them
         // the time that any of them takes before the CTA ends
         const uint64_t t0 = now_ns();
         while (now_ns() - t0 < 10000000ull) {}
     }
     __syncthreads();
-    if (warp == 9) {
+    if (warp == S::kSoft + 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
