@@ -48,7 +48,7 @@ template <bool kE4m3, int kParts> struct Shape {
     static constexpr int kHalves = kParts == 1 ? 2 : 1;
     static constexpr int kStages = kE4m3 ? 3 : 4;
     static constexpr int kRaw = kE4m3 ? 3 : 0;
-    static constexpr int kAuxWarps = kE4m3 ? 5 : 1;
+    static constexpr int kAuxWarps = kE4m3 ? 5 : 3;
     static constexpr int kSoft = 4 * kHalves;                 // softmax warps
     static constexpr int kAux0 = kSoft + 1 + 2 * kHalves;     // first of the others
     static constexpr int kThreads = (kAux0 + kAuxWarps) * 32;
@@ -138,6 +138,24 @@ __device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
+}
+
+// kN words to memory, 32 bytes a store where the address is a multiple of 32 (else 16)
+template <int kN>
+__device__ __forceinline__ void store_words(void* dst, const uint32_t* w, bool wide) {
+#pragma unroll
+    for (int i = 0; i < kN; i += 8) {
+        uint32_t* d = static_cast<uint32_t*>(dst) + i;
+        const uint32_t* x = w + i;
+        if (wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                         :: "l"(d), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]),
+                            "r"(x[5]), "r"(x[6]), "r"(x[7]) : "memory");
+        } else {
+            reinterpret_cast<uint4*>(d)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+            reinterpret_cast<uint4*>(d)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+        }
+    }
 }
 
 // the last token that row r of a tile may attend (-1: none)
@@ -583,43 +601,36 @@ __device__ void softmax_role(const AttendArgs& a, Shared& sh, uint32_t tmem, int
                 const int64_t at = (g.row0 + rr / G) * (static_cast<int64_t>(a.heads) * G) +
                                    g.head * G + rr % G;
                 float* part = a.work + g.part * part_floats(R);
+                const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+                // 32 columns at a time; a thread's 64 or 128 bytes of a row in whole sectors
 #pragma unroll 1
-                for (int q = 0; q < 8; ++q) {
-                    const int col = 16 * q;
-                    uint32_t o[16];
+                for (int q = 0; q < 4; ++q) {
+                    const int col = 32 * q;
+                    uint32_t o[32];
                     if (!empty) {
-                        tmem_ld16(at0 + S::kO + col, o);
+                        tmem_ld32(at0 + S::kO + col, o);
                         tmem_wait_ld();
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < 32; ++i) {
                         const float y = empty ? 0.0f : __uint_as_float(o[i]) * inv;
                         o[i] = __float_as_uint(y);
                     }
-                    if (bad) {
+                    if (__builtin_expect(bad, 0)) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
+                        for (int i = 0; i < 32; ++i)
                             if (sh.bad[seg % kRing][col + i] <= lim) o[i] = 0x7fc00000u;
                     }
                     if (live && g.whole && sizeof(Out) == 2) {
-                        uint4* dst = reinterpret_cast<uint4*>(
-                            static_cast<__nv_bfloat16*>(a.out) + at * D + col);
+                        uint32_t u[16];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint32_t* u = o + 8 * i;
-                            dst[i] = make_uint4(
-                                bf2(__uint_as_float(u[0]), __uint_as_float(u[1])),
-                                bf2(__uint_as_float(u[2]), __uint_as_float(u[3])),
-                                bf2(__uint_as_float(u[4]), __uint_as_float(u[5])),
-                                bf2(__uint_as_float(u[6]), __uint_as_float(u[7])));
-                        }
+                        for (int i = 0; i < 16; ++i)
+                            u[i] = bf2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+                        store_words<16>(static_cast<__nv_bfloat16*>(a.out) + at * D + col, u, wide);
                     } else if (live) {
-                        uint4* dst = reinterpret_cast<uint4*>(
-                            g.whole ? static_cast<float*>(a.out) + at * D + col
-                                    : part + static_cast<size_t>(r) * D + col);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        store_words<32>(g.whole ? static_cast<float*>(a.out) + at * D + col
+                                                : part + static_cast<size_t>(r) * D + col,
+                                        o, wide && g.whole);
                     }
                     __syncwarp();
                 }
@@ -667,40 +678,51 @@ __device__ void aux_role(const AttendArgs& a, Shared& sh, uint8_t* smem) {
                     const uint8_t* src = smem + S::kRawAt + raw * kRawB;
                     const uint8_t* sc = smem + S::kScaleAt + raw * kBlk;
                     uint8_t* dst = smem + S::kKV + st * kStageB;
-                    const bool fix = flags & kFix;
+                    // A thread takes 16 codes; 8 lanes a row. The pieces that 8 lanes read are one
+                    // row, and those they write (two each) meet no bank twice.
 #pragma unroll 2
-                    for (int i = tid; i < kBlk * 16; i += kT) {
-                        const int row = i >> 4, j = i & 15, tok = block * kBlk + row;
-                        const uint2 w = *reinterpret_cast<const uint2*>(src + row * D + j * 8);
+                    for (int i = tid; i < kBlk * 8; i += kT) {
+                        const int row = i >> 3, j = i & 7, tok = block * kBlk + row;
+                        const uint4 w4 = *reinterpret_cast<const uint4*>(src + row * D + j * 16);
+                        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
                         const int byte = sc[row];
                         // code * 2^(byte - 127): the bf16 patterns are 2^-120 too small; the
                         // factor 2^(byte - 7) takes two steps where it is above 2^127
                         uint32_t f = static_cast<uint32_t>(min(byte + 120, 254)) << 7;
                         if (byte == kNanRow) f = 0x7fc0u;
-                        bool zero = false;
-                        if (fix) {
-                            zero = !(sh.entry[slot].mask[row >> 5] >> (row & 31) & 1);
+                        f |= f << 16;
+                        uint32_t y[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t x = k & 1 ? prmt_i<0x3424>(w[k >> 1], 0)
+                                                     : prmt_i<0x1404>(w[k >> 1], 0);
+                            y[k] = mul_bf2((x & 0x80008000u) | ((x >> 4) & 0x07f007f0u), f);
+                        }
+                        if (__builtin_expect(byte > 134 && byte != kNanRow, 0)) {
+                            const uint32_t f2 = static_cast<uint32_t>(byte - 134 + 127) << 7;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) y[k] = mul_bf2(y[k], f2 | f2 << 16);
+                        }
+                        if (__builtin_expect(flags & kFix, 0)) {
+                            bool zero = !(sh.entry[slot].mask[row >> 5] >> (row & 31) & 1);
                             if (t == 1 && !zero && byte == kNanRow && tok > shared) {
-                                for (int k = 0; k < 8; ++k) mark(8 * j + k, tok);
+                                for (int k = 0; k < 16; ++k) mark(16 * j + k, tok);
                                 zero = true;
                             }
-                        }
-                        const uint32_t ff = f | f << 16;
-                        uint32_t y[4];
+                            if (zero) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t x = k & 1 ? prmt_i<0x3424>(k < 2 ? w.x : w.y, 0)
-                                                     : prmt_i<0x1404>(k < 2 ? w.x : w.y, 0);
-                            y[k] = mul_bf2((x & 0x80008000u) | ((x >> 4) & 0x07f007f0u), ff);
+                                for (int k = 0; k < 8; ++k) y[k] = 0;
+                            }
                         }
-                        if (byte > 134 && byte != kNanRow) {
-                            const uint32_t f2 = static_cast<uint32_t>(byte - 134 + 127) << 7;
-                            for (int k = 0; k < 4; ++k) y[k] = mul_bf2(y[k], f2 | f2 << 16);
-                        }
-                        if (zero) y[0] = y[1] = y[2] = y[3] = 0;
-                        *reinterpret_cast<uint4*>(dst + (j >> 3) * kHalfB + row * 128 +
-                                                  (((j & 7) ^ (row & 7)) << 4)) =
-                            make_uint4(y[0], y[1], y[2], y[3]);
+                        // pieces 2 j and 2 j + 1 of the row; the lanes of the second 64 columns
+                        // write them in the other order
+                        uint8_t* to = dst + (j >> 2) * kHalfB + row * 128;
+                        const int c0 = (((2 * j) & 7) ^ (row & 7)) << 4;
+                        const bool odd = j & 4;
+                        const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]);
+                        const uint4 hi = make_uint4(y[4], y[5], y[6], y[7]);
+                        *reinterpret_cast<uint4*>(to + (odd ? c0 ^ 16 : c0)) = odd ? hi : lo;
+                        *reinterpret_cast<uint4*>(to + (odd ? c0 : c0 ^ 16)) = odd ? lo : hi;
                     }
                     fence_async_smem();
                     __syncwarp();
