@@ -34,7 +34,15 @@ __device__ __forceinline__ uint4 pack8(const float v[8]) {
 // warps of a CTA, so the 128-byte pieces of a head's rows meet in L2.
 constexpr int kWriteWarps = 8;
 
-// 8 elements of a row, as they are in memory
+// four values to e4m3, nearest even, saturating
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | hi << 16;
+}
+
+// 8 elements of a row, as they are in memory. top(): the fp32 bits of the largest magnitude in
+// the 16 lanes of a row (a NaN's are above infinity's); codes(e): the codes of x / 2^e.
 template <typename In> struct Raw8;
 template <> struct Raw8<float> {
     float4 a, b;
@@ -44,14 +52,23 @@ template <> struct Raw8<float> {
         b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
     }
     __device__ __forceinline__ void clear() { a = b = make_float4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float v[8]) const {
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    }
     __device__ __forceinline__ uint4 bf16() const {
-        float v[8];
-        get(v);
-        return pack8(v);
+        return make_uint4(bf16_pair(a.x, a.y), bf16_pair(a.z, a.w), bf16_pair(b.x, b.y),
+                          bf16_pair(b.z, b.w));
+    }
+    __device__ __forceinline__ uint32_t top() const {
+        const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        uint32_t t = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t = max(t, __float_as_uint(v[k]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
+        return t;
+    }
+    __device__ __forceinline__ uint2 codes(int e) const {
+        const float f = pow2f(-e);
+        return make_uint2(codes4(a.x * f, a.y * f, a.z * f, a.w * f),
+                          codes4(b.x * f, b.y * f, b.z * f, b.w * f));
     }
 };
 template <> struct Raw8<__nv_bfloat16> {
@@ -61,8 +78,28 @@ template <> struct Raw8<__nv_bfloat16> {
         a = __ldcs(reinterpret_cast<const uint4*>(p));
     }
     __device__ __forceinline__ void clear() { a = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float v[8]) const { unpack8(a, v); }
     __device__ __forceinline__ uint4 bf16() const { return a; }
+    __device__ __forceinline__ uint32_t top() const {   // two magnitudes a word
+        constexpr uint32_t m = 0x7fff7fffu;
+        uint32_t t = __vmaxu2(__vmaxu2(a.x & m, a.y & m), __vmaxu2(a.z & m, a.w & m));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, o));
+        return max(t & 0xffff0000u, t << 16);
+    }
+    __device__ __forceinline__ uint2 codes(int e) const {
+        // the product with a power of two is exact in bf16 (or far below the least code)
+        const uint32_t bits = static_cast<uint32_t>(127 - e) << 7, f = bits | bits << 16;
+        uint32_t y[4] = {a.x, a.y, a.z, a.w};
+        uint2 c;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y[k]) : "r"(y[k]), "r"(f));
+        auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+        auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
+        c.x = codes4(lo(y[0]), hi(y[0]), lo(y[1]), hi(y[1]));
+        c.y = codes4(lo(y[2]), hi(y[2]), lo(y[3]), hi(y[3]));
+        return c;
+    }
 };
 
 template <typename In, bool kE4m3>
@@ -106,43 +143,27 @@ paged_write_kernel(const PagePool pool, const Seqs c, int heads, const In* __res
     if (page < 0 || page >= pool.num_pages) return;
     const int slot = static_cast<int>(pos) & ((1 << pool.shift) - 1);
 
+    constexpr int kEl = kE4m3 ? 1 : 2;
+    uint8_t* const kp = pool.k + page * pool.page_bytes + l8 * kEl;
+    uint8_t* const vp = pool.v + page * pool.page_bytes + l8 * kEl;
     for (int r0 = 0; r0 < 2 * heads; r0 += 2 * kRows) {
         if (r0 > 0) load(r0);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             const int r = r0 + 2 * i + half;
             const bool live = r < 2 * heads, is_v = r >= heads;
-            const int64_t row = static_cast<int64_t>(is_v ? r - heads : r) << pool.shift | slot;
-            uint8_t* base = (is_v ? pool.v : pool.k) + page * pool.page_bytes;
+            const uint32_t row = static_cast<uint32_t>(is_v ? r - heads : r) << pool.shift | slot;
+            uint8_t* to = (is_v ? vp : kp) + static_cast<uint64_t>(row) * (D * kEl);
             if (!kE4m3) {
-                if (live) *reinterpret_cast<uint4*>(base + (row * D + l8) * 2) = x[i].bf16();
+                if (live) *reinterpret_cast<uint4*>(to) = x[i].bf16();
                 continue;
             }
-            float y[8];
-            x[i].get(y);
-            // largest magnitude by its bits: a NaN's are above infinity's
-            uint32_t top = 0;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(y[k]) & 0x7fffffffu);
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const uint32_t top = x[i].top();
             const bool finite = top < 0x7f800000u;
             const int byte = finite ? scale_byte(__uint_as_float(top)) : kNanRow;
-            const float inv = pow2f(finite ? 127 - byte : 0);
-            uint32_t code[2] = {0x7f7f7f7fu, 0x7f7f7f7fu};
-            if (finite) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float* z = y + 4 * k;
-                    code[k] = __nv_cvt_float2_to_fp8x2(make_float2(z[0] * inv, z[1] * inv),
-                                                       __NV_SATFINITE, __NV_E4M3);
-                    code[k] |= uint32_t(__nv_cvt_float2_to_fp8x2(
-                                   make_float2(z[2] * inv, z[3] * inv), __NV_SATFINITE,
-                                   __NV_E4M3)) << 16;
-                }
-            }
+            const uint2 code = finite ? x[i].codes(byte - 127) : make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
             if (live) {
-                *reinterpret_cast<uint2*>(base + row * D + l8) = make_uint2(code[0], code[1]);
+                *reinterpret_cast<uint2*>(to) = code;
                 if ((lane & 15) == 0)
                     (is_v ? pool.vs : pool.ks)[page * pool.scale_stride + row] =
                         static_cast<uint8_t>(byte);
@@ -313,39 +334,28 @@ plan_kernel(const Seqs c, int shift, const PlanShape p, const Plan plan) {
 }
 
 // ------------------------------------------------------------------------------------- join
-// The tile that the cut before CTA c = blockIdx.x + 1 goes through, if that cut is the tile's
-// first: its parts, from the CTA of its first block to the CTA of its last, are rescaled to the
-// common maximum and summed. A warp a row, 4 elements a lane; with many parts (few rows, a long
+// The tile that the cut before CTA blockIdx.x + 1 goes through, if that cut is the tile's first: its
+// parts are rescaled to the common maximum and summed. A warp a row, 4 elements a lane; with many parts (few rows, a long
 // token axis) the CTA's warps share a row's parts and add their sums up in order.
 constexpr int kJoinWarps = 4;
 constexpr int kJoinShared = 8;    // parts from which on the warps share a row
 
 template <typename Out>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-join_kernel(const AttendArgs a, int ctas) {
+join_kernel(const AttendArgs a) {
     __shared__ float s_sum[kJoinWarps][D + 2];
     pdl_wait();
     pdl_launch_dependents();
-    const int nt = *a.plan.ntiles;
-    const int64_t per_head = a.plan.tile[nt].pre, total = per_head * a.heads;
-    const int64_t n = cuts(total, ctas);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (static_cast<int64_t>(blockIdx.x) + 1 >= n) return;
-    const int64_t lo = cut(total, n, blockIdx.x + 1);
-    const int64_t h = lo / per_head;
-    const int at_tile = find_tile(a.plan.tile, nt, lo - h * per_head);
-    const Tile t = a.plan.tile[at_tile];
-    const int64_t start = h * per_head + t.pre;
-    const int64_t end = h * per_head + a.plan.tile[at_tile + 1].pre;
-    if (start == lo) return;
-    const int c0 = static_cast<int>(cut_of(total, n, start));
-    if (c0 != static_cast<int>(blockIdx.x)) return;
-    const int parts = static_cast<int>(cut_of(total, n, end - 1)) - c0 + 1;
+    const Cut t = a.cut[blockIdx.x + 1];
+    if (t.parts == 0) return;
+    const int parts = t.parts;
+    const int64_t h = t.head;
     const int R = a.shape.tile_rows, G = a.shape.group;
     const bool shared = parts >= kJoinShared;
     const size_t step = 2 * part_floats(R);
     // part i: slot 2 (c0 + i), the first one 2 c0 + 1
-    const float* base = a.work + 2 * static_cast<size_t>(c0) * part_floats(R);
+    const float* base = a.work + 2 * static_cast<size_t>(t.c0) * part_floats(R);
     auto part = [&](int i) { return base + i * step + (i == 0 ? part_floats(R) : 0); };
     const int i0 = shared ? warp : 0, istep = shared ? kJoinWarps : 1;
     const int r0 = shared ? blockIdx.y : blockIdx.y * kJoinWarps + warp;
@@ -405,7 +415,7 @@ cudaError_t launch_join(const AttendArgs& a, int ctas, bool f32_out, cudaStream_
     if (ctas < 2) return cudaSuccess;
     const dim3 grid(ctas - 1, min(16, a.shape.tile_rows));
     return launch_pdl(f32_out ? join_kernel<float> : join_kernel<__nv_bfloat16>, grid,
-                      dim3(kJoinWarps * 32), 0, st, a, ctas);
+                      dim3(kJoinWarps * 32), 0, st, a);
 }
 
 namespace {
@@ -636,13 +646,15 @@ pariskv_status pariskv_paged_attend(const pariskv_config* cfg, const pariskv_pag
     if (tiles > (1 << 28)) return fail(PARISKV_EINVAL, "too many query rows for one call");
     const size_t plan = round_up((tiles + 1) * sizeof(Tile), 256);
     const size_t parts = round_up(2 * ctas * part_floats(a.shape.tile_rows) * 4, 256);
+    const size_t cuts = round_up(ctas * sizeof(Cut), 256);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     void* ws = nullptr;
-    if ((s = take_workspace(&ws, parts + plan + 256, st)) != PARISKV_OK) return s;
+    if ((s = take_workspace(&ws, parts + cuts + plan + 256, st)) != PARISKV_OK) return s;
     uint8_t* w = static_cast<uint8_t*>(ws);
     a.work = reinterpret_cast<float*>(w);
-    a.plan.tile = reinterpret_cast<Tile*>(w + parts);
-    a.plan.ntiles = reinterpret_cast<int32_t*>(w + parts + plan);
+    a.cut = reinterpret_cast<Cut*>(w + parts);
+    a.plan.tile = reinterpret_cast<Tile*>(w + parts + cuts);
+    a.plan.ntiles = reinterpret_cast<int32_t*>(w + parts + cuts + plan);
     a.plan.max_tiles = static_cast<int32_t>(tiles);
     cudaError_t e = plan_first ? launch_plan(a, st) : cudaSuccess;
     if (e == cudaSuccess)

@@ -141,6 +141,13 @@ __host__ __device__ __forceinline__ size_t part_floats(int tile_rows) {
     return static_cast<size_t>(round_up(static_cast<int64_t>(tile_rows) * (D + 2), 4));
 }
 
+// What the join needs of the cut before CTA c, left by that CTA: the tile it goes through, if it is
+// that tile's first cut (parts > 0), and the CTAs whose parts make it up.
+struct Cut {
+    int32_t parts, c0;         // number of parts, and the CTA of the first
+    int32_t row0, first, nrow, head;
+};
+
 struct AttendArgs {
     PagePool pool;
     Seqs seqs;
@@ -153,8 +160,24 @@ struct AttendArgs {
     void* out;
     float* lse;             // or NULL
     float* work;            // parts
+    Cut* cut;               // [ctas]
     int32_t inject_wait;    // test hook: a wait of the chunk kernel runs out
 };
+
+// The record of CTA c, of the tile that its range begins in (block b0 of the tile's blocks [start,
+// end) on the whole axis).
+__device__ __forceinline__ Cut cut_record(const Tile& t, int64_t total, int64_t n, int64_t start,
+                                          int64_t end, int b0, int64_t head) {
+    Cut r;
+    r.c0 = static_cast<int32_t>(cut_of(total, n, start));
+    const bool mine = b0 > 0 && r.c0 == static_cast<int32_t>(blockIdx.x) - 1;
+    r.parts = mine ? static_cast<int32_t>(cut_of(total, n, end - 1)) - r.c0 + 1 : 0;
+    r.row0 = t.row0;
+    r.first = t.first;
+    r.nrow = t.nrow;
+    r.head = static_cast<int32_t>(head);
+    return r;
+}
 
 // paged.cu
 cudaError_t launch_plan(const AttendArgs& a, cudaStream_t st);

@@ -145,9 +145,9 @@ __device__ __forceinline__ int find_pre(const int64_t* pre, int n, int64_t x) {
 }
 
 // Where a CTA's range lies. Up to kInline sequences (a tile each, the host sees to that) are
-// planned here, by every CTA for itself; CTA 0 leaves the records that the join reads.
+// planned here, by every CTA for itself.
 struct Range {
-    int64_t x, hi, per_head;
+    int64_t x, hi, per_head, n;   // n: CTAs with work
     int32_t nt;
     bool inline_plan;
 };
@@ -195,27 +195,19 @@ __device__ __forceinline__ Range make_range(const AttendArgs& a, Control& c, boo
             if (w < warp) before += c.warp_sum[w];
             all += c.warp_sum[w];
         }
-        for (int i = 0; i < per && s0 + i < r.nt; ++i) {
-            c.pre[s0 + i] += before;
-            if (blockIdx.x == 0) a.plan.tile[s0 + i] = tile_record(a, s0 + i, c.pre[s0 + i]);
-        }
-        if (threadIdx.x == 0) {
-            c.pre[r.nt] = all;
-            if (blockIdx.x == 0) {
-                a.plan.tile[r.nt].pre = all;
-                *a.plan.ntiles = r.nt;
-            }
-        }
+        for (int i = 0; i < per && s0 + i < r.nt; ++i) c.pre[s0 + i] += before;
+        if (threadIdx.x == 0) c.pre[r.nt] = all;
         r.per_head = all;
         __syncthreads();
     } else {
         r.nt = *a.plan.ntiles;
         r.per_head = a.plan.tile[r.nt].pre;
     }
-    const int64_t total = r.per_head * a.heads, n = cuts(total, gridDim.x);
-    const bool work = blockIdx.x < n;
-    r.x = work ? cut(total, n, blockIdx.x) : 0;
-    r.hi = work ? cut(total, n, blockIdx.x + 1) : 0;
+    const int64_t total = r.per_head * a.heads;
+    r.n = cuts(total, gridDim.x);
+    const bool work = blockIdx.x < r.n;
+    r.x = work ? cut(total, r.n, blockIdx.x) : 0;
+    r.hi = work ? cut(total, r.n, blockIdx.x + 1) : 0;
     return r;
 }
 
@@ -237,12 +229,15 @@ __device__ void few_loads(const AttendArgs& a, const CUtensorMap* mk, const CUte
         tile = range.inline_plan ? find_pre(c.pre, range.nt, rest)
                                  : find_tile(a.plan.tile, range.nt, rest);
     }
+    if (x >= range.hi && lane == 0) a.cut[blockIdx.x].parts = 0;
     while (x < range.hi) {
         const Tile t = range.inline_plan ? tile_record(a, tile, c.pre[tile]) : a.plan.tile[tile];
         const int64_t nb = (range.inline_plan ? c.pre[tile + 1] : a.plan.tile[tile + 1].pre) - t.pre;
         const int64_t start = h * range.per_head + t.pre;
         const int b0 = static_cast<int>(x - start);
         const int b1 = static_cast<int>(min64(nb, range.hi - start));
+        if (seg == 0 && lane == 0)
+            a.cut[blockIdx.x] = cut_record(t, range.per_head * a.heads, range.n, start, start + nb, b0, h);
         const int32_t* table = a.seqs.table + static_cast<int64_t>(t.seq) * a.seqs.stride;
         // page ids come 32 at a time, a lane a run, one window ahead
         auto fetch = [&](int w) -> int {

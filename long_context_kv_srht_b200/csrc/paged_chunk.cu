@@ -15,7 +15,7 @@
 //  - O is rescaled only when a row's maximum has grown by more than 2^8 since the last time (P is
 //    then at most 2^8, which costs bf16 nothing), so tensor memory is not read back each block;
 //  - K, V and Q tiles come by TMA through a ring of 32 KB stages, one copy a page and 64 columns;
-//    with 8-bit pages they come as bytes, and five warps widen them into the ring, scale and all
+//    with 8-bit pages they come as bytes, and seven warps widen them into the ring, scale and all
 //    (a power of two: the bf16 values are exact);
 //  - blocks in which some token must not reach some row (the causal edge, the end of the cache,
 //    pages that are not there) are marked: their scores are masked, and their V rows are made
@@ -48,7 +48,7 @@ template <bool kE4m3, int kParts> struct Shape {
     static constexpr int kHalves = kParts == 1 ? 2 : 1;
     static constexpr int kStages = kE4m3 ? 3 : 4;
     static constexpr int kRaw = kE4m3 ? 3 : 0;
-    static constexpr int kAuxWarps = kE4m3 ? 5 : 3;
+    static constexpr int kAuxWarps = kE4m3 ? 7 : 3;
     static constexpr int kSoft = 4 * kHalves;                 // softmax warps
     static constexpr int kAux0 = kSoft + 1 + 2 * kHalves;     // first of the others
     static constexpr int kThreads = (kAux0 + kAuxWarps) * 32;
@@ -200,6 +200,10 @@ __device__ void load_role(const AttendArgs& a, const CUtensorMap* mq, const CUte
         g.whole = b0 == 0 && b1 == nb;
         g.part = 2 * static_cast<int>(blockIdx.x) + (b0 == 0);
         g.shared = row_limit(g, causal, G, 0);
+        if (seg == 0 && lane == 0) {
+            const int64_t total = per_head * a.heads;
+            a.cut[blockIdx.x] = cut_record(v, total, cuts(total, gridDim.x), start, after + h * per_head, b0, h);
+        }
         const int end = v.end;
         const int32_t* table = a.seqs.table + static_cast<int64_t>(v.seq) * a.seqs.stride;
 
@@ -863,6 +867,7 @@ attend_chunk_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap mq,
 
     if (!work) {
         // nothing to do but to give the tensor memory back
+        if (threadIdx.x == 0) a.cut[blockIdx.x].parts = 0;
     } else if (warp < S::kSoft) {
         softmax_role<kE4m3, kParts, Out>(a, sh, tmem, warp >> 2);
     } else if (warp == S::kSoft) {

@@ -608,6 +608,14 @@ class Chunk:
         self.ref = ctypes.byref(self.raw)
 
 
+def _current_stream(stream) -> int:
+    """_stream, without building a stream object for the usual case."""
+    import torch
+    if stream is None and torch.cuda.is_initialized():
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _stream(stream)
+
+
 def _paged_args(where: str, cfg: Config, pages: Pages, chunk: Chunk) -> None:
     if pages.num_kv_heads != cfg.num_kv_heads or chunk.batch != cfg.batch:
         _refuse(where, f"cfg is for {cfg.batch} sequences and {cfg.num_kv_heads} KV heads, the "
@@ -616,11 +624,13 @@ def _paged_args(where: str, cfg: Config, pages: Pages, chunk: Chunk) -> None:
 
 def _per_token(where: str, name: str, x, dtype, rows: int, heads: int) -> int:
     """Token stride of a per-token tensor [rows, heads, 128]."""
-    if x.dtype != dtype or x.dim() != 3 or x.shape != (rows, heads, 128) or (
-            rows and x.stride()[1:] != (128, 1) and heads > 1) or (rows and x.stride(2) != 1):
-        _refuse(where, f"{name} must be {dtype} [{rows}, {heads}, 128] with contiguous tokens, "
-                f"not {x.dtype} {tuple(x.shape)} with strides {x.stride()}")
-    return x.stride(0) if rows > 1 else heads * 128
+    if x.dtype is dtype and x.shape == (rows, heads, 128):
+        if x.is_contiguous():
+            return heads * 128
+        if x.stride(2) == 1 and (heads == 1 or x.stride(1) == 128):
+            return x.stride(0) if rows > 1 else heads * 128
+    _refuse(where, f"{name} must be {dtype} [{rows}, {heads}, 128] with contiguous tokens, "
+            f"not {x.dtype} {tuple(x.shape)} with strides {x.stride()}")
 
 
 def _cfg_dtype(cfg: Config):
@@ -637,7 +647,7 @@ def paged_write(cfg: Config, pages: Pages, chunk: Chunk, k_new, v_new, stream=No
     k_ld = _per_token(where, "k_new", k_new, dt, n, cfg.num_kv_heads)
     v_ld = _per_token(where, "v_new", v_new, dt, n, cfg.num_kv_heads)
     _check(lib.pariskv_paged_write(ctypes.byref(cfg), pages.ref, chunk.ref, k_new.data_ptr(),
-                                   v_new.data_ptr(), k_ld, v_ld, _stream(stream)), where)
+                                   v_new.data_ptr(), k_ld, v_ld, _current_stream(stream)), where)
 
 
 def paged_read(cfg: Config, pages: Pages, chunk: Chunk, first: int, n: int, K=None, V=None,
@@ -664,7 +674,7 @@ def paged_read(cfg: Config, pages: Pages, chunk: Chunk, first: int, n: int, K=No
     _check(lib.pariskv_paged_read(ctypes.byref(cfg), pages.ref, chunk.ref, int(first), int(n),
                                   K.data_ptr() if K is not None else None,
                                   V.data_ptr() if V is not None else None,
-                                  int(n) if ld is None else ld, _stream(stream)), where)
+                                  int(n) if ld is None else ld, _current_stream(stream)), where)
 
 
 def paged_attend(cfg: Config, pages: Pages, chunk: Chunk, q, scale: float, causal: bool = True,
@@ -692,7 +702,7 @@ def paged_attend(cfg: Config, pages: Pages, chunk: Chunk, q, scale: float, causa
                                     float(scale), int(bool(causal)), out.data_ptr(),
                                     BF16 if out.dtype == torch.bfloat16 else F32,
                                     lse.data_ptr() if lse is not None else None,
-                                    _stream(stream)), where)
+                                    _current_stream(stream)), where)
     return out, lse
 
 
