@@ -636,8 +636,8 @@ pariskv_status pariskv_paged_attend(const pariskv_config* cfg, const pariskv_pag
     const int64_t most = static_cast<int64_t>(chunk->max_q) * cfg->group;
     const bool few = most <= kFewRows;
     a.shape.tile_rows = few ? (most <= 8 ? 8 : kFewRows) : chunk_tile_rows(cfg->group, f32);
-    a.shape.block = few ? kFewBlock : kChunkBlock;
-    const int ctas = few ? few_ctas(sms, pages->format, a.shape.tile_rows) : sms;
+    a.shape.block = few ? few_block(pages->format == PARISKV_PAGES_E4M3) : kChunkBlock;
+    const int ctas = few ? few_ctas(sms) : sms;
     const bool plan_first = !few || !few_plans_inline(cfg->batch);
     a.inject_wait = !few && g_inject_wait.exchange(0);
     // tiles: every sequence may end in a part of one

@@ -184,8 +184,9 @@ cudaError_t launch_plan(const AttendArgs& a, cudaStream_t st);
 cudaError_t launch_join(const AttendArgs& a, int ctas, bool f32_out, cudaStream_t st);
 // paged_attend.cu: up to kFewRows rows a sequence (mma.sync, K/V streamed once), in tiles of 8 or
 // 16. It plans for itself where few_plans_inline says so (no launch_plan then).
-constexpr int kFewBlock = 64, kFewRows = 16;
-int few_ctas(int sms, int format, int tile_rows);
+constexpr int kFewRows = 16;
+constexpr int few_block(bool e4m3) { return e4m3 ? 128 : 64; }   // tokens of a block
+int few_ctas(int sms);
 bool few_plans_inline(int batch);
 cudaError_t launch_attend_few(const AttendArgs& a, int format, bool f32_out, int ctas,
                               cudaStream_t st);

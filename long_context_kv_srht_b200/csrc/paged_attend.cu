@@ -7,10 +7,12 @@
 // copies under way, and to spend few instructions a token:
 //  - all rows of a tile (up to 8 or 16: tokens x heads of the KV head's group) share one pass
 //    over K and V;
-//  - the (head, sequence) streams of a batch form one axis of 64-token blocks that is cut into
-//    equal ranges, two or three CTAs an SM, so ragged lengths leave no SM idle (see Plan);
+//  - the (head, sequence) streams of a batch form one axis of 64- or 128-token blocks that is cut into
+//    equal ranges, two CTAs an SM, so ragged lengths leave no SM idle (see Plan). A block has 128
+//    tokens in 8 bits: what a block costs besides its bytes (the loading warp's walk, the waits)
+//    bounded 64-token blocks there;
 //  - one warp walks the range and brings the pages by TMA into rings of K and of V tiles, across
-//    the ends of sequences; four warps take 16 tokens of a block each, held together by mbarriers
+//    the ends of sequences; four warps take 16 of every 64 tokens each, held together by mbarriers
 //    only (no barrier of the CTA in the loop);
 //  - both products run on mma.sync (m16n8k16, bf16, fp32 accumulators): S^T = K Q^T and O^T +=
 //    V^T P^T, so a lane's softmax state and its accumulators belong to the same two rows of each
@@ -34,18 +36,19 @@ namespace pkv {
 
 namespace {
 
-constexpr int kFW = 4;                        // warps, 16 tokens of a block each
-static_assert(kFewBlock == 16 * kFW, "a warp takes 16 tokens of a block");
+constexpr int kFW = 4;                        // warps, 16 of every 64 tokens each
 constexpr int kInline = 256;                  // sequences that every CTA plans for itself
 constexpr int kSegs = 8;                      // segment records between the loads and the others
 constexpr float kGrow = 8.0f;                 // growth of a maximum (base 2) that rescales O
 
 template <bool kE4m3> struct FewShape {
     static constexpr int kRowB = kE4m3 ? D : 2 * D;          // bytes of a row
-    static constexpr int kTile = kFewBlock * kRowB;          // a K or V tile: 16 or 8 KB
-    static constexpr int kNK = 3, kNV = kE4m3 ? 3 : 2;
-    static constexpr int kScales = (kNK + kNV) * kTile;      // 64 scale bytes a tile (8-bit)
-    static constexpr int kScratch = kScales + (kE4m3 ? (kNK + kNV) * kFewBlock : 0);
+    static constexpr int kBlk = few_block(kE4m3);            // tokens of a block
+    static constexpr int kSub = kBlk / (16 * kFW);           // a warp takes 16 tokens of each 64
+    static constexpr int kTile = kBlk * kRowB;               // a K or V tile: 16 KB
+    static constexpr int kNK = 3, kNV = 2;
+    static constexpr int kScales = (kNK + kNV) * kTile;      // its scale bytes (8-bit)
+    static constexpr int kScratch = kScales + (kE4m3 ? (kNK + kNV) * kBlk : 0);
     static constexpr int kPart = D + 4;                      // a row's partial in the scratch
     static constexpr int kSmem = kScratch + kFW * 8 * kPart * 4 + 1024;   // + alignment
 };
@@ -217,7 +220,9 @@ __device__ void few_loads(const AttendArgs& a, const CUtensorMap* mk, const CUte
                           Control& c, uint8_t* smem, const Range& range) {
     using S = FewShape<kE4m3>;
     const int lane = threadIdx.x & 31, shift = a.pool.shift;
-    const int rs = min(shift, 6), run = 1 << rs, ns = 6 - rs, nrun = 1 << ns;
+    constexpr int kBlk = S::kBlk, kLog = kBlk == 128 ? 7 : 6;
+    static_assert(kBlk == 1 << kLog, "64 or 128 tokens");
+    const int rs = min(shift, kLog), run = 1 << rs, ns = kLog - rs, nrun = 1 << ns;
     const int per_win = 32 >> ns;
     volatile int32_t* ab = &c.abort;
     int64_t x = range.x, h = 0;
@@ -241,7 +246,7 @@ __device__ void few_loads(const AttendArgs& a, const CUtensorMap* mk, const CUte
         const int32_t* table = a.seqs.table + static_cast<int64_t>(t.seq) * a.seqs.stride;
         // page ids come 32 at a time, a lane a run, one window ahead
         auto fetch = [&](int w) -> int {
-            const int tok = w * kFewBlock + lane * run;
+            const int tok = w * kBlk + lane * run;
             return w + (lane >> ns) < b1 && tok < t.end ? table[tok >> shift] : -1;
         };
         int win = b0, id = fetch(b0), id_next = fetch(b0 + per_win);
@@ -273,7 +278,7 @@ __device__ void few_loads(const AttendArgs& a, const CUtensorMap* mk, const CUte
             if (b >= 0) b = live(b + 1);
             const int ks = n % S::kNK, vs = n % S::kNV;
             const bool mine = lane < nrun && (cur_valid >> lane & 1);
-            const int tok = cur * kFewBlock + lane * run;
+            const int tok = cur * kBlk + lane * run;
             const int row = (static_cast<int>(h) << shift) + (tok & ((1 << shift) - 1));
             if (!warp_wait(&c.k_empty[ks], ((n / S::kNK) & 1) ^ 1, ab)) return;
             const uint32_t bytes = __popc(cur_valid) * run * (kE4m3 ? D + 1 : 2 * D);
@@ -295,8 +300,8 @@ __device__ void few_loads(const AttendArgs& a, const CUtensorMap* mk, const CUte
                 m.block = cur;
                 m.flags = (first ? kFirst : 0) | (b < 0 ? kLast : 0);
                 m.runs = 0;
-                for (int i = 0; i < kFW; ++i)
-                    if ((cur_valid >> (16 * i >> rs) & 1) && cur * kFewBlock + 16 * i < t.end)
+                for (int i = 0; i < kBlk / 16; ++i)
+                    if ((cur_valid >> (16 * i >> rs) & 1) && cur * kBlk + 16 * i < t.end)
                         m.runs |= 1u << i;
                 c.meta[ks] = m;
                 mbar_arrive_expect_tx(smem_addr(&c.k_full[ks]), bytes);
@@ -307,7 +312,7 @@ __device__ void few_loads(const AttendArgs& a, const CUtensorMap* mk, const CUte
                 const CUtensorMap* m = of ? mv : mk;
                 tma_load3(smem_addr(dst), m, 0, row, cur_page, smem_addr(bar));
                 if (kE4m3)
-                    bulk_g2s(smem_addr(smem + S::kScales + slot * kFewBlock + lane * run),
+                    bulk_g2s(smem_addr(smem + S::kScales + slot * kBlk + lane * run),
                              (of ? a.pool.vs : a.pool.ks) + cur_page * a.pool.scale_stride + row,
                              run, smem_addr(bar));
                 else
@@ -345,7 +350,7 @@ __device__ void few_loads(const AttendArgs& a, const CUtensorMap* mk, const CUte
 template <bool kE4m3, int NT, int kParts, typename Out>
 __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
     using S = FewShape<kE4m3>;
-    constexpr int R = 8 * NT, kPart = S::kPart;
+    constexpr int R = 8 * NT, kPart = S::kPart, kSub = S::kSub;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3, mi = lane >> 3, j8 = lane & 7;
     // the token of a lane's first row of S (the second is 8 on), and the 16-byte piece of a V row
@@ -438,21 +443,33 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                     o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.0f;
             }
         }
-        const bool live = m.runs >> warp & 1;
-        const int tok = m.block * kFewBlock + 16 * warp + pg;    // this lane's: tok, tok + 8
+        // the warp's 16 tokens of each 64: rows 64 u + 16 warp ... of the tiles
+        bool live[kSub];
+        int tok[kSub];                                   // this lane's: tok, tok + 8
+        bool any = false;
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+            live[u] = m.runs >> (kFW * u + warp) & 1;
+            any = any || live[u];
+            tok[u] = m.block * S::kBlk + 64 * u + 16 * warp + pg;
+        }
 
         // S^T: 16 tokens x R rows
-        float sc[NT][4];
-        float ka = 1.0f, kb = 1.0f;
-        if (live) {
+        float sc[kSub][NT][4];
+        float ka[kSub], kb[kSub];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.0f;
+        for (int u = 0; u < kSub; ++u) {
+            ka[u] = kb[u] = 1.0f;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) sc[u][j][0] = sc[u][j][1] = sc[u][j][2] = sc[u][j][3] = 0.0f;
+            if (!live[u]) continue;
+            const int r0 = 64 * u + 16 * warp;
             const uint8_t* kt = smem + ks * S::kTile;
             if (kE4m3) {
-                const uint8_t* sp = smem + S::kScales + ks * kFewBlock + 16 * warp + pg;
-                ka = scale_value(sp[0]);
-                kb = scale_value(sp[8]);
-                const uint32_t base = smem_addr(kt + (16 * warp + pg) * 128);
+                const uint8_t* sp = smem + S::kScales + ks * S::kBlk + r0 + pg;
+                ka[u] = scale_value(sp[0]);
+                kb[u] = scale_value(sp[8]);
+                const uint32_t base = smem_addr(kt + (r0 + pg) * 128);
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                     const uint32_t at = base + (((4 * hh + t) ^ pg) << 4);
@@ -465,11 +482,11 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                                                widen_hi(wu[i])};
 #pragma unroll
                         for (int j = 0; j < NT; ++j)
-                            mma16<kE4m3>(sc[j], f, qb[j][4 * hh + i][0], qb[j][4 * hh + i][1]);
+                            mma16<kE4m3>(sc[u][j], f, qb[j][4 * hh + i][0], qb[j][4 * hh + i][1]);
                     }
                 }
             } else {
-                const int row = 16 * warp + j8 + 8 * (mi & 1), kc = mi >> 1;
+                const int row = r0 + j8 + 8 * (mi & 1), kc = mi >> 1;
                 const uint32_t base = smem_addr(kt + row * 128);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -477,7 +494,8 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                     const int ch = 2 * i + kc;
                     ldsm_x4(base + (ch >> 3) * (S::kTile / 2) + (((ch & 7) ^ (row & 7)) << 4), f);
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) mma16<kE4m3>(sc[j], f, qb[j][i][0], qb[j][i][1]);
+                    for (int j = 0; j < NT; ++j)
+                        mma16<kE4m3>(sc[u][j], f, qb[j][i][0], qb[j][i][1]);
                 }
             }
         }
@@ -485,22 +503,26 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
         if (lane == 0) arrive(&c.k_empty[ks]);
 
         // softmax: weights with the maxima as they are, unless a score is far above
-        uint32_t pb[NT][kParts][2];
-        float w[NT][4];
-        // brings maxima up to date with the values v where one is far above; factors for the old
-        auto raise = [&](float (&top)[NT][2], const float (&v)[NT][4], float (&co)[NT][2]) -> bool {
+        float w[kSub][NT][4];
+        // brings maxima up to date with the scores where one is far above; factors for the old
+        auto raise = [&](float (&top)[NT][2], float (&co)[NT][2]) -> bool {
             bool grown = false;
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+            for (int u = 0; u < kSub; ++u)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    grown = grown || fmaxf(v[j][e], v[j][2 + e]) > top[j][e] + kGrow;
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        grown = grown || fmaxf(sc[u][j][e], sc[u][j][2 + e]) > top[j][e] + kGrow;
             if (!__any_sync(0xffffffffu, grown)) return false;
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float bm = fmaxf(v[j][e], v[j][2 + e]);
+                    float bm = -INFINITY;
+#pragma unroll
+                    for (int u = 0; u < kSub; ++u)
+                        bm = fmaxf(bm, fmaxf(sc[u][j][e], sc[u][j][2 + e]));
 #pragma unroll
                     for (int k = 4; k < 32; k <<= 1)
                         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, k));
@@ -525,24 +547,32 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float ms = top[j][e] == -INFINITY ? 0.0f : top[j][e];
-                    w[j][e] = exp2f(sc[j][e] - ms);
-                    w[j][2 + e] = exp2f(sc[j][2 + e] - ms);
+#pragma unroll
+                    for (int u = 0; u < kSub; ++u) {
+                        w[u][j][e] = exp2f(sc[u][j][e] - ms);
+                        w[u][j][2 + e] = exp2f(sc[u][j][2 + e] - ms);
+                    }
                 }
         };
-        if (live) {
-            const float fa = qs * ka, fb = qs * kb;
+        if (any) {
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float d0 = pow2f(down[j][e] / 2), d1 = pow2f(down[j][e] - down[j][e] / 2);
-                    const float s0 = kE4m3 ? sc[j][e] * d0 * d1 : sc[j][e];
-                    const float s1 = kE4m3 ? sc[j][2 + e] * d0 * d1 : sc[j][2 + e];
-                    sc[j][e] = tok <= lim[j][e] ? s0 * fa : -INFINITY;
-                    sc[j][2 + e] = tok + 8 <= lim[j][e] ? s1 * fb : -INFINITY;
+                    // (the power that undoes Q's may be out of range: two steps)
+                    const float d0 = kE4m3 ? pow2f(down[j][e] / 2) : 1.0f;
+                    const float d1 = kE4m3 ? pow2f(down[j][e] - down[j][e] / 2) : 1.0f;
+#pragma unroll
+                    for (int u = 0; u < kSub; ++u) {
+                        const float s0 = kE4m3 ? sc[u][j][e] * d0 * d1 : sc[u][j][e];
+                        const float s1 = kE4m3 ? sc[u][j][2 + e] * d0 * d1 : sc[u][j][2 + e];
+                        sc[u][j][e] = live[u] && tok[u] <= lim[j][e] ? s0 * (qs * ka[u]) : -INFINITY;
+                        sc[u][j][2 + e] =
+                            live[u] && tok[u] + 8 <= lim[j][e] ? s1 * (qs * kb[u]) : -INFINITY;
+                    }
                 }
             float co[NT][2];
-            if (raise(mx, sc, co)) {
+            if (raise(mx, co)) {
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
                     den[j][0] *= co[j][0];
@@ -552,33 +582,32 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
             }
             weigh(mx);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                den[j][0] += w[j][0] + w[j][2];
-                den[j][1] += w[j][1] + w[j][3];
-            }
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    den[j][0] += w[u][j][0] + w[u][j][2];
+                    den[j][1] += w[u][j][1] + w[u][j][3];
+                }
         }
         if (!warp_wait(&c.v_full[vs], (n / S::kNV) & 1, ab)) return;
-        if (live) {
+        if (any) {
             uint8_t* vt = smem + (S::kNK + vs) * S::kTile;
-            const int t0 = m.block * kFewBlock + 16 * warp;
-            int ea = 0, eb = 0;    // exponents of the V rows' scales
-            if (kE4m3) {
-                const uint8_t* sp = smem + S::kScales + (S::kNK + vs) * kFewBlock + 16 * warp + pg;
-                ea = sp[0] - 127;
-                eb = sp[8] - 127;
-            }
+            const uint8_t* vsc = smem + S::kScales + (S::kNK + vs) * S::kBlk;   // (8-bit)
             // What no row or not every row may see must not reach them: 0 * NaN is NaN. So rows
             // behind the end of the sequence are cleared, and what is not finite in the rows of
             // the chunk itself (8-bit: a NaN row) is taken out and put back at the end into the
             // rows that see it.
-            if (t0 + 15 > shared && (sg.end - 1 > shared || t0 + 15 >= sg.end)) {
+            const int last = m.block * S::kBlk + S::kBlk - 1;
+            const bool repair = last > shared && (sg.end - 1 > shared || last >= sg.end);
+            if (repair) {
                 int32_t* bad_at = c.bad[seg & 1];
                 constexpr int kPieces = S::kRowB / 16;
 #pragma unroll 1
-                for (int i = lane; i < 16 * kPieces; i += 32) {
-                    const int r16 = i / kPieces, ch = i % kPieces, row = 16 * warp + r16;
-                    const int tk = t0 + r16;
-                    if (tk <= shared) continue;
+                for (int i = lane; i < kSub * 16 * kPieces; i += 32) {
+                    const int r = i / kPieces, ch = i % kPieces;
+                    const int row = 64 * (r >> 4) + 16 * warp + (r & 15);
+                    const int tk = m.block * S::kBlk + row;
+                    if (tk <= shared || !(m.runs >> (row >> 4) & 1)) continue;
                     uint4* e = reinterpret_cast<uint4*>(vt + (ch >> 3) * (S::kTile / 2) + row * 128 +
                                                         (((ch & 7) ^ (row & 7)) << 4));
                     if (tk >= sg.end) {
@@ -586,103 +615,117 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                         continue;
                     }
                     if (kE4m3) {
-                        if (smem[S::kScales + (S::kNK + vs) * kFewBlock + row] != kNanRow) continue;
+                        if (vsc[row] != kNanRow) continue;
                         for (int k = 0; k < 16; ++k) atomicMin(&bad_at[16 * ch + k], tk);
                         *e = make_uint4(0, 0, 0, 0);
                         continue;
                     }
                     const uint4 y = *e;
-                    uint32_t u[4] = {y.x, y.y, y.z, y.w};
+                    uint32_t x[4] = {y.x, y.y, y.z, y.w};
                     bool odd = false;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        if ((u[k] & 0x7f80u) == 0x7f80u) {
+                        if ((x[k] & 0x7f80u) == 0x7f80u) {
                             atomicMin(&bad_at[8 * ch + 2 * k], tk);
-                            u[k] &= 0xffff0000u;
+                            x[k] &= 0xffff0000u;
                             odd = true;
                         }
-                        if ((u[k] & 0x7f800000u) == 0x7f800000u) {
+                        if ((x[k] & 0x7f800000u) == 0x7f800000u) {
                             atomicMin(&bad_at[8 * ch + 2 * k + 1], tk);
-                            u[k] &= 0xffffu;
+                            x[k] &= 0xffffu;
                             odd = true;
                         }
                     }
-                    if (odd) *e = make_uint4(u[0], u[1], u[2], u[3]);
-                }
-                if (kE4m3) {   // (a cleared NaN row weighs nothing)
-                    if (tok > shared && ea == kNanRow - 127) ea = -INT32_MAX / 2;
-                    if (tok + 8 > shared && eb == kNanRow - 127) eb = -INT32_MAX / 2;
+                    if (odd) *e = make_uint4(x[0], x[1], x[2], x[3]);
                 }
                 fence_async_smem();
                 __syncwarp();
             }
             if (kE4m3) {
                 // the weights of O: with V's scales in the exponent, relative to maxima of their own
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) {
+                    const int r0 = 64 * u + 16 * warp + pg;
+                    float ea = static_cast<float>(vsc[r0] - 127);
+                    float eb = static_cast<float>(vsc[r0 + 8] - 127);
+                    if (repair) {   // (a cleared NaN row weighs nothing)
+                        if (tok[u] > shared && vsc[r0] == kNanRow) ea = -INFINITY;
+                        if (tok[u] + 8 > shared && vsc[r0 + 8] == kNanRow) eb = -INFINITY;
+                    }
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            sc[u][j][e] += ea;
+                            sc[u][j][2 + e] += eb;
+                        }
+                }
                 float co[NT][2];
+                if (raise(mw, co)) rescale(co);
+                weigh(mw);
+            }
+#pragma unroll
+            for (int u = 0; u < kSub; ++u) {
+                if (!live[u]) continue;
+                const int r0 = 64 * u + 16 * warp;
+                // the weights as B fragments (k = tokens, n = rows), in parts
+                uint32_t pb[NT][kParts][2];
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        sc[j][e] += static_cast<float>(ea);
-                        sc[j][2 + e] += static_cast<float>(eb);
+                    for (int k = 0; k < kParts; ++k) {
+                        float(&x)[4] = w[u][j];
+                        const uint32_t h01 = kE4m3 ? h2(x[0], x[1]) : bf2(x[0], x[1]);
+                        const uint32_t h23 = kE4m3 ? h2(x[2], x[3]) : bf2(x[2], x[3]);
+                        pb[j][k][0] = movm_t(h01);
+                        pb[j][k][1] = movm_t(h23);
+                        const float2 f01 = kE4m3 ? h2_f(h01) : bf2_f(h01);
+                        const float2 f23 = kE4m3 ? h2_f(h23) : bf2_f(h23);
+                        x[0] -= f01.x; x[1] -= f01.y; x[2] -= f23.x; x[3] -= f23.y;
                     }
-                if (raise(mw, sc, co)) rescale(co);
-                weigh(mw);
-            }
-            // as B fragments (k = tokens, n = rows), in parts
+                // O^T += V^T P^T. MMA i covers elements 16 i + g and 16 i + g + 8 of a row (bf16),
+                // or 16 pg + 2 i and 16 pg + 2 i + 1 (8-bit)
+                if (kE4m3) {
+                    uint32_t wv[4][4];   // S rows 2t, 2t+1, 2t+8, 2t+9: tokens t, t+4, t+8, t+12
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int k = 0; k < kParts; ++k) {
-                    const uint32_t h01 = kE4m3 ? h2(w[j][0], w[j][1]) : bf2(w[j][0], w[j][1]);
-                    const uint32_t h23 = kE4m3 ? h2(w[j][2], w[j][3]) : bf2(w[j][2], w[j][3]);
-                    pb[j][k][0] = movm_t(h01);
-                    pb[j][k][1] = movm_t(h23);
-                    const float2 f01 = kE4m3 ? h2_f(h01) : bf2_f(h01);
-                    const float2 f23 = kE4m3 ? h2_f(h23) : bf2_f(h23);
-                    w[j][0] -= f01.x; w[j][1] -= f01.y; w[j][2] -= f23.x; w[j][3] -= f23.y;
-                }
-            // O^T += V^T P^T. MMA i covers elements 16 i + g and 16 i + g + 8 of a row (bf16),
-            // or 16 pg + 2 i and 16 pg + 2 i + 1 (8-bit)
-            if (kE4m3) {
-                uint32_t wv[4][4];   // S rows 2t, 2t+1, 2t+8, 2t+9 are tokens t, t+4, t+8, t+12
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int row = 16 * warp + t + 4 * k;
-                    const uint4 q4 = lds128(smem_addr(vt + row * 128) + ((pg ^ (row & 7)) << 4));
-                    wv[k][0] = q4.x; wv[k][1] = q4.y; wv[k][2] = q4.z; wv[k][3] = q4.w;
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int u = i >> 1;
-                    // two elements of two neighbouring tokens: a pair a register
-                    uint32_t f[4];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t y = i & 1 ? prmt_i<0x7362>(wv[2 * k][u], wv[2 * k + 1][u])
-                                                 : prmt_i<0x5140>(wv[2 * k][u], wv[2 * k + 1][u]);
-                        f[2 * k] = widen_lo(y);
-                        f[2 * k + 1] = widen_hi(y);
+                    for (int k = 0; k < 4; ++k) {
+                        const int row = r0 + t + 4 * k;
+                        const uint4 q4 =
+                            lds128(smem_addr(vt + row * 128) + ((pg ^ (row & 7)) << 4));
+                        wv[k][0] = q4.x; wv[k][1] = q4.y; wv[k][2] = q4.z; wv[k][3] = q4.w;
                     }
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
+                    for (int i = 0; i < 8; ++i) {
+                        // two elements of two neighbouring tokens: a pair a register
+                        uint32_t f[4];
 #pragma unroll
-                        for (int k = 0; k < kParts; ++k)
-                            mma16<kE4m3>(o[j][i], f, pb[j][k][0], pb[j][k][1]);
-                }
-            } else {
-                const int row = 16 * warp + j8 + 8 * (mi >> 1), vc = mi & 1;
-                const uint32_t base = smem_addr(vt + row * 128);
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t a0 = wv[2 * k][i >> 1], a1 = wv[2 * k + 1][i >> 1];
+                            const uint32_t y = i & 1 ? prmt_i<0x7362>(a0, a1) : prmt_i<0x5140>(a0, a1);
+                            f[2 * k] = widen_lo(y);
+                            f[2 * k + 1] = widen_hi(y);
+                        }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    uint32_t f[4];
-                    const int ch = 2 * i + vc;
-                    ldsm_x4_t(base + (ch >> 3) * (S::kTile / 2) + (((ch & 7) ^ (row & 7)) << 4), f);
+                        for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
+                            for (int k = 0; k < kParts; ++k)
+                                mma16<kE4m3>(o[j][i], f, pb[j][k][0], pb[j][k][1]);
+                    }
+                } else {
+                    const int row = r0 + j8 + 8 * (mi >> 1), vc = mi & 1;
+                    const uint32_t base = smem_addr(vt + row * 128);
 #pragma unroll
-                        for (int k = 0; k < kParts; ++k)
-                            mma16<kE4m3>(o[j][i], f, pb[j][k][0], pb[j][k][1]);
+                    for (int i = 0; i < 8; ++i) {
+                        uint32_t f[4];
+                        const int ch = 2 * i + vc;
+                        ldsm_x4_t(base + (ch >> 3) * (S::kTile / 2) + (((ch & 7) ^ (row & 7)) << 4),
+                                  f);
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int k = 0; k < kParts; ++k)
+                                mma16<kE4m3>(o[j][i], f, pb[j][k][0], pb[j][k][1]);
+                    }
                 }
             }
         }
@@ -762,10 +805,8 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
     }
 }
 
-constexpr int few_per_sm(bool e4m3, int nt) { return e4m3 && nt == 1 ? 3 : 2; }
-
 template <bool kE4m3, int NT, int kParts, typename Out>
-__global__ void __launch_bounds__((kFW + 1) * 32, few_per_sm(kE4m3, NT))
+__global__ void __launch_bounds__((kFW + 1) * 32, 2)
 attend_few_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap mv, int inline_plan) {
     using S = FewShape<kE4m3>;
@@ -825,9 +866,7 @@ cudaError_t launch_few_out(const AttendArgs& a, const CUtensorMap maps[2], bool 
 
 }  // namespace
 
-int few_ctas(int sms, int format, int tile_rows) {
-    return sms * few_per_sm(format == PARISKV_PAGES_E4M3, tile_rows / 8);
-}
+int few_ctas(int sms) { return 2 * sms; }
 
 bool few_plans_inline(int batch) { return batch <= kInline; }
 
@@ -839,7 +878,7 @@ cudaError_t launch_attend_few(const AttendArgs& a, int format, bool f32_out, int
     for (int t = 0; t < 2; ++t)
         if (!encode_rows(&maps[t], t ? a.pool.v : a.pool.k, e4, true,
                          static_cast<uint64_t>(a.heads) << a.pool.shift, a.pool.num_pages, el * D,
-                         a.pool.page_bytes, e4 ? D : 64, min(1 << a.pool.shift, kFewBlock), 1))
+                         a.pool.page_bytes, e4 ? D : 64, min(1 << a.pool.shift, few_block(e4)), 1))
             return cudaErrorInvalidValue;
     const bool one = a.shape.tile_rows == 8;
     if (e4)
