@@ -10,6 +10,7 @@ namespace pkv {
 namespace {
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint32_t kNapNs = 20000;
 
 __device__ int g_wait_status;   // ST_TIMEOUT after a wait ran out (one word a source file)
 
@@ -40,6 +41,28 @@ __device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, volatile i
     }
     return true;
 }
+// The same for a warp that is ahead of the others: asleep for up to kNapNs at a time.
+__device__ __noinline__ bool nap_more(uint32_t bar, uint32_t parity, volatile int32_t* abort) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok) : "r"(bar), "r"(parity), "r"(kNapNs) : "memory");
+        if (ok) return true;
+        if (*abort) return false;
+        const uint64_t t = now_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > kWaitLimitNs) {
+            *abort = 1;
+            atomicExch(&g_wait_status, ST_TIMEOUT);
+            return false;
+        }
+    }
+}
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int32_t* abort,
                                          uint64_t limit = kWaitLimitNs) {
     const uint32_t b = smem_addr(bar);
@@ -49,6 +72,10 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatil
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
                                           volatile int32_t* abort) {
     return __all_sync(0xffffffffu, wait_for(bar, parity, abort));
+}
+__device__ __forceinline__ bool warp_nap(uint64_t* bar, uint32_t parity, volatile int32_t* abort) {
+    const uint32_t b = smem_addr(bar);
+    return __all_sync(0xffffffffu, mbar_try_wait(b, parity) || nap_more(b, parity, abort));
 }
 __device__ __forceinline__ void arrive(uint64_t* bar) { mbar_arrive(smem_addr(bar)); }
 

@@ -37,7 +37,6 @@ namespace {
 
 constexpr int kBlk = 128;                      // tokens of a block
 constexpr int kTurn = 64;                      // tokens whose scores are worked on at a time
-constexpr int kPoly = 0;                       // of 16 exponentials, those on the FMA units
 constexpr int kHalfB = kBlk * 128;             // 64 columns x 128 rows of bf16: one swizzled tile
 constexpr int kStageB = 2 * kHalfB;            // a K, V or Q tile: 32 KB
 constexpr int kRawB = kBlk * D;                // a tile of codes: 16 KB
@@ -104,28 +103,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     float y;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-    return y;
-}
-// 2^x of a pair on the FMA units (the exponential units are the softmax's bottleneck), for x
-// that is not masked: x = n + f, |f| <= 1/2, by adding and taking away 1.5 * 2^23 + 127, 2^f by a
-// polynomial of degree 4 (fitted for the least relative error over the range: 2.6e-6, far below
-// the half step of a bf16 weight), and 2^n from the sum's low bits, which are n + 127. Below
-// 2^-126 it stays there; NaN stays NaN.
-__device__ __forceinline__ float2 ex2_fma(float2 x) {
-    const uint64_t z = pack2(max_nan(x.x, -126.0f), max_nan(x.y, -126.0f));
-    const uint64_t t = add2(z, pack2(12583039.0f, 12583039.0f));
-    const uint64_t f = fma2(add2(t, pack2(-12583039.0f, -12583039.0f)), pack2(-1.0f, -1.0f), z);
-    uint64_t p = pack2(0.00957010128f, 0.00957010128f);
-    p = fma2(p, f, pack2(0.0559178591f, 0.0559178591f));
-    p = fma2(p, f, pack2(0.240247443f, 0.240247443f));
-    p = fma2(p, f, pack2(0.693121791f, 0.693121791f));
-    p = fma2(p, f, pack2(0.999999285f, 0.999999285f));
-    const uint64_t n = pack2u(static_cast<uint32_t>(t) << 23, static_cast<uint32_t>(t >> 32) << 23);
-    return unpack2(fma2(p, n, 0));
 }
 __device__ __forceinline__ uint32_t bf2(float lo, float hi) {
     uint32_t r;
@@ -243,7 +220,7 @@ __device__ void load_role(const AttendArgs& a, const CUtensorMap* mq, const CUte
             if (b >= 0) b = live(b + 1, &valid, &page);
             // the entry
             const int slot = n % kRing;
-            if (!warp_wait(&sh.info_empty[slot], ((n / kRing) & 1) ^ 1, ab)) return;
+            if (!warp_nap(&sh.info_empty[slot], ((n / kRing) & 1) ^ 1, ab)) return;
             Entry e;
             e.block = cur;
             e.flags = (first ? kFirst : 0) | (b < 0 ? kLast : 0) | (cur < 0 ? kEmpty : 0) |
@@ -276,7 +253,7 @@ __device__ void load_role(const AttendArgs& a, const CUtensorMap* mq, const CUte
             ++n;
             if (cur < 0) break;
             if (first) {
-                if (!warp_wait(&sh.q_empty, (nq & 1) ^ 1, ab)) return;
+                if (!warp_nap(&sh.q_empty, (nq & 1) ^ 1, ab)) return;
                 if (lane == 0) {
                     const int halves = e.flags & kTwo ? 2 : 1;
                     mbar_arrive_expect_tx(smem_addr(&sh.q_full), halves * 2 * rt * 128);
@@ -296,7 +273,7 @@ __device__ void load_role(const AttendArgs& a, const CUtensorMap* mq, const CUte
                 constexpr int kSlots = kE4m3 ? S::kRaw : S::kStages;
                 const int st = ld % kSlots;
                 uint64_t* full_bar = kE4m3 ? &sh.raw_full[st] : &sh.kv_full[st];
-                if (!warp_wait(kE4m3 ? &sh.raw_empty[st] : &sh.kv_empty[st],
+                if (!warp_nap(kE4m3 ? &sh.raw_empty[st] : &sh.kv_empty[st],
                               ((ld / kSlots) & 1) ^ 1, ab))
                     return;
                 if (lane == 0)
@@ -328,7 +305,7 @@ __device__ void load_role(const AttendArgs& a, const CUtensorMap* mq, const CUte
     }
     // the end: an entry without a segment
     const int slot = n % kRing;
-    if (!warp_wait(&sh.info_empty[slot], ((n / kRing) & 1) ^ 1, ab)) return;
+    if (!warp_nap(&sh.info_empty[slot], ((n / kRing) & 1) ^ 1, ab)) return;
     if (lane == 0) {
         sh.entry[slot].flags = kEnd;
         sh.entry[slot].block = -1;
@@ -351,8 +328,8 @@ __device__ __forceinline__ int next_block(Shared& sh, uint32_t& n, bool leader) 
     while (true) {
         const int slot = n % kRing;
         if (!warp_wait(&sh.info_full[slot], (n / kRing) & 1, &sh.abort)) return -1;
-        const int f = sh.entry[slot].flags, b = sh.entry[slot].block;
-        __syncwarp();
+        const int f = uniform(static_cast<uint32_t>(sh.entry[slot].flags));
+        const int b = uniform(static_cast<uint32_t>(sh.entry[slot].block));
         if (leader) arrive(&sh.info_empty[slot]);
         ++n;
         if (b >= 0) return f | kSome;
@@ -382,28 +359,24 @@ __device__ void score_role(Shared& sh, uint8_t* smem, uint32_t tmem, int half, b
         if ((flags & kFirst) && !warp_wait(&sh.q_full, nq++ & 1, ab)) return;
         if (!warp_wait(&sh.kv_full[st], (used / S::kStages) & 1, ab)) return;
         const bool mine = half == 0 || (flags & kTwo);
-        const uint64_t k0 = uniform(k_desc + st * (kStageB >> 4));
+        const uint64_t k0 = k_desc + st * (kStageB >> 4);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
             if (mine) {
                 // they go where the weights of the same turn of the last block were read
                 if (nb > 0 && !warp_wait(&sh.pv_done[half][w], (nb - 1) & 1, ab)) return;
                 tc_fence_after();
-                if (leader) {
 #pragma unroll
-                    for (int j = 0; j < D / 16; ++j) {
-                        const uint32_t at = ((j >> 2) * kHalfB + (j & 3) * 32) >> 4;
-                        mma_ss(s_at + kTurn * w, q_desc + at, k0 + (w * kTurn * 128 >> 4) + at, kQK,
-                               j > 0);
-                    }
-                    mma_commit(smem_addr(&sh.s_full[half][w]));
+                for (int j = 0; j < D / 16; ++j) {
+                    const uint32_t at = ((j >> 2) * kHalfB + (j & 3) * 32) >> 4;
+                    mma_ss(leader, s_at + kTurn * w, q_desc + at, k0 + (w * kTurn * 128 >> 4) + at, kQK,
+                           j > 0);
                 }
+                mma_commit(leader, smem_addr(&sh.s_full[half][w]));
             }
         }
-        if (leader) {
-            mma_commit(smem_addr(&sh.kv_empty[st]));
-            if (flags & kLast) mma_commit(smem_addr(&sh.q_empty));
-        }
+        mma_commit(leader, smem_addr(&sh.kv_empty[st]));
+        if (flags & kLast) mma_commit(leader, smem_addr(&sh.q_empty));
         __syncwarp();
         nb += mine ? 1 : 0;
         used += 2;
@@ -430,26 +403,24 @@ __device__ void weight_role(Shared& sh, uint8_t* smem, uint32_t tmem, int half) 
             fix ^= 1u << st;
         }
         const bool mine = half == 0 || (flags & kTwo);
-        const uint64_t v0 = uniform(v_desc + st * (kStageB >> 4));
+        const uint64_t v0 = v_desc + st * (kStageB >> 4);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
             if (mine) {
                 if (!warp_wait(&sh.p_full[half][w], nb & 1, ab)) return;
                 tc_fence_after();
-                if (leader) {
 #pragma unroll
-                    for (int p = 0; p < kParts; ++p)
+                for (int p = 0; p < kParts; ++p)
 #pragma unroll
-                        for (int j = 0; j < kTurn / 16; ++j)
-                            mma_ts(o_at, p_at + S::kPTurn * w + 32 * p + 8 * j,
-                                   v0 + ((w * kTurn * 128 + j * 16 * 128) >> 4), kPV,
-                                   !(flags & kFirst) || w > 0 || p > 0 || j > 0);
-                    mma_commit(smem_addr(&sh.pv_done[half][w]));
-                    if ((flags & kLast) && w == 1) mma_commit(smem_addr(&sh.o_full[half]));
-                }
+                    for (int j = 0; j < kTurn / 16; ++j)
+                        mma_ts(leader, o_at, p_at + S::kPTurn * w + 32 * p + 8 * j,
+                               v0 + ((w * kTurn * 128 + j * 16 * 128) >> 4), kPV,
+                               !(flags & kFirst) || w > 0 || p > 0 || j > 0);
+                mma_commit(leader, smem_addr(&sh.pv_done[half][w]));
+                if ((flags & kLast) && w == 1) mma_commit(leader, smem_addr(&sh.o_full[half]));
             }
         }
-        if (leader) mma_commit(smem_addr(&sh.kv_empty[st]));
+        mma_commit(leader, smem_addr(&sh.kv_empty[st]));
         __syncwarp();
         nb += mine ? 1 : 0;
         used += 2;
@@ -554,18 +525,8 @@ __device__ void softmax_role(const AttendArgs& a, Shared& sh, uint32_t tmem, int
                     for (int i = 0; i < 32; i += 2) {
                         const float2 y = unpack2(
                             fma2(pack2u(s[32 * q + i], s[32 * q + i + 1]), c2, m2));
-                        if (kParts == 1 && i % 16 < kPoly) {
-                            const float2 z = ex2_fma(y);
-                            p[i] = z.x;
-                            p[i + 1] = z.y;
-                            if (flags & kFix) {   // what is masked must be 0
-                                if (y.x == -INFINITY) p[i] = 0.0f;
-                                if (y.y == -INFINITY) p[i + 1] = 0.0f;
-                            }
-                        } else {
-                            p[i] = ex2(y.x);
-                            p[i + 1] = ex2(y.y);
-                        }
+                        p[i] = ex2(y.x);
+                        p[i + 1] = ex2(y.y);
                         sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(p[i], p[i + 1]));
                     }
 #pragma unroll
@@ -664,7 +625,7 @@ __device__ void aux_role(const AttendArgs& a, Shared& sh, uint8_t* smem) {
     uint32_t n = 0, seg = 0, use = 0;   // use: tiles of the ring seen
     while (true) {
         const int slot = n % kRing;
-        if (!warp_wait(&sh.info_full[slot], (n / kRing) & 1, ab)) return;
+        if (!warp_nap(&sh.info_full[slot], (n / kRing) & 1, ab)) return;
         const int flags = sh.entry[slot].flags, block = sh.entry[slot].block;
         if (flags & kEnd) return;
         const int sg = seg % kRing;
@@ -677,8 +638,8 @@ __device__ void aux_role(const AttendArgs& a, Shared& sh, uint8_t* smem) {
             if constexpr (kE4m3) {
                 for (int t = 0; t < 2; ++t) {
                     const int raw = use % S::kRaw, st = use % S::kStages;
-                    if (!warp_wait(&sh.raw_full[raw], (use / S::kRaw) & 1, ab)) return;
-                    if (!warp_wait(&sh.kv_empty[st], ((use / S::kStages) & 1) ^ 1, ab)) return;
+                    if (!warp_nap(&sh.raw_full[raw], (use / S::kRaw) & 1, ab)) return;
+                    if (!warp_nap(&sh.kv_empty[st], ((use / S::kStages) & 1) ^ 1, ab)) return;
                     const uint8_t* src = smem + S::kRawAt + raw * kRawB;
                     const uint8_t* sc = smem + S::kScaleAt + raw * kBlk;
                     uint8_t* dst = smem + S::kKV + st * kStageB;
@@ -739,7 +700,7 @@ __device__ void aux_role(const AttendArgs& a, Shared& sh, uint8_t* smem) {
             } else {
                 const int st = (use + 1) % S::kStages;
                 if (flags & kFix) {
-                    if (!warp_wait(&sh.kv_full[st], ((use + 1) / S::kStages) & 1, ab)) return;
+                    if (!warp_nap(&sh.kv_full[st], ((use + 1) / S::kStages) & 1, ab)) return;
                     // rows from the first one that needs a look: all past `shared`, and all of a
                     // block that is not whole; a warp takes 4 rows of 64 columns at a time, 4
                     // such pieces in flight
@@ -814,7 +775,7 @@ attend_chunk_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap mq,
     extern __shared__ uint8_t raw_smem[];
     __shared__ __align__(16) Shared sh;
     uint8_t* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
-    const int warp = threadIdx.x >> 5;
+    const int warp = uniform(threadIdx.x >> 5);   // (known to be the same in a warp)
     if (threadIdx.x == 0) {
         sh.abort = 0;
         auto init = [&](uint64_t* b, uint32_t count) { mbar_init(smem_addr(b), count); };
@@ -880,7 +841,7 @@ attend_chunk_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap mq,
             score_role<kE4m3, kParts>(sh, smem, tmem, half, a.inject_wait);
         // nothing may be under way in tensor memory when it is given back
         __syncwarp();
-        if (elect_one()) mma_commit(smem_addr(&sh.drain[i]));
+        mma_commit(elect_one(), smem_addr(&sh.drain[i]));
         int32_t no = 0;
         warp_wait(&sh.drain[i], 0, &no);
     } else {

@@ -92,23 +92,30 @@ def attend(cache: Cache, q, group, scale, causal):
         toks = np.array(toks, dtype=np.int64)
         pi = np.array([p for p, _ in slots], dtype=np.int64)
         ri = np.array([r for _, r in slots], dtype=np.int64)
+        rows = cache.rows(s)
+        if not rows:
+            continue
+        row = np.array([r for r, _ in rows])
+        pos = np.array([p for _, p in rows])
+        see = toks[None, :] <= pos[:, None] if causal else np.ones((len(rows), len(toks)), bool)
+        some = see.any(1)
         for h in range(cache.k.shape[1]):
             K, V = cache.k[pi, h, ri], cache.v[pi, h, ri]
-            for row, pos in cache.rows(s):
-                see = toks <= pos if causal else np.ones(len(toks), bool)
-                for g in range(group):
-                    i = (row, h * group + g)
-                    if not see.any():
-                        out[i], lse[i] = 0.0, -np.inf
-                        continue
-                    x = K[see] @ q[i] * scale
-                    m = x.max()
-                    p = np.exp(x - m)
-                    z = p.sum()
-                    out[i] = (p / z) @ V[see]
-                    lse[i] = m + np.log(z)
-                    weight[i] = (p / z) @ np.abs(V[see])
-                    reach[i] = (np.abs(K[see]) @ np.abs(q[i]) * abs(scale)).max()
+            for g in range(group):
+                i = h * group + g
+                out[row[~some], i], lse[row[~some], i] = 0.0, -np.inf
+                if not some.any():
+                    continue
+                r, m = row[some], see[some]
+                x = np.where(m, q[r, i] @ K.T * scale, -np.inf)
+                top = x.max(1, keepdims=True)
+                p = np.exp(x - top)
+                z = p.sum(1, keepdims=True)
+                p /= z
+                out[r, i] = p @ V
+                lse[r, i] = (top + np.log(z))[:, 0]
+                weight[r, i] = p @ np.abs(V)
+                reach[r, i] = np.where(m, np.abs(q[r, i]) @ np.abs(K).T * abs(scale), 0).max(1)
     return out, lse, weight, reach
 
 

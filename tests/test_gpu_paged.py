@@ -432,3 +432,85 @@ def test_a_wait_that_runs_out_reaches_the_caller(fmt):
     out, lse = _attend(c)                  # reported once; the next call is whole again
     pk.paged_sync()
     c.check(out, lse, True)
+
+
+# ------------------------------------------------------------------------------- together
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_prompt_in_chunks_to_the_retrieval_index_and_decode(fmt):
+    """As a serving program uses them: two prompts come in by chunks (write, attend), the pages are
+    read back into slabs, the index is built from those, and decode steps write, attend over all
+    pages, and search and attend sparsely over the slabs."""
+    rng = np.random.default_rng(8)
+    heads, group, page, n = 2, 4, 16, [700, 333]
+    cap, steps = 720, 3
+    width = -(-cap // page)
+    x = rng.standard_normal((2, 2, heads, cap, D)).astype(np.float32)      # k, v by sequence
+    x[0, ..., 5] *= 6
+    x = ref.bf16_round(x)
+    q = ref.bf16_round(rng.standard_normal((2, cap, heads * group, D)).astype(np.float32))
+    dt = torch.bfloat16 if fmt == "bf16" else torch.float8_e4m3fn
+    pool = [torch.zeros((2 * width + 1, heads, page, D), device=DEV).to(dt) for _ in range(2)]
+    sc = [torch.zeros((2 * width + 1, heads, page), dtype=torch.uint8, device=DEV)
+          for _ in range(2)] if fmt == "e4m3" else [None, None]
+    pages = pk.Pages(pool[0], pool[1], sc[0], sc[1])
+    table = _dev(rng.permutation(2 * width + 1)[:2 * width].reshape(2, width).astype(np.int32))
+    cfg = pk.config(batch=2, num_kv_heads=heads, group=group, dtype="bf16", capacity=cap,
+                    cand_bp=2000)
+    if fmt == "bf16":
+        kept = np.float64(x)
+    else:
+        rows = [ref.quantise_row(r) for r in x.reshape(-1, D)]
+        kept = ref.dequantise(np.stack([c for c, _ in rows]),
+                              np.array([b for _, b in rows])).reshape(x.shape)
+
+    def step(done, take):
+        """Write and attend take[s] new tokens of each sequence after done[s]."""
+        starts = np.concatenate([[0], np.cumsum(take)]).astype(np.int32)
+        total = int(starts[-1])
+        kv = np.array([a + b for a, b in zip(done, take)], np.int32)
+        chunk = pk.Chunk(table, _dev(kv), _dev(starts), total, max(take))
+        k_new, v_new = (np.concatenate([x[i, s, :, done[s]:kv[s]].transpose(1, 0, 2)
+                                        for s in range(2)]) for i in range(2))
+        qs = np.concatenate([q[s, done[s]:kv[s]] for s in range(2)])
+        pk.paged_write(cfg, pages, chunk, _bf(k_new), _bf(v_new))
+        out, lse = pk.paged_attend(cfg, pages, chunk, _bf(qs), SCALE, want_lse=True)
+        cache = ref.Cache(kept[0], kept[1], np.arange(2, dtype=np.int32)[:, None], kv, starts)
+        cache.k, cache.v, cache.page = kept[0], kept[1], cap          # a sequence is a page here
+        o, l, w, reach = ref.attend(cache, np.float64(qs), group, SCALE, True)
+        tol, ltol = ref.tolerances(w, reach, o, int(kv.max()), 2.0 ** -8, 2.0 ** -8)
+        assert (np.abs(out.double().cpu().numpy() - o) <= tol).all()
+        assert (np.abs(lse.double().cpu().numpy() - l) <= ltol + 2.0 ** -24 * np.abs(l)).all()
+        return chunk, out
+
+    done = [0, 0]
+    for take in ([256, 200], [256, 133], [188, 0]):
+        chunk, _ = step(done, take)
+        done = [a + b for a, b in zip(done, take)]
+    assert done == n
+    K, V = (torch.zeros((2, heads, cap, D), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    pk.paged_read(cfg, pages, chunk, 0, cap, K, V)
+    for got, want in ((K, kept[0]), (V, kept[1])):
+        for s in range(2):
+            np.testing.assert_array_equal(got[s, :, :n[s]].double().cpu().numpy(), want[s, :, :n[s]])
+            assert (got[s, :, n[s]:] == 0).all()
+    # the index of the slabs is the index of the rows themselves
+    signs = np.where(rng.integers(0, 2, D) == 1, -1, 1).astype(np.int8)
+    m = min(n)
+    ix = pk.build_index(cfg, signs, K, n=m)
+    direct = pk.build_index(cfg, signs, _bf(kept[0][:, :, :m]))
+    for a, b in zip(ix.export_index(), direct.export_index()):
+        np.testing.assert_array_equal(a, b)
+    for _ in range(steps):
+        chunk, out = step(done, [1, 1])
+        done = [a + 1 for a in done]
+    # all rows retrieved, the sparse attention over the slabs is the paged one over those rows
+    top, _ = ix.search(_bf(q[:, n[0]][:, :]).contiguous(), m)
+    assert (torch.sort(top, 1).values == torch.arange(m, device=DEV)).all()
+    qd = _bf(q[:, n[0]]).contiguous()
+    sparse = pk.sparse_attend(cfg, qd, K, V, top, m, SCALE, n=m, out_dtype=torch.float32)
+    last = pk.Chunk(table, _dev(np.full(2, m, np.int32)), _dev(np.arange(3, dtype=np.int32)), 2, 1)
+    dense = pk.dense_attend(cfg, qd, K, V, SCALE, n=m, out_dtype=torch.float32)
+    paged, _ = pk.paged_attend(cfg, pages, last, qd, SCALE, out_dtype=torch.float32)
+    # dense and sparse carry the weights in 16 bits (half a step: 2^-17) and sum the same products
+    bound = 2.0 ** -15 * float(V[:, :, :m].abs().max())
+    assert (dense - paged).abs().max() <= bound and (sparse - paged).abs().max() <= bound
