@@ -275,14 +275,48 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* s_warp, int64_
     return x + before;
 }
 
+// Marks the blocks of a sequence (with new tokens) of which some page is there: a warp 32 blocks, a
+// lane a block. With few sequences several warps share one.
+__device__ __forceinline__ void mark_live(const Seqs& c, const PagePool& pool, const PlanShape& p,
+                                          const Plan& plan) {
+    constexpr int kWarps = kPlanT / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, shift = pool.shift;
+    const int per = c.batch < kWarps ? kWarps / c.batch : 1, step = kWarps / per;
+    for (int s = warp / per; s < c.batch && warp < per * step; s += step) {
+        const SeqView v = seq_view(c, shift, s);
+        if (v.rows == 0) continue;
+        const int32_t* table = c.table + static_cast<int64_t>(s) * c.stride;
+        const int n = static_cast<int>(ceil_div(v.kv, 32 * static_cast<int64_t>(p.block)));
+#pragma unroll 2
+        for (int w = warp % per; w < n; w += per) {
+            const int64_t tok = (static_cast<int64_t>(w) * 32 + lane) * p.block;
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < kChunkBlock / 16; ++i) {   // pages have 16 tokens at least
+                const int64_t t = tok + (static_cast<int64_t>(i) << shift);
+                if ((i << shift) < p.block && t < v.kv)
+                    any |= static_cast<uint32_t>(table[t >> shift]) <
+                           static_cast<uint32_t>(pool.num_pages);
+            }
+            const uint32_t word = __ballot_sync(0xffffffffu, any);
+            if (lane == 0) plan.live[static_cast<int64_t>(s) * plan.words + w] = word;
+        }
+    }
+}
+
 // One CTA: counts each sequence's tiles, writes the tiles in order, and sums their blocks.
 __global__ void __launch_bounds__(kPlanT)
-plan_kernel(const Seqs c, int shift, const PlanShape p, const Plan plan) {
+plan_kernel(const Seqs c, const PagePool pool, const PlanShape p, const Plan plan) {
+    const int shift = pool.shift;
     __shared__ int64_t s_warp[kPlanT / 32];
     __shared__ int32_t s_first[kPlanT], s_count[kPlanT];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     pdl_launch_dependents();
+    if (plan.live) {
+        mark_live(c, pool, p, plan);
+        __syncthreads();
+    }
     int64_t tiles = 0;
     for (int s0 = 0; s0 < c.batch; s0 += kPlanT) {
         const int s = s0 + threadIdx.x;
@@ -302,13 +336,21 @@ plan_kernel(const Seqs c, int shift, const PlanShape p, const Plan plan) {
             for (int t = lane; t < n; t += 32) {
                 Tile x;
                 x.first = t * p.tile_rows;
-                x.pre = tile_blocks(v, p, x.first);   // (its own, until they are summed)
+                x.end = tile_end(v, p, x.first);
+                int64_t blocks = ceil_div(x.end, p.block);
+                if (plan.live) {
+                    const uint32_t* live = plan.live + static_cast<int64_t>(s0 + i) * plan.words;
+                    const int n = static_cast<int>(blocks), left = n & 31;
+                    blocks = left ? __popc(live[n >> 5] & ((1u << left) - 1)) : 0;
+#pragma unroll 4
+                    for (int w = 0; w < n >> 5; ++w) blocks += __popc(live[w]);
+                }
+                x.pre = max64(1, blocks);   // (its own, until they are summed)
                 x.pos0 = v.pos0;
                 x.seq = s0 + i;
                 x.row0 = v.row0;
                 x.nrow = static_cast<int32_t>(
                     min64(p.tile_rows, static_cast<int64_t>(v.rows) * p.group - x.first));
-                x.end = tile_end(v, p, x.first);
                 x.kv = v.kv;
                 x.pad[0] = x.pad[1] = 0;
                 plan.tile[s_first[i] + t] = x;
@@ -407,8 +449,7 @@ join_kernel(const AttendArgs a) {
 }  // namespace
 
 cudaError_t launch_plan(const AttendArgs& a, cudaStream_t st) {
-    return launch_pdl(plan_kernel, dim3(1), dim3(kPlanT), 0, st, a.seqs, a.pool.shift, a.shape,
-                      a.plan);
+    return launch_pdl(plan_kernel, dim3(1), dim3(kPlanT), 0, st, a.seqs, a.pool, a.shape, a.plan);
 }
 
 cudaError_t launch_join(const AttendArgs& a, int ctas, bool f32_out, cudaStream_t st) {
@@ -647,15 +688,19 @@ pariskv_status pariskv_paged_attend(const pariskv_config* cfg, const pariskv_pag
     const size_t plan = round_up((tiles + 1) * sizeof(Tile), 256);
     const size_t parts = round_up(2 * ctas * part_floats(a.shape.tile_rows) * 4, 256);
     const size_t cuts = round_up(ctas * sizeof(Cut), 256);
+    const int64_t held = min64(INT32_MAX, static_cast<int64_t>(chunk->table_width) << a.pool.shift);
+    a.plan.words = few ? 0 : static_cast<int32_t>(ceil_div(held, 32 * kChunkBlock));
+    const size_t live = static_cast<size_t>(cfg->batch) * a.plan.words * sizeof(uint32_t);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     void* ws = nullptr;
-    if ((s = take_workspace(&ws, parts + cuts + plan + 256, st)) != PARISKV_OK) return s;
+    if ((s = take_workspace(&ws, parts + cuts + plan + 256 + live, st)) != PARISKV_OK) return s;
     uint8_t* w = static_cast<uint8_t*>(ws);
     a.work = reinterpret_cast<float*>(w);
     a.cut = reinterpret_cast<Cut*>(w + parts);
     a.plan.tile = reinterpret_cast<Tile*>(w + parts + cuts);
     a.plan.ntiles = reinterpret_cast<int32_t*>(w + parts + cuts + plan);
     a.plan.max_tiles = static_cast<int32_t>(tiles);
+    a.plan.live = few ? nullptr : reinterpret_cast<uint32_t*>(w + parts + cuts + plan + 256);
     cudaError_t e = plan_first ? launch_plan(a, st) : cudaSuccess;
     if (e == cudaSuccess)
         e = few ? launch_attend_few(a, pages->format, f32, ctas, st)

@@ -92,6 +92,10 @@ struct Plan {
     Tile* tile;        // [max_tiles + 1]
     int32_t* ntiles;   // [1]
     int32_t max_tiles;
+    // a bit a block and sequence, [batch][words]: some page of it is there. With it (not NULL) a
+    // tile's cost is the number of those blocks, and its range of blocks counts them alone.
+    uint32_t* live;
+    int32_t words;
 };
 struct PlanShape {
     int32_t group, tile_rows, block;   // block: tokens of a KV block

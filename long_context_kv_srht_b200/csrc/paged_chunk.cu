@@ -158,6 +158,8 @@ __device__ void load_role(const AttendArgs& a, const CUtensorMap* mq, const CUte
     int tile = find_tile(a.plan.tile, nt, x - h * per_head);
     Tile v = a.plan.tile[tile];
     uint32_t n = 0, seg = 0, ld = 0, nq = 0;   // entries, segments, tiles loaded, Q tiles loaded
+    int word_seq = -1, word0 = 0;              // the bits that are held: of which sequence, from where
+    uint32_t words = 0;
     volatile int32_t* ab = &sh.abort;
 
     while (x < hi) {
@@ -184,40 +186,89 @@ __device__ void load_role(const AttendArgs& a, const CUtensorMap* mq, const CUte
         const int end = v.end;
         const int32_t* table = a.seqs.table + static_cast<int64_t>(v.seq) * a.seqs.stride;
 
-        // page ids come 32 at a time, a lane a run, one window ahead
-        const int per_win = 32 >> ns;                   // blocks of a window
-        int win = b0, id = -1, id_next = -1;
-        auto fetch = [&](int w) -> int {
-            const int64_t tok = static_cast<int64_t>(w) * kBlk + lane * run;
-            return w + (lane >> ns) < b1 && tok < end ? table[tok >> shift] : -1;
+        // The tile's blocks [b0, b1), counting those with a page that is there. The sequence's bits
+        // are held 32 words at a time, a lane a word, and stay for its next tile.
+        const int blocks = static_cast<int>(ceil_div(end, kBlk)), nwords = (blocks + 31) >> 5;
+        const int kv_words = static_cast<int>(ceil_div(v.kv, 32 * kBlk));
+        const uint32_t* bits = a.plan.live + static_cast<int64_t>(v.seq) * a.plan.words;
+        auto hold = [&](int w) {
+            word0 = w;
+            word_seq = v.seq;
+            words = w + lane < kv_words ? bits[w + lane] : 0u;
         };
-        id = fetch(win);
-        id_next = fetch(win + per_win);
-        // the next block with a page that is there, from b on; *ids: this lane's page of it
-        auto live = [&](int b, uint32_t* valid, int* page) -> int {
-            for (; b < b1; ++b) {
-                if (b >= win + per_win) {
-                    win += per_win;
-                    id = id_next;
-                    id_next = fetch(win + per_win);
-                }
-                const uint32_t ok = __ballot_sync(
-                    0xffffffffu, static_cast<uint32_t>(id) < static_cast<uint32_t>(a.pool.num_pages));
-                const int at = (b - win) << ns;
-                *valid = (ok >> at) & (nrun == 32 ? ~0u : (1u << nrun) - 1);
-                *page = __shfl_sync(0xffffffffu, id, (at + lane) & 31);
-                if (*valid) return b;
+        if (word_seq != v.seq || word0 != 0) hold(0);
+        int at_word = -1, left = b1 - b0;
+        uint32_t rest = 0;                              // bits of that word not yet taken
+        auto take = [&]() -> int {
+            if (left-- <= 0) return -1;
+            while (rest == 0) {
+                if (++at_word >= nwords) return -1;
+                if (at_word >= word0 + 32) hold(at_word);
+                rest = __shfl_sync(0xffffffffu, words, at_word - word0);
+                if (at_word == nwords - 1 && (blocks & 31)) rest &= (1u << (blocks & 31)) - 1;
             }
-            return -1;
+            const int b = 32 * at_word + __ffs(rest) - 1;
+            rest &= rest - 1;
+            return b;
         };
-        uint32_t valid = 0;
-        int page = 0;
-        int b = live(b0, &valid, &page);
+        if (b0 > 0) {                                   // pass the first b0
+            int skip = b0, sum, total;
+            while (true) {
+                sum = __popc(words);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += y;
+                }
+                total = __shfl_sync(0xffffffffu, sum, 31);
+                if (skip < total || word0 + 32 >= kv_words) break;
+                skip -= total;
+                hold(word0 + 32);
+            }
+            const int k = __popc(__ballot_sync(0xffffffffu, sum <= skip)) & 31;
+            rest = __shfl_sync(0xffffffffu, words, k);
+            skip -= __shfl_sync(0xffffffffu, sum, k) - __popc(rest);
+            at_word = word0 + k;
+            const bool it = (rest >> lane & 1) && __popc(rest & ((1u << lane) - 1)) == skip;
+            const uint32_t from = __ballot_sync(0xffffffffu, it);   // one bit
+            rest &= ~(from - 1);
+            if (at_word == nwords - 1 && (blocks & 31)) rest &= (1u << (blocks & 31)) - 1;
+        }
+        // page ids come a window of blocks at a time, a lane a run, one window ahead
+        const int per_win = min(8, 32 >> ns);
+        auto fetch = [&](int* block) -> int {
+            *block = -1;
+            for (int i = 0; i < per_win; ++i) {
+                const int b = take();
+                if (lane >> ns == i) *block = b;
+            }
+            const int64_t tok = static_cast<int64_t>(*block) * kBlk + (lane & (nrun - 1)) * run;
+            return *block >= 0 && tok < v.kv ? table[tok >> shift] : -1;
+        };
+        int block = -1, block_next = -1, at = 0;
+        int id = fetch(&block), id_next = fetch(&block_next);
+        uint32_t valid = 0;                             // pages of the block that are there
+        int page = 0;                                   // this lane's
+        auto advance = [&]() -> int {
+            if (at == per_win) {
+                at = 0;
+                block = block_next;
+                id = id_next;
+                id_next = fetch(&block_next);
+            }
+            const uint32_t ok = __ballot_sync(
+                0xffffffffu, static_cast<uint32_t>(id) < static_cast<uint32_t>(a.pool.num_pages));
+            const int l0 = at++ << ns;
+            valid = (ok >> l0) & ((1u << nrun) - 1);
+            page = __shfl_sync(0xffffffffu, id, (l0 + lane) & 31);
+            return __shfl_sync(0xffffffffu, block, l0);
+        };
+        int b = advance();
         bool first = true;
         while (first || b >= 0) {
             const uint32_t cur_valid = valid;
             const int cur_page = page, cur = b;
-            if (b >= 0) b = live(b + 1, &valid, &page);
+            if (b >= 0) b = advance();
             // the entry
             const int slot = n % kRing;
             if (!warp_nap(&sh.info_empty[slot], ((n / kRing) & 1) ^ 1, ab)) return;
@@ -230,11 +281,11 @@ __device__ void load_role(const AttendArgs& a, const CUtensorMap* mq, const CUte
             for (int f = 0; f < 4; ++f) {
                 const uint32_t l = cur_valid >> (32 * f >> rs) & 1,
                                u = cur_valid >> ((32 * f + 16) >> rs) & 1;
-                const int left = end - (cur * kBlk + 32 * f);
-                e.mask[f] = cur < 0 || left <= 0
+                const int more = end - (cur * kBlk + 32 * f);
+                e.mask[f] = cur < 0 || more <= 0
                                 ? 0u
                                 : ((l ? 0xffffu : 0u) | (u ? 0xffff0000u : 0u)) &
-                                      (left >= 32 ? ~0u : (1u << left) - 1);
+                                      (more >= 32 ? ~0u : (1u << more) - 1);
                 full = full && e.mask[f] == ~0u;
             }
             const int last_tok = min(end, (cur + 1) * kBlk) - 1;
