@@ -512,14 +512,19 @@ static cudaError_t workspace_pool(cudaMemPool_t* out) {
         props.location.type = cudaMemLocationTypeDevice;
         props.location.id = dev;
         cudaMemPool_t p = nullptr;
-        e = cudaMemPoolCreate(&p, &props);
+        // creating a pool touches no stream, but a capture in the strict modes refuses it: the
+        // first call of a process may well be a captured one
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        e = cudaThreadExchangeStreamCaptureMode(&mode);
         if (e != cudaSuccess) return e;
+        e = cudaMemPoolCreate(&p, &props);
         uint64_t keep = ~uint64_t{0};
-        e = cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep);
-        if (e != cudaSuccess) {
-            cudaMemPoolDestroy(p);
-            return e;
+        if (e == cudaSuccess) {
+            e = cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep);
+            if (e != cudaSuccess) cudaMemPoolDestroy(p);
         }
+        cudaThreadExchangeStreamCaptureMode(&mode);
+        if (e != cudaSuccess) return e;
         pools[dev] = p;
     }
     *out = pools[dev];

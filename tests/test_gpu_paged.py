@@ -1,5 +1,9 @@
 """The paged K/V cache on the GPU (include/pariskv_paged.h) against 64-bit references: codes and
 scale bytes exactly, read-back exactly, attention within bounds counted from its roundings."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -88,7 +92,9 @@ class Case:
     def check(self, out, lse, causal, scale=SCALE):
         o, l, w, reach = self.reference(causal, scale)
         f32 = out.dtype == torch.float32
-        tol, ltol = ref.tolerances(w, reach, o, int(self.kv.max()), 2.0 ** (-24 if f32 else -8),
+        longest = max(len(ref.Cache(self.k, self.v, self.table, self.kv, self.q_start).tokens(s))
+                      for s in range(len(self.q_len)))
+        tol, ltol = ref.tolerances(w, reach, o, longest, 2.0 ** (-24 if f32 else -8),
                                    2.0 ** (-24 if f32 else -8))
         got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
         n = int(self.q_start[-1])
@@ -387,6 +393,93 @@ def test_many_tiles_a_cta(fmt, out_dtype, causal):
     out, lse = _attend(c, causal, out_dtype)
     pk.paged_sync()
     c.check(out, lse, causal)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("q,page", [([3, 2], 16), ([90, 33], 16), ([90, 33], 128)])
+def test_long_caches_of_which_little_is_left(fmt, out_dtype, q, page):
+    """Caches of some 300 000 tokens with a few pages here and there: first ones, whole stretches
+    without any, single pages inside a block of 128 tokens, the last ones."""
+    c = Case(13, fmt, q, [40 * page, 40 * page], heads=1, group=4, page=page)
+    rng = np.random.default_rng(4)
+    n = [300_000 // page, 270_000 // page]
+    table = np.full((2, n[0]), -1, np.int32)
+    for s in range(2):
+        tail = np.arange(n[s] - 9, n[s])
+        at = [0, 1, 5] if s == 0 else []
+        at = np.concatenate([at, np.sort(rng.choice(np.arange(n[s] // 2, n[s] - 40),
+                                                    31 - len(at), replace=False)), tail])
+        table[s, at.astype(int)] = c.table[s, :40]
+    c.table, c.kv = table, np.array([n[0] * page, n[1] * page], np.int32)
+    c.chunk = pk.Chunk(_dev(table), _dev(c.kv), _dev(c.q_start), c.total, max(q))
+    for causal in (True, False):
+        out, lse = _attend(c, causal, out_dtype)
+        c.check(out, lse, causal)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("q", [[2, 1], [140, 1]])
+def test_outputs_on_16_bytes_and_two_streams_at_once(fmt, q):
+    """Outputs that begin on 16 bytes but not on 32, and calls that overlap on two streams."""
+    c = Case(31, fmt, q, [2000, 500], heads=2, group=4, page=64)
+    qd, pages, n = _bf(c.q), c.pool(), c.total * 8 * D
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for out_dtype in (torch.bfloat16, torch.float32):
+        want, wl = _attend(c, True, out_dtype, q=qd)
+        pad = 16 // want.element_size()
+        outs = []
+        for i in range(8):
+            buf = torch.full((n + pad,), float("nan"), dtype=out_dtype, device=DEV)
+            lse = torch.full((c.total, 8), float("nan"), device=DEV)
+            outs.append((buf[pad:].view(c.total, 8, D), lse))
+            assert outs[-1][0].data_ptr() % 32 == 16
+        torch.cuda.synchronize()
+        for i, (out, lse) in enumerate(outs):
+            with torch.cuda.stream(streams[i % 2]):
+                pk.paged_attend(c.cfg, pages, c.chunk, qd, SCALE, out=out, lse=lse)
+        torch.cuda.synchronize()
+        rows = int(c.q_start[-1])
+        for out, lse in outs:
+            assert torch.equal(out[:rows], want[:rows]) and torch.equal(lse[:rows], wl[:rows])
+            assert torch.isnan(out[rows:].float()).all()
+
+
+_FIRST_IN_CAPTURE = """
+import torch
+from long_context_kv_srht_b200 import pariskv as pk
+dev = "cuda:0"
+torch.manual_seed(0)
+k, v = (torch.randn(9, 2, 64, 128, device=dev).bfloat16() for _ in range(2))
+ints = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)
+table, kv = ints([[3, 1, 4, 0, 5, 8, 2, 6]]), ints([500])
+cfg, pages = pk.config(batch=1, num_kv_heads=2, group=4, dtype="bf16"), pk.Pages(k, v)
+runs = []
+for n in (1, 100):
+    chunk = pk.Chunk(table, kv, ints([0, n]), n, n)
+    q = torch.randn(n, 8, 128, device=dev).bfloat16()
+    out = torch.zeros(n, 8, 128, device=dev).bfloat16()
+    runs.append((chunk, q, out))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    for chunk, q, out in runs:
+        pk.paged_attend(cfg, pages, chunk, q, 0.1, out=out)
+graph.replay()
+torch.cuda.synchronize()
+pk.paged_sync()
+for chunk, q, out in runs:
+    want, _ = pk.paged_attend(cfg, pages, chunk, q, 0.1)
+    assert torch.equal(out, want) and out.abs().max() > 0
+print("same")
+"""
+
+
+def test_first_call_of_a_process_inside_a_capture():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST_IN_CAPTURE], capture_output=True, text=True,
+                       timeout=300, cwd=root)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
 
 
 def test_refusals_with_device_buffers():
