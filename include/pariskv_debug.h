@@ -88,10 +88,9 @@ PARISKV_API pariskv_status pariskv_debug_inject_bad_candidate(pariskv_index* ind
  * the pages. Errors: EINVAL. */
 PARISKV_API pariskv_status pariskv_debug_inject_wait_timeout(pariskv_index* index);
 
-/* The next pariskv_paged_attend of many query rows a sequence (more than 16: the tensor-core
- * chunk kernel; calls with fewer rows pass it on) waits, in every CTA, for an arrival that never
- * comes: that wait runs out after a millisecond, the CTA's other waits end with it, and
- * pariskv_paged_sync then returns PARISKV_ETIMEOUT. No counterpart on the pages. */
+/* The next pariskv_paged_attend waits, in every CTA, for an arrival that never comes: that wait
+ * runs out after a millisecond, the CTA's other waits end with it, and pariskv_paged_sync then
+ * returns PARISKV_ETIMEOUT. No counterpart on the pages. */
 PARISKV_API pariskv_status pariskv_debug_inject_paged_timeout(void);
 
 /* Forces the launch shapes of later searches on this index, for tests that require the same

@@ -107,10 +107,12 @@ PARISKV_API pariskv_status pariskv_paged_read(const pariskv_config* cfg,
  *          PARISKV_BF16: the probabilities enter the second product with at least bf16's 8
  *          bits; PARISKV_F32: with 24 bits, so that the result is as exact as fp32 sums are.
  *   lse:   device pointer [total_q][num_kv_heads * group] fp32, or NULL.
- * Sums, maxima and accumulators are fp32. A K or V row with an infinity or a NaN in it makes the
+ * Sums, maxima and accumulators are fp32; the accumulators are relative to maxima that may lag by
+ * a factor of 2^8, so sums of V's magnitudes over the attended tokens past 2^119 can overflow to
+ * infinity. A K or V row with an infinity or a NaN in it makes the
  * rows that attend it infinite or NaN (V: in the elements concerned) and no others. The same
  * call on the same data gives the same bits. The workspace comes from the library's per-device
- * memory pool, stream-ordered on `stream`.
+ * memory pool, stream-ordered on `stream`. Two or three launches.
  * Errors: EINVAL, ENOMEM, ECUDA; ETIMEOUT from pariskv_paged_sync. */
 PARISKV_API pariskv_status pariskv_paged_attend(const pariskv_config* cfg,
                                                 const pariskv_pages* pages,

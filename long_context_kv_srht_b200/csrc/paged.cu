@@ -680,7 +680,7 @@ pariskv_status pariskv_paged_attend(const pariskv_config* cfg, const pariskv_pag
     a.shape.block = few ? few_block(pages->format == PARISKV_PAGES_E4M3) : kChunkBlock;
     const int ctas = few ? few_ctas(sms) : sms;
     const bool plan_first = !few || !few_plans_inline(cfg->batch);
-    a.inject_wait = !few && g_inject_wait.exchange(0);
+    a.inject_wait = g_inject_wait.exchange(0);
     // tiles: every sequence may end in a part of one
     const int64_t tiles = min64(cfg->batch * ceil_div(most, a.shape.tile_rows),
                                 chunk->total_q * cfg->group / a.shape.tile_rows + cfg->batch);

@@ -165,7 +165,7 @@ struct AttendArgs {
     float* lse;             // or NULL
     float* work;            // parts
     Cut* cut;               // [ctas]
-    int32_t inject_wait;    // test hook: a wait of the chunk kernel runs out
+    int32_t inject_wait;    // test hook: a wait runs out
 };
 
 // The record of CTA c, of the tile that its range begins in (block b0 of the tile's blocks [start,

@@ -53,6 +53,7 @@ template <bool kE4m3> struct FewShape {
     static constexpr int kSmem = kScratch + kFW * 8 * kPart * 4 + 1024;   // + alignment
 };
 static_assert(FewShape<true>::kNK < kSegs, "a record outlives the entries behind it");
+static_assert(FewShape<true>::kNK < 4, "one barrier is left that nothing arrives at");
 
 enum : int { kFirst = 1, kLast = 2, kEnd = 4 };
 struct Meta {
@@ -832,16 +833,18 @@ attend_few_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap mk,
     pdl_launch_dependents();
     const Range range = make_range(a, c, inline_plan != 0);
     __syncthreads();
-    if (warp == kFW) {
+    if (warp == kFW)
         few_loads<kE4m3>(a, &mk, &mv, c, smem, range);
-        if (*reinterpret_cast<volatile int32_t*>(&c.abort)) {
-            // copies that were under way when a wait ran out write into this CTA's memory: give
-            // them the time that any of them takes before the CTA ends
-            const uint64_t t0 = now_ns();
-            while (now_ns() - t0 < 10000000ull) {}
-        }
-    } else {
+    else if (a.inject_wait && warp == 0)   // test hook: a wait for an arrival that never comes
+        wait_for(&c.k_full[S::kNK], 0, &c.abort, 1000000ull);
+    else
         few_consume<kE4m3, NT, kParts, Out>(a, c, smem);
+    __syncthreads();
+    if (c.abort && warp == kFW) {
+        // copies that were under way when a wait ran out write into this CTA's memory: give them
+        // the time that any of them takes before the CTA ends
+        const uint64_t t0 = now_ns();
+        while (now_ns() - t0 < 10000000ull) {}
     }
 }
 

@@ -713,5 +713,5 @@ def paged_sync(stream=None) -> None:
 
 
 def inject_paged_timeout() -> None:
-    """pariskv_debug_inject_paged_timeout (test hook, consumed by the next chunk attention)."""
+    """pariskv_debug_inject_paged_timeout (test hook, consumed by the next paged attention)."""
     _check(lib.pariskv_debug_inject_paged_timeout(), "pariskv_debug_inject_paged_timeout")

@@ -514,8 +514,9 @@ def test_injected_failures_leave_outputs_alone(monkeypatch, kind, status):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
-def test_a_wait_that_runs_out_reaches_the_caller(fmt):
-    c = Case(8, fmt, [200], [300], heads=2, group=4, page=16)
+@pytest.mark.parametrize("n", [1, 200])
+def test_a_wait_that_runs_out_reaches_the_caller(fmt, n):
+    c = Case(8, fmt, [n], [300], heads=2, group=4, page=16)
     pk.paged_sync()
     pk.inject_paged_timeout()
     _attend(c)
