@@ -47,7 +47,7 @@ template <bool kE4m3, int kParts> struct Shape {
     static constexpr int kHalves = kParts == 1 ? 2 : 1;
     static constexpr int kStages = kE4m3 ? 3 : 4;
     static constexpr int kRaw = kE4m3 ? 3 : 0;
-    static constexpr int kAuxWarps = kE4m3 ? 7 : 3;
+    static constexpr int kAuxWarps = kE4m3 ? (kParts == 1 ? 7 : 8) : 3;
     static constexpr int kSoft = 4 * kHalves;                 // softmax warps
     static constexpr int kAux0 = kSoft + 1 + 2 * kHalves;     // first of the others
     static constexpr int kThreads = (kAux0 + kAuxWarps) * 32;
@@ -670,10 +670,15 @@ __device__ void softmax_role(const AttendArgs& a, Shared& sh, uint32_t tmem, int
 template <bool kE4m3, int kParts>
 __device__ void aux_role(const AttendArgs& a, Shared& sh, uint8_t* smem) {
     using S = Shape<kE4m3, kParts>;
-    constexpr int kT = S::kAuxWarps * 32;
     const int tid = threadIdx.x - S::kAux0 * 32, lane = tid & 31;
     volatile int32_t* ab = &sh.abort;
     uint32_t n = 0, seg = 0, use = 0;   // use: tiles of the ring seen
+    // (8-bit: this thread's places in a tile of codes and in a tile of bf16)
+    const int j = lane & 3, odd = lane >> 2 & 1;
+    const int in0 = 16 * (j + 4 * odd), in1 = 16 * (j + 4 - 4 * odd);
+    const int at_row = ((2 * j) ^ (lane >> 2)) << 4;
+    const int out0 = odd * kHalfB + at_row, out1 = (1 - odd) * kHalfB + at_row;
+    int turn = tid >> 5;
     while (true) {
         const int slot = n % kRing;
         if (!warp_nap(&sh.info_full[slot], (n / kRing) & 1, ab)) return;
@@ -691,54 +696,54 @@ __device__ void aux_role(const AttendArgs& a, Shared& sh, uint8_t* smem) {
                     const int raw = use % S::kRaw, st = use % S::kStages;
                     if (!warp_nap(&sh.raw_full[raw], (use / S::kRaw) & 1, ab)) return;
                     if (!warp_nap(&sh.kv_empty[st], ((use / S::kStages) & 1) ^ 1, ab)) return;
+                    // A warp takes 8 rows at a time, 4 lanes a row, a lane its pieces of 16 codes j
+                    // and j + 4 (odd rows the other way round): in every access 8 lanes meet no
+                    // bank twice. Which warp takes a piece more moves on from tile to tile.
                     const uint8_t* src = smem + S::kRawAt + raw * kRawB;
                     const uint8_t* sc = smem + S::kScaleAt + raw * kBlk;
                     uint8_t* dst = smem + S::kKV + st * kStageB;
-                    // A thread takes 16 codes; 8 lanes a row. The pieces that 8 lanes read are one
-                    // row, and those they write (two each) meet no bank twice.
-#pragma unroll 2
-                    for (int i = tid; i < kBlk * 8; i += kT) {
-                        const int row = i >> 3, j = i & 7, tok = block * kBlk + row;
-                        const uint4 w4 = *reinterpret_cast<const uint4*>(src + row * D + j * 16);
-                        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-                        const int byte = sc[row];
+#pragma unroll 1
+                    for (int g = turn; g < kBlk / 8; g += S::kAuxWarps) {
+                        const int row = 8 * g + (lane >> 2), byte = sc[row];
                         // code * 2^(byte - 127): the bf16 patterns are 2^-120 too small; the
                         // factor 2^(byte - 7) takes two steps where it is above 2^127
                         uint32_t f = static_cast<uint32_t>(min(byte + 120, 254)) << 7;
                         if (byte == kNanRow) f = 0x7fc0u;
                         f |= f << 16;
-                        uint32_t y[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t x = k & 1 ? prmt_i<0x3424>(w[k >> 1], 0)
-                                                     : prmt_i<0x1404>(w[k >> 1], 0);
-                            y[k] = mul_bf2((x & 0x80008000u) | ((x >> 4) & 0x07f007f0u), f);
-                        }
-                        if (__builtin_expect(byte > 134 && byte != kNanRow, 0)) {
-                            const uint32_t f2 = static_cast<uint32_t>(byte - 134 + 127) << 7;
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) y[k] = mul_bf2(y[k], f2 | f2 << 16);
-                        }
+                        bool zero = false;
                         if (__builtin_expect(flags & kFix, 0)) {
-                            bool zero = !(sh.entry[slot].mask[row >> 5] >> (row & 31) & 1);
+                            const int tok = block * kBlk + row;
+                            zero = !(sh.entry[slot].mask[row >> 5] >> (row & 31) & 1);
                             if (t == 1 && !zero && byte == kNanRow && tok > shared) {
-                                for (int k = 0; k < 16; ++k) mark(16 * j + k, tok);
+#pragma unroll 1
+                                for (int k = 0; k < D; k += 4) mark(k + j, tok);
                                 zero = true;
                             }
-                            if (zero) {
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) y[k] = 0;
-                            }
                         }
-                        // pieces 2 j and 2 j + 1 of the row; the lanes of the second 64 columns
-                        // write them in the other order
-                        uint8_t* to = dst + (j >> 2) * kHalfB + row * 128;
-                        const int c0 = (((2 * j) & 7) ^ (row & 7)) << 4;
-                        const bool odd = j & 4;
-                        const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]);
-                        const uint4 hi = make_uint4(y[4], y[5], y[6], y[7]);
-                        *reinterpret_cast<uint4*>(to + (odd ? c0 ^ 16 : c0)) = odd ? hi : lo;
-                        *reinterpret_cast<uint4*>(to + (odd ? c0 : c0 ^ 16)) = odd ? lo : hi;
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            const uint4 w4 =
+                                *reinterpret_cast<const uint4*>(src + row * D + (p ? in1 : in0));
+                            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+                            uint32_t y[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const uint32_t x = k & 1 ? prmt_i<0x3424>(w[k >> 1], 0)
+                                                         : prmt_i<0x1404>(w[k >> 1], 0);
+                                y[k] = mul_bf2((x & 0x80008000u) | ((x >> 4) & 0x07f007f0u), f);
+                            }
+                            if (__builtin_expect(zero || (byte > 134 && byte != kNanRow), 0)) {
+                                const uint32_t f2 = static_cast<uint32_t>(byte - 134 + 127) << 7;
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    y[k] = zero ? 0u : mul_bf2(y[k], f2 | f2 << 16);
+                            }
+                            uint8_t* to = dst + row * 128;
+                            const int c = p ? out1 : out0;
+                            *reinterpret_cast<uint4*>(to + c) = make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4*>(to + (c ^ 16)) =
+                                make_uint4(y[4], y[5], y[6], y[7]);
+                        }
                     }
                     fence_async_smem();
                     __syncwarp();
@@ -747,6 +752,8 @@ __device__ void aux_role(const AttendArgs& a, Shared& sh, uint8_t* smem) {
                         arrive(&sh.raw_empty[raw]);
                     }
                     ++use;
+                    turn += (S::kAuxWarps - kBlk / 8 % S::kAuxWarps) % S::kAuxWarps;
+                    turn -= turn >= S::kAuxWarps ? S::kAuxWarps : 0;
                 }
             } else {
                 const int st = (use + 1) % S::kStages;
