@@ -222,6 +222,7 @@ paged_read_kernel(const PagePool pool, const Seqs c, int heads, int64_t first, i
         }
     }
     Out* dst = (is_v ? V : K) + ((static_cast<int64_t>(s) * heads + h) * ld) * D + l8;
+    const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
 #pragma unroll
     for (int i = 0; i < kReadRun / 2; ++i) {
         const int64_t pos = p0 + 2 * i + (lane >> 4);
@@ -245,8 +246,10 @@ paged_read_kernel(const PagePool pool, const Seqs c, int heads, int64_t first, i
         if constexpr (sizeof(Out) == 2) {
             *reinterpret_cast<uint4*>(o) = kE4m3 ? pack8(v) : raw[i];
         } else {
-            *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4*>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            uint32_t u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(v[k]);
+            store_words<8>(o, u, wide);
         }
     }
 }

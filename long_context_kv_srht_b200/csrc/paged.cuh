@@ -31,6 +31,24 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
     return byte == kNanRow ? __uint_as_float(0x7fc00000u) : __uint_as_float(byte << 23);
 }
 
+// kN words to memory, 32 bytes a store where the address is a multiple of 32 (else 16)
+template <int kN>
+__device__ __forceinline__ void store_words(void* dst, const uint32_t* w, bool wide) {
+#pragma unroll
+    for (int i = 0; i < kN; i += 8) {
+        uint32_t* d = static_cast<uint32_t*>(dst) + i;
+        const uint32_t* x = w + i;
+        if (wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                         :: "l"(d), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]),
+                            "r"(x[5]), "r"(x[6]), "r"(x[7]) : "memory");
+        } else {
+            reinterpret_cast<uint4*>(d)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+            reinterpret_cast<uint4*>(d)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+        }
+    }
+}
+
 // ---- device views ----
 struct PagePool {
     uint8_t* k;

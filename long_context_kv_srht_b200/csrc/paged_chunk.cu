@@ -27,8 +27,9 @@
 // take the other half's columns, and a tile is 128 rows.
 //
 // Roles, by warp: 0-3 and 4-7 softmax and output of the halves, 8 loads, 9 to 12 the halves'
-// scores and products, 13 and up repair (bf16) or widening (8-bit). They meet in mbarriers; every wait gives up after
-// kWaitLimitNs, which ends the whole CTA in order and reaches the caller as a status.
+// scores and products, 13 and up repair (bf16) or widening (8-bit); with one half there are four
+// softmax and two product warps. They meet in mbarriers; every wait gives up after kWaitLimitNs,
+// which ends the whole CTA in order and reaches the caller as a status.
 #include "paged_async.cuh"
 
 namespace pkv {
@@ -115,24 +116,6 @@ __device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
-}
-
-// kN words to memory, 32 bytes a store where the address is a multiple of 32 (else 16)
-template <int kN>
-__device__ __forceinline__ void store_words(void* dst, const uint32_t* w, bool wide) {
-#pragma unroll
-    for (int i = 0; i < kN; i += 8) {
-        uint32_t* d = static_cast<uint32_t*>(dst) + i;
-        const uint32_t* x = w + i;
-        if (wide) {
-            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                         :: "l"(d), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]),
-                            "r"(x[5]), "r"(x[6]), "r"(x[7]) : "memory");
-        } else {
-            reinterpret_cast<uint4*>(d)[0] = make_uint4(x[0], x[1], x[2], x[3]);
-            reinterpret_cast<uint4*>(d)[1] = make_uint4(x[4], x[5], x[6], x[7]);
-        }
-    }
 }
 
 // the last token that row r of a tile may attend (-1: none)

@@ -214,6 +214,12 @@ def test_read_matches_pages(fmt, dtype, page, kv, first, n, holes):
                 wK[s, :, t - first], wV[s, :, t - first] = cache.k[p, :, r], cache.v[p, :, r]
     np.testing.assert_array_equal(K.float().cpu().numpy(), wK)
     np.testing.assert_array_equal(V.float().cpu().numpy(), wV)
+    # slabs on 16 bytes but not on 32
+    pad = 16 // K.element_size()
+    both = [torch.full((K.numel() + pad,), -7.0, dtype=td, device=DEV)[pad:].view(shape) for _ in range(2)]
+    assert all(t.data_ptr() % 32 == 16 for t in both)
+    pk.paged_read(c.cfg, c.pool(), c.chunk, first, n, *both)
+    assert torch.equal(both[0], K) and torch.equal(both[1], V)
     # one of the two alone, and into pinned host memory
     V2 = torch.full(shape, -7.0, dtype=td).pin_memory()
     pk.paged_read(c.cfg, c.pool(), c.chunk, first, n, V=V2)
