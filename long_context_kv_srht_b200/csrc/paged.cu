@@ -31,7 +31,10 @@ __device__ __forceinline__ uint4 pack8(const float v[8]) {
 // a time, 16 lanes a row and 8 elements a lane. The first rows are under way while the warp finds
 // out where they go (a chain of dependent loads: starts, lengths, the page's id). Bound by HBM: it
 // reads each row once and writes 256 or 129 bytes of it; neighbouring tokens are in neighbouring
-// warps of a CTA, so the 128-byte pieces of a head's rows meet in L2.
+// warps of a CTA, so the 128-byte pieces of a head's rows meet in L2. 131072 tokens of 8 heads from
+// bf16 to 8 bits: 157 us, 5.1 TB/s, two thirds of it reads (the 1-byte stores of the scales cost 4%
+// of that; streaming hints, 4 or 16 warps a CTA and 32-byte loads nothing or less). 16 tokens: 7.6
+// us, the launch and the chain of four dependent loads.
 constexpr int kWriteWarps = 8;
 
 // four values to e4m3, nearest even, saturating
@@ -175,7 +178,9 @@ paged_write_kernel(const PagePool pool, const Seqs c, int heads, const In* __res
 // ------------------------------------------------------------------------------------- read
 // A warp takes 16 consecutive positions (aligned, so they lie in one page) of one KV head of K
 // or of V: 8 loads of two rows in flight, then 8 stores. Both sides are contiguous runs of 16
-// rows. Bound by HBM.
+// rows. Bound by HBM: 131072 tokens of 8 heads from 8 bits to bf16 132 us, 6.1 TB/s; a window of
+// bf16 pages to fp32 31 us, 5.35 TB/s, with 32 bytes a store (37 us with two stores of 16, which
+// is what slabs that begin off 32 bytes get).
 constexpr int kReadWarps = 8;
 constexpr int kReadRun = 16;
 
@@ -307,7 +312,8 @@ __device__ __forceinline__ void mark_live(const Seqs& c, const PagePool& pool, c
     }
 }
 
-// One CTA: counts each sequence's tiles, writes the tiles in order, and sums their blocks.
+// One CTA: counts each sequence's tiles, writes the tiles in order, and sums their blocks. Bound by
+// latency (a scan, and a chain of loads a sequence): 5 us of a call.
 __global__ void __launch_bounds__(kPlanT)
 plan_kernel(const Seqs c, const PagePool pool, const PlanShape p, const Plan plan) {
     const int shift = pool.shift;
@@ -380,8 +386,12 @@ plan_kernel(const Seqs c, const PagePool pool, const PlanShape p, const Plan pla
 
 // ------------------------------------------------------------------------------------- join
 // The tile that the cut before CTA blockIdx.x + 1 goes through, if that cut is the tile's first: its
-// parts are rescaled to the common maximum and summed. A warp a row, 4 elements a lane; with many parts (few rows, a long
-// token axis) the CTA's warps share a row's parts and add their sums up in order.
+// parts are rescaled to the common maximum and summed. A warp a row, 4 elements a lane. Where a
+// tile has many parts and fewer rows than there are warps (few rows, a long token axis), the
+// CTA's warps share a row's parts and add their sums up in order. Measured, whole calls: one row a
+// group of 4 over 65536 tokens 52.0 us with shared rows, 58.3 without (37 parts a head); 64 tokens
+// over 65536 (256 rows a head, 19 parts) 129 us with shared rows, 118 without. Bound by the latency
+// of its two dependent loads (record, parts): some 4 us of a call.
 constexpr int kJoinWarps = 4;
 constexpr int kJoinShared = 8;    // parts from which on the warps share a row
 
@@ -397,7 +407,7 @@ join_kernel(const AttendArgs a) {
     const int parts = t.parts;
     const int64_t h = t.head;
     const int R = a.shape.tile_rows, G = a.shape.group;
-    const bool shared = parts >= kJoinShared;
+    const bool shared = parts >= kJoinShared && t.nrow < static_cast<int>(gridDim.y) * kJoinWarps;
     const size_t step = 2 * part_floats(R);
     // part i: slot 2 (c0 + i), the first one 2 c0 + 1
     const float* base = a.work + 2 * static_cast<size_t>(t.c0) * part_floats(R);
@@ -590,10 +600,14 @@ pariskv_status pariskv_paged_write(const pariskv_config* cfg, const pariskv_page
     const float* vf = static_cast<const float*>(v_new);
     const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(k_new);
     const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(v_new);
-    if (f32 && e4) paged_write_kernel<float, true><<<grid, t, 0, st>>>(p, c, h, kf, vf, k_ld, v_ld);
-    else if (f32) paged_write_kernel<float, false><<<grid, t, 0, st>>>(p, c, h, kf, vf, k_ld, v_ld);
-    else if (e4) paged_write_kernel<__nv_bfloat16, true><<<grid, t, 0, st>>>(p, c, h, kb, vb, k_ld, v_ld);
-    else paged_write_kernel<__nv_bfloat16, false><<<grid, t, 0, st>>>(p, c, h, kb, vb, k_ld, v_ld);
+    if (f32) {
+        auto kernel = e4 ? paged_write_kernel<float, true> : paged_write_kernel<float, false>;
+        kernel<<<grid, t, 0, st>>>(p, c, h, kf, vf, k_ld, v_ld);
+    } else {
+        auto kernel = e4 ? paged_write_kernel<__nv_bfloat16, true>
+                         : paged_write_kernel<__nv_bfloat16, false>;
+        kernel<<<grid, t, 0, st>>>(p, c, h, kb, vb, k_ld, v_ld);
+    }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "page write launch");
     set_last_launches(1);
@@ -627,10 +641,14 @@ pariskv_status pariskv_paged_read(const pariskv_config* cfg, const pariskv_pages
     const bool e4 = pages->format == PARISKV_PAGES_E4M3, f32 = cfg->dtype == PARISKV_F32;
     float *Kf = static_cast<float*>(K), *Vf = static_cast<float*>(V);
     __nv_bfloat16 *Kb = static_cast<__nv_bfloat16*>(K), *Vb = static_cast<__nv_bfloat16*>(V);
-    if (f32 && e4) paged_read_kernel<float, true><<<grid, t, 0, st>>>(p, c, h, first, n, Kf, Vf, ld_tok, runs, total);
-    else if (f32) paged_read_kernel<float, false><<<grid, t, 0, st>>>(p, c, h, first, n, Kf, Vf, ld_tok, runs, total);
-    else if (e4) paged_read_kernel<__nv_bfloat16, true><<<grid, t, 0, st>>>(p, c, h, first, n, Kb, Vb, ld_tok, runs, total);
-    else paged_read_kernel<__nv_bfloat16, false><<<grid, t, 0, st>>>(p, c, h, first, n, Kb, Vb, ld_tok, runs, total);
+    if (f32) {
+        auto kernel = e4 ? paged_read_kernel<float, true> : paged_read_kernel<float, false>;
+        kernel<<<grid, t, 0, st>>>(p, c, h, first, n, Kf, Vf, ld_tok, runs, total);
+    } else {
+        auto kernel = e4 ? paged_read_kernel<__nv_bfloat16, true>
+                         : paged_read_kernel<__nv_bfloat16, false>;
+        kernel<<<grid, t, 0, st>>>(p, c, h, first, n, Kb, Vb, ld_tok, runs, total);
+    }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "page read launch");
     set_last_launches(1);

@@ -110,8 +110,9 @@ inline EncodeTiled encode_tiled() {
 
 // a 3-d tensor of rows of 128 elements (bytes or bf16); boxes of `cols` x r1 x r2, their 128-byte
 // rows swizzled in shared memory or not
-inline bool encode_rows(CUtensorMap* m, const void* base, bool bytes, bool swizzle, uint64_t n1, uint64_t n2, uint64_t s1,
-            uint64_t s2, uint32_t cols, uint32_t r1, uint32_t r2) {
+inline bool encode_rows(CUtensorMap* m, const void* base, bool bytes, bool swizzle, uint64_t n1,
+                        uint64_t n2, uint64_t s1, uint64_t s2, uint32_t cols, uint32_t r1,
+                        uint32_t r2) {
     const EncodeTiled fn = encode_tiled();
     if (!fn) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), n1, n2}, strides[2] = {s1, s2};

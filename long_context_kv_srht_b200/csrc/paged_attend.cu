@@ -7,10 +7,10 @@
 // copies under way, and to spend few instructions a token:
 //  - all rows of a tile (up to 8 or 16: tokens x heads of the KV head's group) share one pass
 //    over K and V;
-//  - the (head, sequence) streams of a batch form one axis of 64- or 128-token blocks that is cut into
-//    equal ranges, two CTAs an SM, so ragged lengths leave no SM idle (see Plan). A block has 128
-//    tokens in 8 bits: what a block costs besides its bytes (the loading warp's walk, the waits)
-//    bounded 64-token blocks there;
+//  - the (head, sequence) streams of a batch form one axis of 64- or 128-token blocks that is cut
+//    into equal ranges, two CTAs an SM, so ragged lengths leave no SM idle (see Plan). A block has
+//    128 tokens in 8 bits: what a block costs besides its bytes (the loading warp's walk, the
+//    waits) bounds 64-token blocks there (131072 tokens of 8 heads: 66.8 us with 64, 58.9 with 128);
 //  - one warp walks the range and brings the pages by TMA into rings of K and of V tiles, across
 //    the ends of sequences; four warps take 16 of every 64 tokens each, held together by mbarriers
 //    only (no barrier of the CTA in the loop);
@@ -28,6 +28,14 @@
 //    bits), three (24 bits and more) for fp32 output;
 //  - a row's maximum is only brought up to date (three shuffles, O rescaled) when a score exceeds
 //    it by more than 2^8; sums stay per lane until the end of a range, where the warps merge.
+//
+// Measured (8 KV heads, groups of 4, whole calls): 16 sequences of 65536 bf16 tokens 600 us, 7.2
+// TB/s, HBM's bound; one of 131072 8-bit tokens 59 us, 4.5 TB/s, bound by the latency of the eight
+// consuming warps an SM between a block's waits; one of 4096 bf16 tokens 17 us, bound by the chain
+// of launch, lengths, page ids, tiles and the join. Why tiles of 8 and of 16 rows: 2 tokens over
+// 65536 (8 rows) take 53.2 us in tiles of 8 and 55.0 in tiles of 16 in bf16, 39.6 and 57.0 in 8
+// bits. Why not the chunk kernel's tiles up to 16 rows: 4 tokens over 65536 take 59.2 us here and
+// 66.2 there in bf16, 61.4 and 85.2 in 8 bits; 8 sequences of 32768 170 and 204, 170 and 263.
 #include <cuda_fp16.h>
 
 #include "paged_async.cuh"
@@ -37,7 +45,10 @@ namespace pkv {
 namespace {
 
 constexpr int kFW = 4;                        // warps, 16 of every 64 tokens each
-constexpr int kInline = 256;                  // sequences that every CTA plans for itself
+// Sequences that every CTA plans for itself. The plan kernel costs 5 us more at 1 sequence (52.0 and
+// 57.0 us a call over 65536 tokens) and still 14 us at 256 of 2000 tokens (306 and 319); the sums
+// of 256 sequences are what shared memory is kept for.
+constexpr int kInline = 256;
 constexpr int kSegs = 8;                      // segment records between the loads and the others
 constexpr float kGrow = 8.0f;                 // growth of a maximum (base 2) that rescales O
 
@@ -130,8 +141,12 @@ __device__ __forceinline__ uint32_t widen2(uint16_t codes) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(codes));
     return y;
 }
-__device__ __forceinline__ uint32_t widen_lo(uint32_t w) { return widen2(static_cast<uint16_t>(w)); }
-__device__ __forceinline__ uint32_t widen_hi(uint32_t w) { return widen2(static_cast<uint16_t>(w >> 16)); }
+__device__ __forceinline__ uint32_t widen_lo(uint32_t w) {
+    return widen2(static_cast<uint16_t>(w));
+}
+__device__ __forceinline__ uint32_t widen_hi(uint32_t w) {
+    return widen2(static_cast<uint16_t>(w >> 16));
+}
 
 // The last of n + 1 sums with pre[i] <= x.
 __device__ __forceinline__ int find_pre(const int64_t* pre, int n, int64_t x) {
@@ -164,7 +179,8 @@ __device__ __forceinline__ Tile tile_record(const AttendArgs& a, int s, int64_t 
     t.seq = s;
     t.row0 = v.row0;
     t.first = 0;
-    t.nrow = static_cast<int32_t>(min64(a.shape.tile_rows, static_cast<int64_t>(v.rows) * a.shape.group));
+    t.nrow = static_cast<int32_t>(
+        min64(a.shape.tile_rows, static_cast<int64_t>(v.rows) * a.shape.group));
     t.end = tile_end(v, a.shape, 0);
     t.kv = v.kv;
     t.pad[0] = t.pad[1] = 0;
@@ -243,7 +259,8 @@ __device__ void few_loads(const AttendArgs& a, const CUtensorMap* mk, const CUte
         const int b0 = static_cast<int>(x - start);
         const int b1 = static_cast<int>(min64(nb, range.hi - start));
         if (seg == 0 && lane == 0)
-            a.cut[blockIdx.x] = cut_record(t, range.per_head * a.heads, range.n, start, start + nb, b0, h);
+            a.cut[blockIdx.x] =
+                cut_record(t, range.per_head * a.heads, range.n, start, start + nb, b0, h);
         const int32_t* table = a.seqs.table + static_cast<int64_t>(t.seq) * a.seqs.stride;
         // page ids come 32 at a time, a lane a run, one window ahead
         auto fetch = [&](int w) -> int {
@@ -397,7 +414,8 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                 const bool ok = r < sg.nrow;
                 const int rr = sg.first + (ok ? r : 0);
                 const uint32_t* qr = reinterpret_cast<const uint32_t*>(
-                    a.q + (sg.row0 + rr / G) * a.q_ld + (static_cast<int64_t>(sg.head) * G + rr % G) * D);
+                    a.q + (sg.row0 + rr / G) * a.q_ld +
+                    (static_cast<int64_t>(sg.head) * G + rr % G) * D);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int i0 = kE4m3 ? 32 * (i >> 2) + 8 * t + 2 * (i & 3) : 8 * i + t;
@@ -418,7 +436,8 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     // (in two steps: the power itself may be out of range)
-                    const int e = top >= 0x7f80u || top < 0x80u ? 0 : 127 + 14 - static_cast<int>(top >> 7);
+                    const int e =
+                        top >= 0x7f80u || top < 0x80u ? 0 : 127 + 14 - static_cast<int>(top >> 7);
                     const float f0 = pow2f(e / 2), f1 = pow2f(e - e / 2);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -864,7 +883,8 @@ template <bool kE4m3, int NT>
 cudaError_t launch_few_out(const AttendArgs& a, const CUtensorMap maps[2], bool f32_out, int ctas,
                            bool inline_plan, cudaStream_t st) {
     return f32_out ? launch_few<kE4m3, NT, 3, float>(a, maps, ctas, inline_plan, st)
-                   : launch_few<kE4m3, NT, kE4m3 ? 1 : 2, __nv_bfloat16>(a, maps, ctas, inline_plan, st);
+                   : launch_few<kE4m3, NT, kE4m3 ? 1 : 2, __nv_bfloat16>(a, maps, ctas, inline_plan,
+                                                                         st);
 }
 
 }  // namespace
