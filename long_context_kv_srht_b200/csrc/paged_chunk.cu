@@ -315,13 +315,17 @@ __device__ void load_role(const AttendArgs& a, const CUtensorMap* mq, const CUte
             for (int t = 0; t < 2; ++t) {
                 constexpr int kSlots = kE4m3 ? S::kRaw : S::kStages;
                 const int st = ld % kSlots;
-                uint64_t* full_bar = kE4m3 ? &sh.raw_full[st] : &sh.kv_full[st];
+                // bf16 rows that are looked over before they are used land for those who do that
+                const bool look = !kE4m3 && t == 1 && (e.flags & kFix);
+                uint64_t* full_bar = kE4m3 || look ? &sh.raw_full[st] : &sh.kv_full[st];
                 if (!warp_nap(kE4m3 ? &sh.raw_empty[st] : &sh.kv_empty[st],
                               ((ld / kSlots) & 1) ^ 1, ab))
                     return;
-                if (lane == 0)
+                if (lane == 0) {
                     mbar_arrive_expect_tx(smem_addr(full_bar),
                                           __popc(cur_valid) * run * (kE4m3 ? D + 1 : 2 * D));
+                    if (look) arrive(&sh.kv_full[st]);
+                }
                 __syncwarp();
                 if (mine) {
                     const CUtensorMap* m = t ? mv : mk;
@@ -390,7 +394,7 @@ __device__ void score_role(Shared& sh, uint8_t* smem, uint32_t tmem, int half, b
     const uint64_t k_desc = smem_desc(uniform(smem_addr(smem + S::kKV)), 16);
     const uint32_t s_at = uniform(tmem + S::kS + 128 * half);
     if (inject) {   // test hook: a wait for an arrival that never comes
-        wait_for(&sh.raw_full[3], 0, ab, 1000000ull);
+        wait_for(&sh.raw_empty[3], 0, ab, 1000000ull);
         return;
     }
     uint32_t n = 0, nq = 0, nb = 0, used = 0;   // entries, Q tiles, blocks of the half, K/V tiles
@@ -665,6 +669,7 @@ __device__ void aux_role(const AttendArgs& a, Shared& sh, uint8_t* smem) {
     const int tid = threadIdx.x - S::kAux0 * 32, lane = tid & 31;
     volatile int32_t* ab = &sh.abort;
     uint32_t n = 0, seg = 0, use = 0;   // use: tiles of the ring seen
+    uint32_t looked = 0;                // a bit a stage: parity of the looks at it (bf16)
     // (8-bit: this thread's places in a tile of codes and in a tile of bf16)
     const int j = lane & 3, odd = lane >> 2 & 1;
     const int in0 = 16 * (j + 4 * odd), in1 = 16 * (j + 4 - 4 * odd);
@@ -750,7 +755,11 @@ __device__ void aux_role(const AttendArgs& a, Shared& sh, uint8_t* smem) {
             } else {
                 const int st = (use + 1) % S::kStages;
                 if (flags & kFix) {
-                    if (!warp_nap(&sh.kv_full[st], ((use + 1) / S::kStages) & 1, ab)) return;
+                    // (a barrier of their own, waited for at each of its phases: a wait for a phase
+                    // of kv_full, of which some are passed over, could be answered for the one
+                    // two before it)
+                    if (!warp_nap(&sh.raw_full[st], looked >> st & 1, ab)) return;
+                    looked ^= 1u << st;
                     // rows from the first one that needs a look: all past `shared`, and all of a
                     // block that is not whole; a warp takes 4 rows of 64 columns at a time, 4
                     // such pieces in flight

@@ -402,6 +402,47 @@ def test_many_tiles_a_cta(fmt, out_dtype, causal):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,n", [(8, 1600), (4, 1984)])
+def test_masked_blocks_soon_after_a_cta_begins(fmt, heads, n):
+    """Prompts whose ranges begin a few blocks before the end of a tile, so that a block that is
+    masked and looked over for its V comes while the first copies are still under way, out of a
+    cold L2 as well. Against the formula in 64 bits: one rounding of the output and one of the
+    weights to bf16, and the same bits from every call."""
+    rng = np.random.default_rng(n)
+    page, width = 64, -(-n // 64)
+    dt = torch.bfloat16
+    k, v = (torch.randn((width, heads, page, D), device=DEV).to(dt) for _ in range(2))
+    table = rng.permutation(width).astype(np.int32)
+    if fmt == "bf16":
+        pages, kf, vf = pk.Pages(k, v), k.double(), v.double()
+    else:
+        one = torch.full((width, heads, page), 127, dtype=torch.uint8, device=DEV)
+        k, v = k.to(torch.float8_e4m3fn), v.to(torch.float8_e4m3fn)
+        pages, kf, vf = pk.Pages(k, v, one, one.clone()), k.double(), v.double()
+    chunk = pk.Chunk(_dev(table[None]), _dev(np.array([n], np.int32)), _dev(np.array([0, n], np.int32)),
+                     n, n)
+    cfg = pk.config(batch=1, num_kv_heads=heads, group=4, dtype="bf16")
+    q = torch.randn((n, heads * 4, D), device=DEV).to(dt)
+    order = torch.tensor(table.astype(np.int64), device=DEV)
+    kf, vf = (x[order].permute(1, 0, 2, 3).reshape(heads, width * page, D)[:, :n] for x in (kf, vf))
+    late = torch.ones((n, n), dtype=torch.bool, device=DEV).triu(1)
+    want, weight = (torch.empty((n, heads * 4, D), dtype=torch.float64, device=DEV) for _ in range(2))
+    for h in range(heads * 4):
+        p = (q[:, h].double() @ kf[h // 4].T * SCALE).masked_fill(late, -np.inf).softmax(-1)
+        want[:, h], weight[:, h] = p @ vf[h // 4], p @ vf[h // 4].abs()
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device=DEV)
+    first = None
+    for i in range(6):
+        flush.fill_(i)
+        out, _ = pk.paged_attend(cfg, pages, chunk, q, SCALE)
+        # (the scores' part of the bound, 2 * 136 * 2^-23 of at most some 30, is below 2^-9)
+        tol = 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -9) * weight
+        assert ((out.double() - want).abs() <= tol).all()
+        assert first is None or torch.equal(out, first)
+        first = out
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("q,page", [([3, 2], 16), ([90, 33], 16), ([90, 33], 128)])
 def test_long_caches_of_which_little_is_left(fmt, out_dtype, q, page):
