@@ -27,14 +27,14 @@ __device__ __forceinline__ uint4 pack8(const float v[8]) {
 }
 
 // ------------------------------------------------------------------------------------ write
-// A warp takes one new token: 2 * heads rows of 128 elements (K of every head, then V), two at
-// a time, 16 lanes a row and 8 elements a lane. The first rows are under way while the warp finds
-// out where they go (a chain of dependent loads: starts, lengths, the page's id). Bound by HBM: it
+// A warp takes one new token, a head at a time: 16 lanes its K row and 16 its V row, 8 elements a
+// lane. The first rows are under way while the warp finds out where they go (a chain of dependent loads: starts, lengths, the page's id). Bound by HBM: it
 // reads each row once and writes 256 or 129 bytes of it; neighbouring tokens are in neighbouring
 // warps of a CTA, so the 128-byte pieces of a head's rows meet in L2. 131072 tokens of 8 heads from
-// bf16 to 8 bits: 157 us, 5.1 TB/s, two thirds of it reads (the 1-byte stores of the scales cost 4%
-// of that; streaming hints, 4 or 16 warps a CTA and 32-byte loads nothing or less). 16 tokens: 7.6
-// us, the launch and the chain of four dependent loads.
+// bf16 to 8 bits: 142 us, 5.7 TB/s, two thirds of it reads (158 us when a lane's rows were K's of
+// one head and then another's: twice the instructions; 170 us with 32 lanes a row, whose maximum
+// is one instruction, but whose stores are half as wide). 16 tokens: 7.6 us, the launch and the
+// chain of four dependent loads.
 constexpr int kWriteWarps = 8;
 
 // four values to e4m3, nearest even, saturating
@@ -49,12 +49,11 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 template <typename In> struct Raw8;
 template <> struct Raw8<float> {
     float4 a, b;
-    static constexpr int kRows = 4;      // row pairs in flight
+    static constexpr int kRows = 4;      // heads in flight
     __device__ __forceinline__ void load(const float* p) {
         a = __ldcs(reinterpret_cast<const float4*>(p));
         b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
     }
-    __device__ __forceinline__ void clear() { a = b = make_float4(0, 0, 0, 0); }
     __device__ __forceinline__ uint4 bf16() const {
         return make_uint4(bf16_pair(a.x, a.y), bf16_pair(a.z, a.w), bf16_pair(b.x, b.y),
                           bf16_pair(b.z, b.w));
@@ -80,7 +79,6 @@ template <> struct Raw8<__nv_bfloat16> {
     __device__ __forceinline__ void load(const __nv_bfloat16* p) {
         a = __ldcs(reinterpret_cast<const uint4*>(p));
     }
-    __device__ __forceinline__ void clear() { a = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ uint4 bf16() const { return a; }
     __device__ __forceinline__ uint32_t top() const {   // two magnitudes a word
         constexpr uint32_t m = 0x7fff7fffu;
@@ -114,18 +112,12 @@ paged_write_kernel(const PagePool pool, const Seqs c, int heads, const In* __res
     const int64_t tok = static_cast<int64_t>(blockIdx.x) * kWriteWarps + warp;
     if (tok >= c.total_q) return;
     const int half = lane >> 4, l8 = (lane & 15) * 8;
+    const In* const src = (half ? vn + tok * v_ld : kn + tok * k_ld) + l8;
     Raw8<In> x[kRows];
-    auto load = [&](int r0) {
+    auto load = [&](int h0) {
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int r = r0 + 2 * i + half;
-            const bool is_v = r >= heads;
-            if (r < 2 * heads)
-                x[i].load((is_v ? vn + tok * v_ld : kn + tok * k_ld) +
-                          static_cast<int64_t>(is_v ? r - heads : r) * D + l8);
-            else
-                x[i].clear();
-        }
+        for (int i = 0; i < kRows; ++i)
+            if (h0 + i < heads) x[i].load(src + (h0 + i) * D);
     };
     load(0);
     // the sequence of the token: the last start <= tok
@@ -147,30 +139,25 @@ paged_write_kernel(const PagePool pool, const Seqs c, int heads, const In* __res
     const int slot = static_cast<int>(pos) & ((1 << pool.shift) - 1);
 
     constexpr int kEl = kE4m3 ? 1 : 2;
-    uint8_t* const kp = pool.k + page * pool.page_bytes + l8 * kEl;
-    uint8_t* const vp = pool.v + page * pool.page_bytes + l8 * kEl;
-    for (int r0 = 0; r0 < 2 * heads; r0 += 2 * kRows) {
-        if (r0 > 0) load(r0);
+    uint8_t* to = (half ? pool.v : pool.k) + page * pool.page_bytes + (slot * D + l8) * kEl;
+    uint8_t* scale = (half ? pool.vs : pool.ks) + (page * pool.scale_stride + slot);
+    for (int h0 = 0; h0 < heads; h0 += kRows) {
+        if (h0 > 0) load(h0);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            const int r = r0 + 2 * i + half;
-            const bool live = r < 2 * heads, is_v = r >= heads;
-            const uint32_t row = static_cast<uint32_t>(is_v ? r - heads : r) << pool.shift | slot;
-            uint8_t* to = (is_v ? vp : kp) + static_cast<uint64_t>(row) * (D * kEl);
+            if (h0 + i >= heads) break;
             if (!kE4m3) {
-                if (live) *reinterpret_cast<uint4*>(to) = x[i].bf16();
-                continue;
+                *reinterpret_cast<uint4*>(to) = x[i].bf16();
+            } else {
+                const uint32_t top = x[i].top();
+                const bool finite = top < 0x7f800000u;
+                const int byte = finite ? scale_byte(__uint_as_float(top)) : kNanRow;
+                *reinterpret_cast<uint2*>(to) =
+                    finite ? x[i].codes(byte - 127) : make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+                if ((lane & 15) == 0) *scale = static_cast<uint8_t>(byte);
+                scale += int64_t{1} << pool.shift;
             }
-            const uint32_t top = x[i].top();
-            const bool finite = top < 0x7f800000u;
-            const int byte = finite ? scale_byte(__uint_as_float(top)) : kNanRow;
-            const uint2 code = finite ? x[i].codes(byte - 127) : make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-            if (live) {
-                *reinterpret_cast<uint2*>(to) = code;
-                if ((lane & 15) == 0)
-                    (is_v ? pool.vs : pool.ks)[page * pool.scale_stride + row] =
-                        static_cast<uint8_t>(byte);
-            }
+            to += static_cast<int64_t>(D * kEl) << pool.shift;
         }
     }
 }
