@@ -115,6 +115,23 @@ __device__ __forceinline__ void mma16(float d[4], const uint32_t a[4], uint32_t 
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// o += f * (the parts of 16 tokens' weights). The tensor cores truncate their sums, which over a
+// long range would shrink o by half a step a product; three parts are wanted for more than that
+// leaves, so their sum begins anew every time and is added with rounding.
+template <bool kF16, int kParts>
+__device__ __forceinline__ void accumulate(float o[4], const uint32_t f[4],
+                                           const uint32_t (&p)[kParts][2]) {
+    if constexpr (kParts < 3) {
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) mma16<kF16>(o, f, p[k][0], p[k][1]);
+    } else {
+        float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = kParts - 1; k >= 0; --k) mma16<kF16>(z, f, p[k][0], p[k][1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] += z[i];
+    }
+}
 __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -726,10 +743,7 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                             f[2 * k + 1] = widen_hi(y);
                         }
 #pragma unroll
-                        for (int j = 0; j < NT; ++j)
-#pragma unroll
-                            for (int k = 0; k < kParts; ++k)
-                                mma16<kE4m3>(o[j][i], f, pb[j][k][0], pb[j][k][1]);
+                        for (int j = 0; j < NT; ++j) accumulate<kE4m3, kParts>(o[j][i], f, pb[j]);
                     }
                 } else {
                     const int row = r0 + j8 + 8 * (mi >> 1), vc = mi & 1;
@@ -741,10 +755,7 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                         ldsm_x4_t(base + (ch >> 3) * (S::kTile / 2) + (((ch & 7) ^ (row & 7)) << 4),
                                   f);
 #pragma unroll
-                        for (int j = 0; j < NT; ++j)
-#pragma unroll
-                            for (int k = 0; k < kParts; ++k)
-                                mma16<kE4m3>(o[j][i], f, pb[j][k][0], pb[j][k][1]);
+                        for (int j = 0; j < NT; ++j) accumulate<kE4m3, kParts>(o[j][i], f, pb[j]);
                     }
                 }
             }

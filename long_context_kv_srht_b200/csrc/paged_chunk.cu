@@ -24,12 +24,15 @@
 //  - blocks without a single page that is there are passed over, and count nothing when the work
 //    is cut into equal ranges (the plan leaves a bit a block).
 //
-// fp32 output takes P in three bf16 parts (24 bits, three products); the parts of one half then
-// take the other half's columns, and a tile is 128 rows.
+// fp32 output takes P in three bf16 parts (24 bits, three products); a tile is then 128 rows, and the
+// other half's columns of tensor memory take the third parts and a sum of O: the tensor cores
+// truncate, which shrinks O by half a step a product, so every 8 blocks O is added to the sum with
+// rounding and begins anew. (512 tokens over 65536, 8 bits: off by 2.7e-6 of the output, 8.6e-5
+// without the sum; 1024 over 16384: 593 us, 580 with a sum every 16 blocks, 545 with none.)
 //
 // Measured (8 KV heads, groups of 4, whole calls, flops counted once a pair): 2048 tokens over
 // 32768 in bf16 1106 us, 963 TFLOP/s; 1024 over 65536 in 8 bits 1260 us, 866 TFLOP/s; a prompt of
-// 8192 621 us, 886 TFLOP/s; a mixed batch with pages given back, 8 bits to fp32, 160 us. In bf16
+// 8192 630 us, 873 TFLOP/s; a mixed batch with pages given back, 8 bits to fp32, 167 us. In bf16
 // the board's power limit lowers the clock to 1.65 GHz or so at that rate, and within a block the
 // softmax waits for the products' latency; in 8 bits the widening takes half of all instructions;
 // short tiles lose their ends (Q's load, the last products, the output's store).
@@ -51,6 +54,7 @@ constexpr int kStageB = 2 * kHalfB;            // a K, V or Q tile: 32 KB
 constexpr int kRawB = kBlk * D;                // a tile of codes: 16 KB
 constexpr int kRing = 8;                       // block entries between the loads and the others
 constexpr float kRescale = 8.0f;               // growth of a maximum (base 2) that rescales O
+constexpr int kFold = 8;                       // blocks after which O goes into its sum (fp32 output)
 
 template <bool kE4m3, int kParts> struct Shape {
     static constexpr int kHalves = kParts == 1 ? 2 : 1;
@@ -62,9 +66,12 @@ template <bool kE4m3, int kParts> struct Shape {
     static constexpr int kThreads = (kAux0 + kAuxWarps) * 32;
     // tensor memory columns
     static constexpr int kS = 0;                              // + 128 half + 64 turn
-    static constexpr int kP = kParts == 1 ? 0 : 128;          // + 128 half, + kPTurn turn, + 32 part
-    static constexpr int kPTurn = kParts == 1 ? 64 : 32 * kParts;
-    static constexpr int kO = kParts == 1 ? 256 : 320;        // + 128 half
+    // weights of a turn: over its scores (the third part: 128 + 32 turn)
+    static constexpr int kO = kParts == 1 ? 256 : 192;        // + 128 half
+    static constexpr int kSum = kO + 128;                     // (three parts) O's sum so far
+    static __device__ __forceinline__ constexpr int weights(int turn, int part) {
+        return part < 2 ? 64 * turn + 32 * part : 128 + 32 * turn;   // + 128 half
+    }
     // shared memory
     static constexpr int kQ = 0;
     static constexpr int kKV = kHalves * kStageB;
@@ -437,8 +444,8 @@ __device__ void weight_role(Shared& sh, uint8_t* smem, uint32_t tmem, int half) 
     volatile int32_t* ab = &sh.abort;
     const bool leader = elect_one();
     const uint64_t v_desc = smem_desc(uniform(smem_addr(smem + S::kKV)), kHalfB);
-    const uint32_t o_at = uniform(tmem + S::kO + 128 * half), p_at = uniform(tmem + S::kP + 128 * half);
-    uint32_t n = 0, nb = 0, used = 1, fix = 0;
+    const uint32_t o_at = uniform(tmem + S::kO + 128 * half), p_at = uniform(tmem + 128 * half);
+    uint32_t n = 0, nb = 0, used = 1, fix = 0, run = 0;   // run: blocks of the tile
 #pragma unroll 1
     while (true) {
         const int flags = next_block(sh, n, leader);
@@ -451,6 +458,8 @@ __device__ void weight_role(Shared& sh, uint8_t* smem, uint32_t tmem, int half) 
         }
         const bool mine = half == 0 || (flags & kTwo);
         const uint64_t v0 = v_desc + st * (kStageB >> 4);
+        run = flags & kFirst ? 0 : run + 1;
+        const bool anew = kParts == 1 ? flags & kFirst : run % kFold == 0;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
             if (mine) {
@@ -460,9 +469,9 @@ __device__ void weight_role(Shared& sh, uint8_t* smem, uint32_t tmem, int half) 
                 for (int p = 0; p < kParts; ++p)
 #pragma unroll
                     for (int j = 0; j < kTurn / 16; ++j)
-                        mma_ts(leader, o_at, p_at + S::kPTurn * w + 32 * p + 8 * j,
+                        mma_ts(leader, o_at, p_at + S::weights(w, p) + 8 * j,
                                v0 + ((w * kTurn * 128 + j * 16 * 128) >> 4), kPV,
-                               !(flags & kFirst) || w > 0 || p > 0 || j > 0);
+                               !anew || w > 0 || p > 0 || j > 0);
                 mma_commit(leader, smem_addr(&sh.pv_done[half][w]));
                 if ((flags & kLast) && w == 1) mma_commit(leader, smem_addr(&sh.o_full[half]));
             }
@@ -475,6 +484,23 @@ __device__ void weight_role(Shared& sh, uint8_t* smem, uint32_t tmem, int half) 
 }
 
 // ----------------------------------------------------------------- softmax and the output
+// 128 columns of a thread's row: to = O, or O and what is in the sum (out of line: the softmax's
+// loop is what the instruction cache is for)
+__device__ __noinline__ void fold(uint32_t to, uint32_t at, uint32_t sum, bool kept) {
+#pragma unroll 1
+    for (int i = 0; i < 128; i += 16) {
+        uint32_t o[16], x[16];
+        tmem_ld16(at + i, o);
+        tmem_ld16(sum + i, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            o[k] = __float_as_uint(__uint_as_float(o[k]) + (kept ? __uint_as_float(x[k]) : 0.0f));
+        tmem_st16(to + i, o);
+    }
+    tmem_wait_st();
+}
+
 // A warpgroup a half, a thread a row.
 template <bool kE4m3, int kParts, typename Out>
 __device__ void softmax_role(const AttendArgs& a, Shared& sh, uint32_t tmem, int half) {
@@ -492,6 +518,7 @@ __device__ void softmax_role(const AttendArgs& a, Shared& sh, uint32_t tmem, int
     uint32_t n = 0, seg = 0, nt = 0, no = 0;   // entries, segments; turns, outputs of this half
     float m = -INFINITY, l = 0.0f;      // the row's maximum (times c) as last used, and its sum
     int lim = -1;
+    uint32_t run = 0;                   // blocks of the tile (fp32 output)
     while (true) {
         const int slot = n % kRing;
         if (!warp_wait(&sh.info_full[slot], (n / kRing) & 1, ab)) return;
@@ -502,12 +529,19 @@ __device__ void softmax_role(const AttendArgs& a, Shared& sh, uint32_t tmem, int
             lim = row_limit(g, a.shape.causal, G, r);
             m = -INFINITY;
             l = 0.0f;
+            run = 0;
         }
         const bool mine = half == 0 || (flags & kTwo);
         if (mine && !(flags & kEmpty)) {
 #pragma unroll 1
             for (int w = 0; w < 2; ++w, ++nt) {
                 const int turn = nt & 1;
+                if (kParts > 1 && w == 0 && run > 0 && run % kFold == 0) {
+                    // (after the products into O of all turns so far)
+                    if (!warp_wait(&sh.pv_done[half][turn ^ 1], (nt - 1) >> 1 & 1, ab)) return;
+                    tc_fence_after();
+                    fold(at0 + S::kSum, at0 + S::kO, at0 + S::kSum, run > kFold);
+                }
                 if (!warp_wait(&sh.s_full[half][turn], nt >> 1 & 1, ab)) return;
                 tc_fence_after();
                 uint32_t s[kTurn];
@@ -551,15 +585,16 @@ __device__ void softmax_role(const AttendArgs& a, Shared& sh, uint32_t tmem, int
                     // before it is: its weights' columns hold these scores)
                     if (!warp_wait(&sh.pv_done[half][turn ^ 1], (nt - 1) >> 1 & 1, ab)) return;
                     tc_fence_after();
+                    const int cols = kParts > 1 && run >= kFold ? 256 : 128;   // the sum too
 #pragma unroll 1
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < cols; i += 16) {
                         uint32_t o[16];
-                        tmem_ld16(at0 + S::kO + 16 * i, o);
+                        tmem_ld16(at0 + S::kO + i, o);
                         tmem_wait_ld();
 #pragma unroll
                         for (int k = 0; k < 16; ++k)
                             o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                        tmem_st16(at0 + S::kO + 16 * i, o);
+                        tmem_st16(at0 + S::kO + i, o);
                     }
                 }
                 const float ms = m == -INFINITY ? 0.0f : m;
@@ -587,7 +622,7 @@ __device__ void softmax_role(const AttendArgs& a, Shared& sh, uint32_t tmem, int
                                 p[2 * i + 1] -= hi_f(x[i]);
                             }
                         }
-                        tmem_st16(at0 + S::kP + S::kPTurn * turn + 32 * k + 16 * q, x);
+                        tmem_st16(at0 + S::weights(turn, k) + 16 * q, x);
                     }
                 }
                 tmem_wait_st();
@@ -597,6 +632,7 @@ __device__ void softmax_role(const AttendArgs& a, Shared& sh, uint32_t tmem, int
                 const float2 y = unpack2(add2(sum[0], sum[1]));
                 l += y.x + y.y;
             }
+            ++run;
         }
         if (flags & kLast) {
             if (mine) {
@@ -604,6 +640,8 @@ __device__ void softmax_role(const AttendArgs& a, Shared& sh, uint32_t tmem, int
                 if (!empty) {
                     if (!warp_wait(&sh.o_full[half], no++ & 1, ab)) return;
                     tc_fence_after();
+                    if (kParts > 1 && run > kFold)
+                        fold(at0 + S::kO, at0 + S::kO, at0 + S::kSum, true);
                 }
                 if (!warp_wait(&sh.bad_full[seg % kRing], (seg / kRing) & 1, ab)) return;
                 const bool bad = sh.any_bad[seg % kRing] != 0;

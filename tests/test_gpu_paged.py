@@ -402,6 +402,40 @@ def test_many_tiles_a_cta(fmt, out_dtype, causal):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rows", [1, 32])
+def test_fp32_sums_do_not_shrink_over_a_long_range(fmt, rows):
+    """2.4 million tokens (a few pages again and again), 128 blocks a CTA, V all of one sign and
+    scores near zero: what truncating sums would take from the output grows with the range. The
+    output is that of the pages once, lse more by ln of how often they come. Bound: at most 192
+    truncated steps of 2^-23 in a row (8 blocks of 8 products of three parts), and roundings of
+    2^-24: 256 turns' sums of 64 weights each (7 additions deep), 16 folds, 296 parts; exponentials
+    2^-22, scores 2 * 136 * 2^-23 of at most 2^-7."""
+    sms, page, few = torch.cuda.get_device_properties(0).multi_processor_count, 64, 64
+    n = sms * 128 * 128 // (few * page)                  # times that the pages come
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(6)
+    k = torch.randn((few, 1, page, D), device=DEV, generator=gen)
+    v = 1 + 0.1 * torch.randn((few, 1, page, D), device=DEV, generator=gen)
+    kind = torch.bfloat16 if fmt == "bf16" else torch.float8_e4m3fn
+    k, v = k.to(kind), v.to(kind)
+    one = torch.full((few, 1, page), 127, dtype=torch.uint8, device=DEV)
+    pages = pk.Pages(k, v, *((one, one.clone()) if fmt == "e4m3" else ()))
+    q = (torch.randn((rows, 4, D), device=DEV, generator=gen) * 2.0 ** -12).to(torch.bfloat16)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    table = torch.arange(few, dtype=torch.int32, device=DEV).repeat(n)[None].contiguous()
+    chunk = pk.Chunk(table, ints([n * few * page]), ints([0, rows]), rows, rows)
+    cfg = pk.config(batch=1, num_kv_heads=1, group=4, dtype="bf16")
+    out, lse = pk.paged_attend(cfg, pages, chunk, q, SCALE, causal=False, want_lse=True,
+                               out_dtype=torch.float32)
+    x = torch.einsum("rhd,td->rht", q.double(), k.double().view(-1, D)) * SCALE
+    want = x.softmax(-1) @ v.double().view(-1, D)
+    rel = (192 + 2 * 136 * 2.0 ** -7 + 2) * 2.0 ** -23 + (256 + 7 + 16 + 296) * 2.0 ** -24
+    assert ((out.double() - want).abs() <= rel * want.abs()).all()
+    more = x.logsumexp(-1) + np.log(n)
+    assert ((lse.double() - more).abs() <= (256 + 7 + 296 + 4) * 2.0 ** -24 + 2.0 ** -23 * more).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("heads,n", [(8, 1600), (4, 1984)])
 def test_masked_blocks_soon_after_a_cta_begins(fmt, heads, n):
     """Prompts whose ranges begin a few blocks before the end of a tile, so that a block that is
