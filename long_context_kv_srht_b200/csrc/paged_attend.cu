@@ -99,37 +99,57 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
-// d += a * b (m16n8k16, fp32 accumulators; bf16 factors, or fp16 ones)
+// d = a * b + c (m16n8k16, fp32 accumulators; bf16 factors, or fp16 ones)
 template <bool kF16>
-__device__ __forceinline__ void mma16(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1,
+                                      float c0, float c1, float c2, float c3) {
     if (kF16)
         asm volatile(
             "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-            "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+            "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1),
+              "f"(c2), "f"(c3));
     else
         asm volatile(
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-            "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+            "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1),
+              "f"(c2), "f"(c3));
 }
-// o += f * (the parts of 16 tokens' weights). The tensor cores truncate their sums, which over a
-// long range would shrink o by half a step a product; three parts are wanted for more than that
-// leaves, so their sum begins anew every time and is added with rounding.
-template <bool kF16, int kParts>
-__device__ __forceinline__ void accumulate(float o[4], const uint32_t f[4],
-                                           const uint32_t (&p)[kParts][2]) {
+template <bool kF16>
+__device__ __forceinline__ void mma16(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+    mma16<kF16>(d, a, b0, b1, d[0], d[1], d[2], d[3]);
+}
+// o[j][i] += f * (the parts of 16 tokens' weights) for every group j of 8 rows. The tensor cores
+// truncate their sums, which over a long range would shrink o by half a step a product; three
+// parts are wanted for more than that leaves, so their sum begins anew every time and is added with
+// rounding. (16 sequences of 4 tokens, 16 rows, over 16384 8-bit tokens: 283 us, 228 with sums left
+// to the tensor cores; single tokens 223 and 217 over 32768.)
+template <bool kF16, int NT, int kParts>
+__device__ __forceinline__ void accumulate(float (&o)[NT][8][4], int i, const uint32_t f[4],
+                                           const uint32_t (&p)[NT][kParts][2]) {
     if constexpr (kParts < 3) {
 #pragma unroll
-        for (int k = 0; k < kParts; ++k) mma16<kF16>(o, f, p[k][0], p[k][1]);
+        for (int k = 0; k < kParts; ++k)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma16<kF16>(o[j][i], f, p[j][k][0], p[j][k][1]);
     } else {
-        float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float z[NT][4];
 #pragma unroll
-        for (int k = kParts - 1; k >= 0; --k) mma16<kF16>(z, f, p[k][0], p[k][1]);
+        for (int k = kParts - 1; k >= 0; --k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] += z[i];
+            for (int j = 0; j < NT; ++j) {
+                if (k == kParts - 1)
+                    mma16<kF16>(z[j], f, p[j][k][0], p[j][k][1], 0.0f, 0.0f, 0.0f, 0.0f);
+                else
+                    mma16<kF16>(z[j], f, p[j][k][0], p[j][k][1]);
+            }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j][i][e] += z[j][e];
     }
 }
 __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
@@ -742,8 +762,7 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                             f[2 * k] = widen_lo(y);
                             f[2 * k + 1] = widen_hi(y);
                         }
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) accumulate<kE4m3, kParts>(o[j][i], f, pb[j]);
+                        accumulate<kE4m3>(o, i, f, pb);
                     }
                 } else {
                     const int row = r0 + j8 + 8 * (mi >> 1), vc = mi & 1;
@@ -754,8 +773,7 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                         const int ch = 2 * i + vc;
                         ldsm_x4_t(base + (ch >> 3) * (S::kTile / 2) + (((ch & 7) ^ (row & 7)) << 4),
                                   f);
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) accumulate<kE4m3, kParts>(o[j][i], f, pb[j]);
+                        accumulate<kE4m3>(o, i, f, pb);
                     }
                 }
             }
