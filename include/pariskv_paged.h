@@ -33,7 +33,8 @@ extern "C" {
  *     code = x / 2^e rounded to nearest even, saturating at 448. The division is exact, so the
  *     codes are the same however they are computed, and code * 2^e is exact in bf16 and fp32.
  *     A row that holds an infinity or a NaN is stored with b = 255 and codes 0x7f; it reads back
- *     as NaN. */
+ *     as NaN. Rows that the caller fills in keep to the same: b in [7, 246] and codes other than
+ *     0x7f and 0xff, or b = 255 and codes 0x7f. */
 enum { PARISKV_PAGES_BF16 = 0, PARISKV_PAGES_E4M3 = 1 };
 
 /* A pool of pages (caller's device memory). Row r of KV head h in page p is the 128 elements

@@ -15,8 +15,8 @@
 //  - O is rescaled only when a row's maximum has grown by more than 2^8 since the last time (P is
 //    then at most 2^8, which costs bf16 nothing), so tensor memory is not read back each block;
 //  - K, V and Q tiles come by TMA through a ring of 32 KB stages, one copy a page and 64 columns;
-//    with 8-bit pages they come as bytes, and seven warps widen them into the ring, scale and all
-//    (a power of two: the bf16 values are exact);
+//    with 8-bit pages they come as bytes, and seven or eight warps widen them into the ring, scale
+//    and all (a power of two: the bf16 values are exact);
 //  - blocks in which some token must not reach some row (the causal edge, the end of the cache,
 //    pages that are not there) are marked: their scores are masked, and their V rows are made
 //    finite first, because 0 * NaN is NaN; what was not finite is put back into the rows that see
@@ -287,7 +287,7 @@ __device__ void load_role(const AttendArgs& a, const CUtensorMap* mq, const CUte
                                       (more >= 32 ? ~0u : (1u << more) - 1);
                 full = full && e.mask[f] == ~0u;
             }
-            const int last_tok = min(end, (cur + 1) * kBlk) - 1;
+            const int last_tok = cur * kBlk + min(end - cur * kBlk, kBlk) - 1;
             if (!full || (causal && last_tok > g.shared)) e.flags |= kFix;
             if (first)
                 for (int i = lane; i < D; i += 32) sh.bad[seg % kRing][i] = INT32_MAX;

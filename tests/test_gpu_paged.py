@@ -435,6 +435,36 @@ def test_fp32_sums_do_not_shrink_over_a_long_range(fmt, rows):
     assert ((lse.double() - more).abs() <= (256 + 7 + 296 + 4) * 2.0 ** -24 + 2.0 ** -23 * more).all()
 
 
+@pytest.mark.parametrize("rows", [1, 32])
+def test_as_many_tokens_as_a_length_can_say(rows):
+    """2^31 - 1 tokens of a few pages again and again, the last block ending 1 short: a row's output
+    is that of the pages once, each token with the number of times that the row sees it. Weights
+    near 1 are added up 2^18 times in a row at most, each time off by 2^-24 of the sum."""
+    page, few, n = 256, 64, (1 << 31) - 1
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(8)
+    k, v = (torch.randn((few, 1, page, D), device=DEV, generator=gen).to(torch.bfloat16)
+            for _ in range(2))
+    v[:, :, 200:] += 2
+    q = (torch.randn((rows, 4, D), device=DEV, generator=gen) * 2.0 ** -6).to(torch.bfloat16)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    table = torch.arange(few, dtype=torch.int32, device=DEV).repeat((n + 1) // (few * page))[None]
+    chunk = pk.Chunk(table.contiguous(), ints([n]), ints([0, rows]), rows, rows)
+    cfg = pk.config(batch=1, num_kv_heads=1, group=4, dtype="bf16")
+    out, lse = pk.paged_attend(cfg, pk.Pages(k, v), chunk, q, SCALE, want_lse=True,
+                               out_dtype=torch.float32)
+    pk.paged_sync()
+    seen = n - rows + 1 + torch.arange(rows, device=DEV)                     # tokens a row sees
+    often = seen[:, None] // (few * page) + \
+        (torch.arange(few * page, device=DEV) < seen[:, None] % (few * page))
+    x = torch.einsum("rhd,td->rht", q.double(), k.double().view(-1, D)) * SCALE
+    x = x + often.double().log()[:, None]
+    want, weight = (x.softmax(-1) @ y.double().view(-1, D) for y in (v, v.abs()))
+    tol = 2.0 ** 18 * 2.0 ** -24
+    assert ((out.double() - want).abs() <= 2 * tol * weight).all()
+    assert ((lse.double() - x.logsumexp(-1)).abs() <= tol).all()
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("heads,n", [(8, 1600), (4, 1984)])
 def test_masked_blocks_soon_after_a_cta_begins(fmt, heads, n):
