@@ -378,8 +378,10 @@ plan_kernel(const Seqs c, const PagePool pool, const PlanShape p, const Plan pla
 // CTA's warps share a row's parts and add their sums up in order. Measured, whole calls: one row a
 // group of 4 over 65536 tokens 52.0 us with shared rows, 58.3 without (37 parts a head); 64 tokens
 // over 65536 (256 rows a head, 19 parts) 129 us with shared rows, 118 without. Bound by the latency
-// of its two dependent loads (record, parts): some 4 us of a call.
-constexpr int kJoinWarps = 4;
+// of its two dependent loads (record, parts), some 4 us of a call, and by the parts' bytes from L2
+// (64 tokens over 2000, 16 parts of 256 rows a head: 42.1 us a call with 4 warps a CTA, 34.7 with 8,
+// 34.8 with 16, which cost few rows 1 us).
+constexpr int kJoinWarps = 8;
 constexpr int kJoinShared = 8;    // parts from which on the warps share a row
 
 template <typename Out>

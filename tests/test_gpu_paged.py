@@ -716,6 +716,11 @@ def test_prompt_in_chunks_to_the_retrieval_index_and_decode(fmt):
     last = pk.Chunk(table, _dev(np.full(2, m, np.int32)), _dev(np.arange(3, dtype=np.int32)), 2, 1)
     dense = pk.dense_attend(cfg, qd, K, V, SCALE, n=m, out_dtype=torch.float32)
     paged, _ = pk.paged_attend(cfg, pages, last, qd, SCALE, out_dtype=torch.float32)
-    # dense and sparse carry the weights in 16 bits (half a step: 2^-17) and sum the same products
-    bound = 2.0 ** -15 * float(V[:, :, :m].abs().max())
+    # of each of the two that are compared: 16 bits of a weight (half a step: 2^-17), scores off by
+    # 136 * 2^-23 of their reach, above and below the bar, sums of m weights, 16 at a time
+    reach = SCALE * max(float(np.einsum("hd,td->ht", np.abs(q[s, n[0], 4 * h:4 * h + 4]),
+                                        np.abs(kept[0][s, h, :m])).max())
+                        for s in range(2) for h in range(heads))
+    bound = 2 * (2.0 ** -17 + 2 * 136 * 2.0 ** -23 * reach + 2 * (m / 16 + 16) * 2.0 ** -23)
+    bound *= float(V[:, :, :m].abs().max())
     assert (dense - paged).abs().max() <= bound and (sparse - paged).abs().max() <= bound
