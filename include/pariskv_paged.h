@@ -107,8 +107,8 @@ PARISKV_API pariskv_status pariskv_paged_read(const pariskv_config* cfg,
  *   out:   device pointer [total_q][num_kv_heads * group][128] of out_dtype, 16-byte aligned.
  *          PARISKV_BF16: the probabilities enter the second product with at least bf16's 8
  *          bits; PARISKV_F32: with 24 bits, so that the result is as exact as fp32 sums are (the
- *          tensor cores truncate theirs, which is bounded to some 2^-18 of sum p |V|, however
- *          many tokens there are).
+ *          tensor cores truncate theirs, which is bounded to some 2^-20 of the output, however many
+ *          tokens there are).
  *   lse:   device pointer [total_q][num_kv_heads * group] fp32, or NULL.
  * Sums, maxima and accumulators are fp32; the accumulators are relative to maxima that may lag by
  * a factor of 2^8, so sums of V's magnitudes over the attended tokens past 2^119 can overflow to

@@ -26,13 +26,14 @@
 //
 // fp32 output takes P in three bf16 parts (24 bits, three products); a tile is then 128 rows, and the
 // other half's columns of tensor memory take the third parts and a sum of O: the tensor cores
-// truncate, which shrinks O by half a step a product, so every 8 blocks O is added to the sum with
-// rounding and begins anew. (512 tokens over 65536, 8 bits: off by 2.7e-6 of the output, 8.6e-5
-// without the sum; 1024 over 16384: 593 us, 580 with a sum every 16 blocks, 545 with none.)
+// truncate, which shrinks O by half a step a product, so every 2 blocks O is added to the sum with
+// rounding and begins anew. (512 tokens over 16384, 8 bits: 357 us and off by 9.5e-7 of the output,
+// a sum in fp32 steps by 2.2e-6; every 8 blocks 322 us and 2.6e-6, every block 405 us and 7.1e-7;
+// without the sum over 65536 tokens 8.6e-5.)
 //
 // Measured (8 KV heads, groups of 4, whole calls, flops counted once a pair): 2048 tokens over
 // 32768 in bf16 1106 us, 963 TFLOP/s; 1024 over 65536 in 8 bits 1260 us, 866 TFLOP/s; a prompt of
-// 8192 630 us, 873 TFLOP/s; a mixed batch with pages given back, 8 bits to fp32, 167 us. In bf16
+// 8192 630 us, 873 TFLOP/s; a mixed batch with pages given back, 8 bits to fp32, 179 us. In bf16
 // the board's power limit lowers the clock to 1.65 GHz or so at that rate, and within a block the
 // softmax waits for the products' latency; in 8 bits the widening takes half of all instructions;
 // short tiles lose their ends (Q's load, the last products, the output's store).
@@ -54,7 +55,7 @@ constexpr int kStageB = 2 * kHalfB;            // a K, V or Q tile: 32 KB
 constexpr int kRawB = kBlk * D;                // a tile of codes: 16 KB
 constexpr int kRing = 8;                       // block entries between the loads and the others
 constexpr float kRescale = 8.0f;               // growth of a maximum (base 2) that rescales O
-constexpr int kFold = 8;                       // blocks after which O goes into its sum (fp32 output)
+constexpr int kFold = 2;                       // blocks after which O goes into its sum (fp32 output)
 
 template <bool kE4m3, int kParts> struct Shape {
     static constexpr int kHalves = kParts == 1 ? 2 : 1;
