@@ -120,3 +120,22 @@ def test_reference_rows_agree_with_the_8_bit_type():
         assert top <= 448 * 2.0 ** e and top > 448 * 2.0 ** (e - 1)
         np.testing.assert_allclose(ref.dequantise(code, byte), x, rtol=2.0 ** -4,
                                    atol=2.0 ** (e - 10))
+
+
+def _ints(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def test_tables_whose_rows_overlap_are_refused():
+    """One row expanded over the batch, or rows closer than they are wide: the library would step
+    past the tensor's end. Rows further apart are a slice of a wider table."""
+    n, q = _ints(4), _ints(5)
+    for table in (_ints(1, 3).expand(4, 3), _ints(3).expand(4, 3), _ints(9).as_strided((4, 3), (2, 1))):
+        with pytest.raises(pk.PariskvError) as e:
+            pk.Chunk(table, n, q, 4, 2)
+        assert e.value.status == pk.EINVAL
+    assert pk.Chunk(_ints(4, 3), n, q, 4, 2).raw.table_stride == 3
+    assert pk.Chunk(_ints(4, 7)[:, :3], n, q, 4, 2).raw.table_stride == 7
+    # (one row has no distance to the next)
+    assert pk.Chunk(_ints(1, 7)[:, :3], n[:1], q[:2], 4, 2).raw.table_stride in (3, 7)
+    assert pk.Chunk(_ints(9).as_strided((1, 3), (1, 1)), n[:1], q[:2], 4, 2).raw.table_stride == 3
