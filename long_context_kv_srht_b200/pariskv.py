@@ -602,11 +602,17 @@ class Chunk:
         self.tensors = (page_table, kv_len, q_start)
         self.batch = page_table.shape[0]
         width = page_table.shape[1]
+        # (ctypes would cut larger numbers down to its fields' bits)
+        for name, x in (("total_q", total_q), ("max_q", max_q)):
+            if not 0 <= int(x) < 1 << 31:
+                _refuse("Chunk", f"{name} {x} is not in [0, 2^31 - 1]")
         # (a single row may have any stride)
         stride = page_table.stride(0) if self.batch > 1 else width
         if stride < width:
             _refuse("Chunk", f"the rows of page_table overlap: they are {width} entries wide and "
                     f"{stride} apart (an expanded table needs .contiguous())")
+        if stride >= 1 << 31:
+            _refuse("Chunk", f"the rows of page_table are {stride} entries apart, 2^31 or more")
         self.raw = _Chunk(page_table.data_ptr(), kv_len.data_ptr(), q_start.data_ptr(),
                           int(total_q), width, stride, int(max_q))
         self.ref = ctypes.byref(self.raw)

@@ -139,3 +139,15 @@ def test_tables_whose_rows_overlap_are_refused():
     # (one row has no distance to the next)
     assert pk.Chunk(_ints(1, 7)[:, :3], n[:1], q[:2], 4, 2).raw.table_stride in (3, 7)
     assert pk.Chunk(_ints(9).as_strided((1, 3), (1, 1)), n[:1], q[:2], 4, 2).raw.table_stride == 3
+
+
+def test_counts_that_the_description_cannot_hold_are_refused():
+    """max_q and total_q are passed in 32 and 64 bits: 2^32 must not become 0 rows."""
+    t, n, q = _ints(2, 3), _ints(2), _ints(3)
+    for total, most in ((4, 1 << 31), (4, 1 << 32), (4, (1 << 32) + 1), (4, -1), (1 << 31, 4),
+                        ((1 << 64) + 3, 4), (-1, 4)):
+        with pytest.raises(pk.PariskvError) as e:
+            pk.Chunk(t, n, q, total, most)
+        assert e.value.status == pk.EINVAL
+    raw = pk.Chunk(t, n, q, (1 << 31) - 1, (1 << 31) - 1).raw
+    assert raw.total_q == raw.max_q == (1 << 31) - 1
