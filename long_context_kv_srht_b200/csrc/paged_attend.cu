@@ -25,7 +25,7 @@
 //  - the 8-bit rows' scales are powers of two: K's multiply the scores, V's go into the exponents
 //    of the weights, which are then relative to maxima of their own (so that they fit fp16);
 //  - P enters the second product in parts: two of bf16 (16 bits; 8-bit pages: one of fp16, 11
-//    bits), three (24 bits and more) for fp32 output;
+//    bits, 8 at 2^-30 of the largest), three (24 bits and more) for fp32 output;
 //  - a row's maximum is only brought up to date (three shuffles, O rescaled) when a score exceeds
 //    it by more than 2^8; sums stay per lane until the end of a range, where the warps merge.
 //
@@ -51,6 +51,16 @@ constexpr int kFW = 4;                        // warps, 16 of every 64 tokens ea
 constexpr int kInline = 256;
 constexpr int kSegs = 8;                      // segment records between the loads and the others
 constexpr float kGrow = 8.0f;                 // growth of a maximum (base 2) that rescales O
+// 8-bit pages: the growth for the maxima of the fp16 weights, and the exponent that the weight of such
+// a maximum gets (together 15: the largest number of fp16 is just below 2^16). fp16's steps end at
+// 2^-24, so one part of a weight is off by 2^-12 of it or 2^-38 of the largest, whichever is more: 8
+// bits down to 2^-30. What one part leaves is taken kPartStep times for the next, so three have 24
+// bits and more down to 2^-36, and are off by 2^-60 of the largest below. (Were the largest 1 and the
+// parts as they are, weights would be cut at 2^-25 of it, in three parts as in one, while their sum
+// has them in full: a tail of 131072 tokens at 2^-26 would be missing. Rescaling at a growth of 2^2
+// costs no more than at 2^8: single tokens over 131072 70.2 us with either.)
+constexpr float kGrow16 = 2.0f, kLift = 13.0f;
+constexpr float kPartStep = 2048.0f;
 
 template <bool kE4m3> struct FewShape {
     static constexpr int kRowB = kE4m3 ? D : 2 * D;          // bytes of a row
@@ -125,8 +135,8 @@ __device__ __forceinline__ void mma16(float d[4], const uint32_t a[4], uint32_t 
 // o[j][i] += f * (the parts of 16 tokens' weights) for every group j of 8 rows. The tensor cores
 // truncate their sums, which over a long range would shrink o by half a step a product; three
 // parts are wanted for more than that leaves, so their sum begins anew every time and is added with
-// rounding. (16 sequences of 4 tokens, 16 rows, over 16384 8-bit tokens: 283 us, 228 with sums left
-// to the tensor cores; single tokens 223 and 217 over 32768.)
+// rounding. (16 sequences of 4 tokens, 16 rows, over 16384 8-bit tokens: 269 us with the parts' sums
+// apart, 316 with one after the other; single tokens over 32768 240 and 242.)
 template <bool kF16, int NT, int kParts>
 __device__ __forceinline__ void accumulate(float (&o)[NT][8][4], int i, const uint32_t f[4],
                                            const uint32_t (&p)[NT][kParts][2]) {
@@ -136,20 +146,28 @@ __device__ __forceinline__ void accumulate(float (&o)[NT][8][4], int i, const ui
 #pragma unroll
             for (int j = 0; j < NT; ++j) mma16<kF16>(o[j][i], f, p[j][k][0], p[j][k][1]);
     } else {
-        float z[NT][4];
+        // (bf16 parts into one sum; fp16 parts, each kPartStep times as large as it counts, apart)
+        constexpr int kSums = kF16 ? kParts : 1;
+        float z[kSums][NT][4];
 #pragma unroll
         for (int k = kParts - 1; k >= 0; --k)
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                if (k == kParts - 1)
-                    mma16<kF16>(z[j], f, p[j][k][0], p[j][k][1], 0.0f, 0.0f, 0.0f, 0.0f);
+                float(&y)[4] = z[kF16 ? k : 0][j];
+                if (kF16 || k == kParts - 1)
+                    mma16<kF16>(y, f, p[j][k][0], p[j][k][1], 0.0f, 0.0f, 0.0f, 0.0f);
                 else
-                    mma16<kF16>(z[j], f, p[j][k][0], p[j][k][1]);
+                    mma16<kF16>(y, f, p[j][k][0], p[j][k][1]);
             }
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][i][e] += z[j][e];
+            for (int e = 0; e < 4; ++e) {
+                float y = z[kSums - 1][j][e];
+#pragma unroll
+                for (int k = kSums - 2; k >= 0; --k) y = fmaf(y, 1.0f / kPartStep, z[k][j][e]);
+                o[j][i][e] += y;
+            }
     }
 }
 __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
@@ -562,7 +580,7 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
         // softmax: weights with the maxima as they are, unless a score is far above
         float w[kSub][NT][4];
         // brings maxima up to date with the scores where one is far above; factors for the old
-        auto raise = [&](float (&top)[NT][2], float (&co)[NT][2]) -> bool {
+        auto raise = [&](float (&top)[NT][2], float (&co)[NT][2], float grow) -> bool {
             bool grown = false;
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
@@ -570,7 +588,7 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        grown = grown || fmaxf(sc[u][j][e], sc[u][j][2 + e]) > top[j][e] + kGrow;
+                        grown = grown || fmaxf(sc[u][j][e], sc[u][j][2 + e]) > top[j][e] + grow;
             if (!__any_sync(0xffffffffu, grown)) return false;
 #pragma unroll
             for (int j = 0; j < NT; ++j)
@@ -598,12 +616,12 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                     o[j][i][2] *= co[j][0]; o[j][i][3] *= co[j][1];
                 }
         };
-        auto weigh = [&](const float (&top)[NT][2]) {
+        auto weigh = [&](const float (&top)[NT][2], float lift) {   // of a maximum: 2^lift
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float ms = top[j][e] == -INFINITY ? 0.0f : top[j][e];
+                    const float ms = top[j][e] == -INFINITY ? 0.0f : top[j][e] - lift;
 #pragma unroll
                     for (int u = 0; u < kSub; ++u) {
                         w[u][j][e] = exp2f(sc[u][j][e] - ms);
@@ -629,7 +647,7 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                     }
                 }
             float co[NT][2];
-            if (raise(mx, co)) {
+            if (raise(mx, co, kGrow)) {
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
                     den[j][0] *= co[j][0];
@@ -637,7 +655,7 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                 }
                 if (!kE4m3) rescale(co);
             }
-            weigh(mx);
+            weigh(mx, 0.0f);
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
 #pragma unroll
@@ -718,8 +736,8 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                         }
                 }
                 float co[NT][2];
-                if (raise(mw, co)) rescale(co);
-                weigh(mw);
+                if (raise(mw, co, kGrow16)) rescale(co);
+                weigh(mw, kLift);
             }
 #pragma unroll
             for (int u = 0; u < kSub; ++u) {
@@ -739,6 +757,10 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                         const float2 f01 = kE4m3 ? h2_f(h01) : bf2_f(h01);
                         const float2 f23 = kE4m3 ? h2_f(h23) : bf2_f(h23);
                         x[0] -= f01.x; x[1] -= f01.y; x[2] -= f23.x; x[3] -= f23.y;
+                        if (kE4m3) {   // (a part of what is left would run into fp16's last steps)
+                            x[0] *= kPartStep; x[1] *= kPartStep;
+                            x[2] *= kPartStep; x[3] *= kPartStep;
+                        }
                     }
                 // O^T += V^T P^T. MMA i covers elements 16 i + g and 16 i + g + 8 of a row (bf16),
                 // or 16 pg + 2 i and 16 pg + 2 i + 1 (8-bit)
@@ -800,7 +822,7 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                 if (g == 0) {
                     p[D] = mx[j][e];
                     p[D + 1] = den[j][e];
-                    p[D + 2] = kE4m3 ? mw[j][e] : mx[j][e];
+                    p[D + 2] = kE4m3 ? mw[j][e] - kLift : mx[j][e];   // (as the weights were put)
                 }
             }
             if (!meet()) return;

@@ -639,6 +639,100 @@ def test_a_wait_that_runs_out_reaches_the_caller(fmt, n):
     c.check(out, lse, True)
 
 
+def _far_below(fmt, page, n, sinks, tail0, tail1, rng):
+    """K and V pages [n / page, 1, page, D] in fmt and as values: tokens `sinks` score 0 for the
+    queries of the tests below and have V = 0 in the first half of the elements and -1 in the
+    others; the rest have K = (tail0, tail1[t]) in the first two elements, V in [1, 2)."""
+    k = rng.integers(-8, 8, (n, D)).astype(np.float32) / 8         # (q is 0 there)
+    k[:, 0], k[:, 1] = tail0, tail1
+    v = 1 + rng.integers(0, 8, (n, D)).astype(np.float32) / 8
+    k[sinks, :2] = 0
+    v[sinks, :D // 2], v[sinks, D // 2:] = 0, -1
+    kind = torch.bfloat16 if fmt == "bf16" else torch.float8_e4m3fn
+    kd, vd = (_dev(x.reshape(-1, 1, page, D)).to(kind) for x in (k, v))
+    assert torch.equal(kd.float().cpu().view(-1, D), torch.tensor(k))       # exact in both
+    one = torch.full(kd.shape[:3], 127, dtype=torch.uint8, device=DEV)
+    return pk.Pages(kd, vd, *((one, one.clone()) if fmt == "e4m3" else ())), k, v
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 2, 4, 40])
+@pytest.mark.parametrize("n", [64, 320])
+def test_weights_far_below_the_largest_keep_their_bits(fmt, out_dtype, rows, n):
+    """A few tokens at score 0 that have V = 0 in half of the elements, and tokens of one score
+    each row, down to 2^-30 of them: what is left in those elements is the small weights' alone.
+    Scores are exact but for the factor scale * log2(e), so the bounds can be the weights': 24 bits
+    (fp32) or 8 bits (bf16, down to 2^-24).
+    In units of 2^-24 relative to sum p|v|: scores 3 roundings times their size times ln 2, and one
+    of at most 16 where the weight's exponent is put together; two exponentials 4 each; the tensor
+    cores' sums truncate, three parts every 16 tokens, for 256 tokens in a row at most (2 each);
+    sums of 64 weights, warps and parts: n / 64 + 16, of weights and of O; the division and the
+    output 2; the weight itself 1."""
+    rng = np.random.default_rng(n + rows)
+    pages, k, v = _far_below(fmt, 64, n, [0, 16, 32, 48], -1, -1, rng)
+    f32 = out_dtype == torch.float32
+    q = np.zeros((rows, 4, D), np.float32)
+    q[..., 0] = rng.integers(0, 30 if f32 else 24, (rows, 4))
+    q[0, 0, 0] = 0
+    q[0, 1:, 0] = [8, 16, 29 if f32 else 23]
+    q[..., 1] = rng.integers(0, 64, (rows, 4)) / 64
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    chunk = pk.Chunk(ints([list(range(n // 64))]), ints([n]), ints([0, rows]), rows, rows)
+    cfg = pk.config(batch=1, num_kv_heads=1, group=4, dtype="bf16")
+    scale = float(np.float32(np.log(2)))
+    out, lse = pk.paged_attend(cfg, pages, chunk, _bf(q), scale, causal=False, want_lse=True,
+                               out_dtype=out_dtype)
+    x = np.float64(q) @ np.float64(k).T * scale
+    p = np.exp(x)
+    z = p.sum(-1, keepdims=True)
+    want, weight = p / z @ v, p / z @ np.abs(v)
+    size = np.abs(x).max(-1)[..., None]                      # (ln 2 is in it)
+    rel = (3 * size + 16 * np.log(2) + 8 + 6 * min(n, 256) / 16 + 2 * (n / 64 + 16) + 3) * 2.0 ** -24
+    tol = weight * rel if f32 else weight * (rel + 2.0 ** -8) + 2.0 ** -8 * np.abs(want)
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert (err <= tol).all(), (err / tol).max()
+    assert (np.abs(lse.double().cpu().numpy() - np.log(z[..., 0])) <= rel[..., 0]).all()
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 4])
+def test_a_long_tail_far_below_the_largest_counts(out_dtype, rows):
+    """131072 8-bit tokens, all but a few at the start with weights of 2^-26 to 2^-25.2 of theirs,
+    in so many sequences that a CTA takes one from its start on: together the tail is 2^-11 of the
+    output and more, and all of it where V of the few is 0.
+    Bound in fp32: roundings of 2^-24, 2 blocks of 128 tokens a block and lane in the sums of the
+    weights and 2 in those of O, 64 more for warps, parts and the rest; scores 3 times their size
+    (they matter to the tail alone). In bf16: the output's rounding, and each weight's 2^-8."""
+    rng = np.random.default_rng(rows)
+    page, n, batch, heads = 64, 131072, 40, 8
+    few = 4 * page
+    pages, k, v = _far_below("e4m3", page, few, [0, 16, 32, 48], -26,
+                             rng.integers(0, 8, few) / 8, rng)
+    kd, vd, ks, vs = (x.expand(-1, heads, *x.shape[2:]).contiguous() for x in pages.tensors)
+    pages = pk.Pages(kd, vd, ks, vs)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    table = [0] + [1 + i % 3 for i in range(n // page - 1)]  # the page of the few, then the others
+    often = np.repeat(np.bincount(table), page).astype(np.float64)
+    q = np.zeros((rows * batch, 4 * heads, D), np.float32)
+    q[..., 0], q[..., 1] = 1, rng.choice([0.5, 0.75, 0.875], q.shape[:2])
+    chunk = pk.Chunk(ints([table] * batch), ints([n] * batch),
+                     ints([rows * i for i in range(batch + 1)]), rows * batch, rows)
+    cfg = pk.config(batch=batch, num_kv_heads=heads, group=4, dtype="bf16")
+    scale = float(np.float32(np.log(2)))
+    out, _ = pk.paged_attend(cfg, pages, chunk, _bf(q), scale, causal=False, out_dtype=out_dtype)
+    x = np.float64(q) @ np.float64(k).T * scale
+    p = np.exp(x) * often
+    z = p.sum(-1, keepdims=True)
+    want, weight, tail = p / z @ v, p / z @ np.abs(v), p / z @ np.where(k[:, :1] == 0, 0, np.abs(v))
+    assert (tail > 2.0 ** -11).all()
+    tol = weight * (4 * (n / 128) + 64) * 2.0 ** -24 + 2 * tail * 3 * 26 * 2.0 ** -24
+    if out_dtype == torch.bfloat16:
+        tol += 2.0 ** -8 * (tail + np.abs(want))
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert (err <= tol).all(), (err / tol).max()
+
+
 # ------------------------------------------------------------------------------- together
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 def test_prompt_in_chunks_to_the_retrieval_index_and_decode(fmt):
