@@ -723,12 +723,11 @@ pariskv_status pariskv_paged_attend(const pariskv_config* cfg, const pariskv_pag
 }
 
 pariskv_status pariskv_paged_sync(void* stream) {
-    int status = ST_OK;
-    int other = ST_OK;
-    cudaError_t e = take_chunk_status(&status, static_cast<cudaStream_t>(stream));
-    if (e == cudaSuccess) e = take_few_status(&other, static_cast<cudaStream_t>(stream));
+    bool few = false, chunk = false;
+    cudaError_t e = take_chunk_waits_out(&chunk, static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) e = take_few_waits_out(&few, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "paged attention");
-    if (status == ST_TIMEOUT || other == ST_TIMEOUT)
+    if (few || chunk)
         return fail(PARISKV_ETIMEOUT, "a bounded device-side wait of the paged attention expired");
     return PARISKV_OK;
 }

@@ -212,12 +212,12 @@ int few_ctas(int sms);
 bool few_plans_inline(int batch);
 cudaError_t launch_attend_few(const AttendArgs& a, int format, bool f32_out, int ctas,
                               cudaStream_t st);
-cudaError_t take_few_status(int* status, cudaStream_t st);     // read and clear
+cudaError_t take_few_waits_out(bool* out, cudaStream_t st);     // since the last time
 // paged_chunk.cu: many rows a sequence (tcgen05); one CTA an SM
 constexpr int kChunkBlock = 128;
 int chunk_tile_rows(int group, bool f32_out);
 cudaError_t launch_attend_chunk(const AttendArgs& a, int format, bool f32_out, int ctas,
                                 cudaStream_t st);
-cudaError_t take_chunk_status(int* status, cudaStream_t st);   // read and clear
+cudaError_t take_chunk_waits_out(bool* out, cudaStream_t st);   // since the last time
 
 }  // namespace pkv

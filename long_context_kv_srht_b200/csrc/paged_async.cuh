@@ -12,7 +12,7 @@ namespace {
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint32_t kNapNs = 20000;
 
-__device__ int g_wait_status;   // ST_TIMEOUT after a wait ran out (one word a source file)
+__device__ unsigned long long g_waits_out;   // waits that ran out (one count a source file)
 
 __device__ __forceinline__ uint64_t now_ns() {
     uint64_t t;
@@ -35,7 +35,7 @@ __device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, volatile i
         if (t0 == 0) t0 = t;
         if (t - t0 > limit) {
             *abort = 1;
-            atomicExch(&g_wait_status, ST_TIMEOUT);
+            atomicAdd(&g_waits_out, 1ull);
             return false;
         }
     }
@@ -58,7 +58,7 @@ __device__ __noinline__ bool nap_more(uint32_t bar, uint32_t parity, volatile in
         if (t0 == 0) t0 = t;
         if (t - t0 > kWaitLimitNs) {
             *abort = 1;
-            atomicExch(&g_wait_status, ST_TIMEOUT);
+            atomicAdd(&g_waits_out, 1ull);
             return false;
         }
     }
@@ -79,15 +79,23 @@ __device__ __forceinline__ bool warp_nap(uint64_t* bar, uint32_t parity, volatil
 }
 __device__ __forceinline__ void arrive(uint64_t* bar) { mbar_arrive(smem_addr(bar)); }
 
-// The status word, read and cleared after `st`'s work is done.
-inline cudaError_t take_wait_status(int* status, cudaStream_t st) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(status, g_wait_status, sizeof(int), 0,
-                                              cudaMemcpyDeviceToHost, st);
+// Whether a wait on the current device has run out since this was last asked, after `st`'s work is
+// done. The device only counts up and the host remembers how far it has reported, so a wait that
+// runs out on another stream meanwhile is never lost, and of two threads one gets the report.
+inline cudaError_t take_waits_out(bool* out, cudaStream_t st) {
+    static std::atomic<unsigned long long> reported[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    unsigned long long now = 0;
+    e = cudaMemcpyFromSymbolAsync(&now, g_waits_out, sizeof(now), 0, cudaMemcpyDeviceToHost, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e != cudaSuccess || *status == ST_OK) return e;
-    const int ok = ST_OK;
-    e = cudaMemcpyToSymbolAsync(g_wait_status, &ok, sizeof(int), 0, cudaMemcpyHostToDevice, st);
-    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
+    if (e != cudaSuccess) return e;
+    unsigned long long before = reported[dev].load();
+    while (before < now && !reported[dev].compare_exchange_weak(before, now)) {}
+    *out = before < now;
+    return cudaSuccess;
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,

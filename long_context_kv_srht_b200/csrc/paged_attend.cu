@@ -962,6 +962,6 @@ cudaError_t launch_attend_few(const AttendArgs& a, int format, bool f32_out, int
                : launch_few_out<false, 2>(a, maps, f32_out, ctas, in, st);
 }
 
-cudaError_t take_few_status(int* status, cudaStream_t st) { return take_wait_status(status, st); }
+cudaError_t take_few_waits_out(bool* out, cudaStream_t st) { return take_waits_out(out, st); }
 
 }  // namespace pkv

@@ -1006,6 +1006,6 @@ cudaError_t launch_attend_chunk(const AttendArgs& a, int format, bool f32_out, i
                    : launch_chunk<false, 1, __nv_bfloat16>(a, maps, ctas, st);
 }
 
-cudaError_t take_chunk_status(int* status, cudaStream_t st) { return take_wait_status(status, st); }
+cudaError_t take_chunk_waits_out(bool* out, cudaStream_t st) { return take_waits_out(out, st); }
 
 }  // namespace pkv

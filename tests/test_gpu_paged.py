@@ -3,6 +3,7 @@ scale bytes exactly, read-back exactly, attention within bounds counted from its
 import os
 import subprocess
 import sys
+import threading
 
 import numpy as np
 import pytest
@@ -731,6 +732,35 @@ def test_a_long_tail_far_below_the_largest_counts(out_dtype, rows):
         tol += 2.0 ** -8 * (tail + np.abs(want))
     err = np.abs(out.double().cpu().numpy() - want)
     assert (err <= tol).all(), (err / tol).max()
+
+
+@pytest.mark.parametrize("n", [1, 200])
+def test_of_two_threads_one_gets_the_report(n):
+    """Two threads ask at once, on streams of their own, about one wait that ran out: it is reported
+    once, and the next one again."""
+    c = Case(8, "bf16", [n], [300], heads=2, group=4, page=16)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    pk.paged_sync()
+    for _ in range(20):
+        pk.inject_paged_timeout()
+        _attend(c)
+        torch.cuda.synchronize()
+        gate, told = threading.Barrier(2), [None, None]
+
+        def ask(i):
+            torch.cuda.set_device(0)
+            gate.wait()
+            told[i] = pk.lib.pariskv_paged_sync(streams[i].cuda_stream)
+
+        threads = [threading.Thread(target=ask, args=(i,)) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert sorted(told) == [pk.OK, pk.ETIMEOUT]
+    out, lse = _attend(c)
+    pk.paged_sync()
+    c.check(out, lse, True)
 
 
 # ------------------------------------------------------------------------------- together
