@@ -338,6 +338,57 @@ def test_rows_past_max_q_are_left_and_malformed_starts_stay_inside():
     torch.cuda.synchronize()
 
 
+def _inside(t, margin):
+    """A contiguous copy of t in the middle of a larger tensor of the same bytes' pattern 0xa5, and
+    that larger tensor's bytes before and behind."""
+    n = t.numel() * t.element_size()
+    buf = torch.full((n + 2 * margin,), 0xa5, dtype=torch.uint8, device=DEV)
+    x = buf[margin:margin + n].view(t.dtype).view(t.shape)
+    x.copy_(t)
+    return x, (buf[:margin], buf[margin + n:])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("max_q", [2, 45])
+@pytest.mark.parametrize("starts", [[0, 45, 20], [40, 0, 45], [-5, 10, 1000], [30, 1 << 30, (1 << 31) - 1],
+                                    [-(1 << 31), (1 << 31) - 1, 0], [45, 45, 45], [3, 9, 4]])
+def test_malformed_starts_touch_nothing_else(fmt, max_q, starts):
+    """Outputs and pools lie inside larger buffers of a pattern: what no start covers, and all around,
+    keeps it. A sequence covers rows [a, a + min(b - a, max_q, total - a)) (none if a < 0), at
+    positions from kv_len - (b - a) on."""
+    c = Case(6, fmt, [40, 2], [90, 2], heads=2, group=4, page=16)
+    chunk = pk.Chunk(_dev(c.table), _dev(c.kv), _dev(np.array(starts, np.int32)), c.total, max_q)
+    rows, slots = np.zeros(c.total, bool), np.zeros((c.pages, 16), bool)
+    cache = ref.Cache(c.k, c.v, c.table, c.kv, c.q_start)
+    for s in range(2):
+        a, b = starts[s], starts[s + 1]
+        n = 0 if a < 0 else max(0, min(b - a, max_q, c.total - a))
+        rows[a:a + n] = True
+        for j in range(n):
+            pos = int(c.kv[s]) - max(0, b - a) + j
+            if pos < c.kv[s] and cache.slot(s, pos) is not None:
+                slots[cache.slot(s, pos)] = True
+    free, margin = _dev(~rows), 1 << 16
+    untouched = lambda around: all((x == 0xa5).all() for x in around)
+    for out_dtype in (torch.bfloat16, torch.float32):
+        out, around = _inside(torch.full((c.total, 8, D), -7.0, dtype=out_dtype, device=DEV), margin)
+        lse, beside = _inside(torch.full((c.total, 8), -7.0, device=DEV), margin)
+        pk.paged_attend(c.cfg, c.pool(), chunk, _bf(c.q), SCALE, out=out, lse=lse)
+        assert untouched(around) and untouched(beside)
+        assert (out[free] == -7).all() and (lse[free] == -7).all()
+        assert (lse[~free] != -7).all()                  # and the rows covered are written
+    pool, sides = zip(*(_inside(t, margin) for t in _fresh(c).tensors if t is not None))
+    before = [t.clone() for t in pool]
+    new = torch.ones((c.total, 2, D), dtype=torch.bfloat16, device=DEV)
+    pk.paged_write(c.cfg, pk.Pages(*pool), chunk, new, new)
+    free = _dev(~slots)
+    for t, old, around in zip(pool, before, sides):
+        assert untouched(around)
+        kept = (t.view(torch.uint8) == old.view(torch.uint8)).reshape(*t.shape[:3], -1).all(-1)
+        assert kept.transpose(1, 2)[free].all()
+    pk.paged_sync()
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 def test_same_bits_on_every_call_streams_and_graphs(fmt):
     """Twice in a row, on another stream, and from a captured graph that follows new lengths."""
