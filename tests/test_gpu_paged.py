@@ -338,6 +338,36 @@ def test_rows_past_max_q_are_left_and_malformed_starts_stay_inside():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("q", [[1, 2], [4, 1], [60, 1]])
+@pytest.mark.parametrize("scale", [3.0, SCALE, 0.0, -0.5])
+def test_saturated_zero_and_negative_scores(fmt, out_dtype, q, scale):
+    """Scores up to hundreds apart and none apart, by every kernel and in every type."""
+    c = Case(4, fmt, q, [200, 65], heads=2, group=4, page=32, amp=8.0)
+    out, lse = _attend(c, out_dtype=out_dtype, scale=scale)
+    c.check(out, lse, True, scale)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rows", [1, 2, 4, 40])
+def test_fp32_output_of_small_scores_and_few_tokens(fmt, rows):
+    """Scores near zero, 60 tokens, V of every size and sign: what is left to be off is the weights'
+    bits and the sums. In units of 2^-24 of sum p|v|: 48 for truncated sums (4 products of 16 tokens
+    and three parts, 2 each: 24; and their alignment as much again), 2 * 20 for sums of 64 weights,
+    warps and parts, 8 for exponentials, 4 for the division and the output, and scores off by 136 *
+    2^-23 of their reach (below 2^-7), above and below the bar. In all less than half a step of
+    weights of 16 bits (2^-17)."""
+    c = Case(17, fmt, [rows], [60], heads=2, group=4, page=16)
+    c.q = c.q * np.float32(2.0 ** -12)
+    out, _ = _attend(c, False, torch.float32)
+    o, _, w, reach = c.reference(False)
+    assert reach.max() < 2.0 ** -7
+    err = np.abs(out.double().cpu().numpy() - o)[:rows]
+    tol = (w * (48 + 40 + 8 + 4 + 4 * 136 * reach[..., None]) * 2.0 ** -24)[:rows]
+    assert (err <= tol).all(), (err / tol).max()
+
+
 def _inside(t, margin):
     """A contiguous copy of t in the middle of a larger tensor of the same bytes' pattern 0xa5, and
     that larger tensor's bytes before and behind."""
