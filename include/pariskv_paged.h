@@ -109,8 +109,8 @@ PARISKV_API pariskv_status pariskv_paged_read(const pariskv_config* cfg,
  *          bits; PARISKV_F32: with 24 bits, so that the result is as exact as fp32 sums are (the
  *          tensor cores truncate theirs, which is bounded to some 2^-20 of sum_t p_t |V_t|, however
  *          many tokens there are). Over E4M3 pages with max_q * group <= 16 this holds for weights
- *          p_t * 2^(V's scale) down to 2^-30 (BF16) or 2^-36 (F32) of the row's largest; smaller ones
- *          are off by at most 2^-38 or 2^-60 of it.
+ *          p_t * 2^(V's scale) down to 2^-24 (BF16) or 2^-30 (F32) of the row's largest; smaller ones
+ *          are off by at most 2^-32 or 2^-54 of it.
  *   lse:   device pointer [total_q][num_kv_heads * group] fp32, or NULL.
  * Sums, maxima and accumulators are fp32; the accumulators are relative to maxima that may lag by
  * a factor of 2^8, so sums of V's magnitudes over the attended tokens past 2^119 can overflow to

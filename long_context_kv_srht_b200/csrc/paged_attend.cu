@@ -25,7 +25,7 @@
 //  - the 8-bit rows' scales are powers of two: K's multiply the scores, V's go into the exponents
 //    of the weights, which are then relative to maxima of their own (so that they fit fp16);
 //  - P enters the second product in parts: two of bf16 (16 bits; 8-bit pages: one of fp16, 11
-//    bits, 8 at 2^-30 of the largest), three (24 bits and more) for fp32 output;
+//    bits, 8 at 2^-24 of the largest), three (24 bits and more) for fp32 output;
 //  - a row's maximum is only brought up to date (three shuffles, O rescaled) when a score exceeds
 //    it by more than 2^8; sums stay per lane until the end of a range, where the warps merge.
 //
@@ -51,15 +51,16 @@ constexpr int kFW = 4;                        // warps, 16 of every 64 tokens ea
 constexpr int kInline = 256;
 constexpr int kSegs = 8;                      // segment records between the loads and the others
 constexpr float kGrow = 8.0f;                 // growth of a maximum (base 2) that rescales O
-// 8-bit pages: the growth for the maxima of the fp16 weights, and the exponent that the weight of such
-// a maximum gets (together 15: the largest number of fp16 is just below 2^16). fp16's steps end at
-// 2^-24, so one part of a weight is off by 2^-12 of it or 2^-38 of the largest, whichever is more: 8
-// bits down to 2^-30. What one part leaves is taken kPartStep times for the next, so three have 24
-// bits and more down to 2^-36, and are off by 2^-60 of the largest below. (Were the largest 1 and the
-// parts as they are, weights would be cut at 2^-25 of it, in three parts as in one, while their sum
-// has them in full: a tail of 131072 tokens at 2^-26 would be missing. Rescaling at a growth of 2^2
-// costs no more than at 2^8: single tokens over 131072 70.2 us with either.)
-constexpr float kGrow16 = 2.0f, kLift = 13.0f;
+// 8-bit pages: the exponent that the fp16 weight of a maximum gets (with kGrow 15: fp16 ends just
+// below 2^16). Its steps end at 2^-24, so one part of a weight is off by 2^-12 of it or by 2^-32 of the
+// largest, whichever is more: 8 bits down to 2^-24, and all weights that can be lost are less than
+// 2^-12 of the largest together (180 GB of rows are 2^20 tokens a warp at most). What one part
+// leaves is taken kPartStep times for the next, so three have 24 bits and more down to 2^-30, and
+// are off by 2^-54 of the largest below. (Were the largest 1 and the parts as they are, weights would
+// be cut at 2^-25 of it, in three parts as in one, while their sum has them in full: a tail of 131072
+// tokens at 2^-26 would be missing. 2^13, with rescaling at a growth of 2^2, takes 62.4 us for 4
+// tokens over 65536, 2^7 60.8, as without any.)
+constexpr float kLift = 7.0f;
 constexpr float kPartStep = 2048.0f;
 
 template <bool kE4m3> struct FewShape {
@@ -135,8 +136,8 @@ __device__ __forceinline__ void mma16(float d[4], const uint32_t a[4], uint32_t 
 // o[j][i] += f * (the parts of 16 tokens' weights) for every group j of 8 rows. The tensor cores
 // truncate their sums, which over a long range would shrink o by half a step a product; three
 // parts are wanted for more than that leaves, so their sum begins anew every time and is added with
-// rounding. (16 sequences of 4 tokens, 16 rows, over 16384 8-bit tokens: 269 us with the parts' sums
-// apart, 316 with one after the other; single tokens over 32768 240 and 242.)
+// rounding. (16 sequences of 4 tokens, 16 rows, over 16384 8-bit tokens: 259 us with the parts' sums
+// apart, some 300 with one after the other; single tokens over 32768 242 with either.)
 template <bool kF16, int NT, int kParts>
 __device__ __forceinline__ void accumulate(float (&o)[NT][8][4], int i, const uint32_t f[4],
                                            const uint32_t (&p)[NT][kParts][2]) {
@@ -580,7 +581,7 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
         // softmax: weights with the maxima as they are, unless a score is far above
         float w[kSub][NT][4];
         // brings maxima up to date with the scores where one is far above; factors for the old
-        auto raise = [&](float (&top)[NT][2], float (&co)[NT][2], float grow) -> bool {
+        auto raise = [&](float (&top)[NT][2], float (&co)[NT][2]) -> bool {
             bool grown = false;
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
@@ -588,7 +589,7 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        grown = grown || fmaxf(sc[u][j][e], sc[u][j][2 + e]) > top[j][e] + grow;
+                        grown = grown || fmaxf(sc[u][j][e], sc[u][j][2 + e]) > top[j][e] + kGrow;
             if (!__any_sync(0xffffffffu, grown)) return false;
 #pragma unroll
             for (int j = 0; j < NT; ++j)
@@ -647,7 +648,7 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                     }
                 }
             float co[NT][2];
-            if (raise(mx, co, kGrow)) {
+            if (raise(mx, co)) {
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
                     den[j][0] *= co[j][0];
@@ -736,7 +737,7 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                         }
                 }
                 float co[NT][2];
-                if (raise(mw, co, kGrow16)) rescale(co);
+                if (raise(mw, co)) rescale(co);
                 weigh(mw, kLift);
             }
 #pragma unroll
