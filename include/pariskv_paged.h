@@ -68,7 +68,9 @@ typedef struct {
     int64_t total_q;            /* rows of the per-token arrays; 0 .. 2^31 - 1 */
     int32_t table_width;        /* entries of each sequence's table, >= 1 */
     int32_t table_stride;       /* >= table_width */
-    int32_t max_q;              /* at least every q_len: a sequence's rows past max_q are left out */
+    int32_t max_q;              /* at least every q_len: a sequence's rows past max_q are left out.
+                                 * It also chooses the attention's kernel, for the whole call (see
+                                 * pariskv_paged_attend), so it should not be larger than need be. */
 } pariskv_chunk;
 
 /* Writes the new tokens' K and V rows into their pages.
@@ -115,9 +117,15 @@ PARISKV_API pariskv_status pariskv_paged_read(const pariskv_config* cfg,
  * Sums, maxima and accumulators are fp32; the accumulators are relative to maxima that may lag by
  * a factor of 2^8, so sums of V's magnitudes over the attended tokens past 2^119 can overflow to
  * infinity. A K or V row with an infinity or a NaN in it makes the
- * rows that attend it infinite or NaN (V: in the elements concerned) and no others. The same
- * call on the same data gives the same bits. The workspace comes from the library's per-device
- * memory pool, stream-ordered on `stream`. Two or three launches.
+ * rows that attend it infinite or NaN (V: in the elements concerned) and no others; but a token
+ * whose score is minus infinity weighs nothing. The same call on the same data gives the same bits.
+ * Calls with max_q * group <= 16 stream K and V once for up to 16 rows a sequence and KV head; with
+ * more rows, every sequence of the call goes by tiles of 128 or 256 rows. Each rounds its weights
+ * differently, so a sequence's last bits can depend on what else is in the call, and one long chunk
+ * among single tokens (or a max_q that is not reached) makes those slower: 32 of them over 32768
+ * tokens 1.3 times over BF16 pages and 2.8 times over E4M3 ones. Two calls avoid that.
+ * The workspace comes from the library's per-device memory pool, stream-ordered on `stream`. Two or
+ * three launches.
  * Errors: EINVAL, ENOMEM, ECUDA; ETIMEOUT from pariskv_paged_sync. */
 PARISKV_API pariskv_status pariskv_paged_attend(const pariskv_config* cfg,
                                                 const pariskv_pages* pages,
@@ -128,7 +136,8 @@ PARISKV_API pariskv_status pariskv_paged_attend(const pariskv_config* cfg,
 
 /* Waits for the work on `stream` and reports whether a device-side wait of a paged attention on
  * the current device has run out since the last report (PARISKV_ETIMEOUT: the outputs of that
- * call are not complete; never seen while the device works). Not to be captured. */
+ * call are not complete; never seen while the device works). The report is the device's, not the
+ * stream's: of several threads that ask at once, one gets it. Not to be captured. */
 PARISKV_API pariskv_status pariskv_paged_sync(void* stream);
 
 #ifdef __cplusplus

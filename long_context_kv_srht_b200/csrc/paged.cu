@@ -28,13 +28,14 @@ __device__ __forceinline__ uint4 pack8(const float v[8]) {
 
 // ------------------------------------------------------------------------------------ write
 // A warp takes one new token, a head at a time: 16 lanes its K row and 16 its V row, 8 elements a
-// lane. The first rows are under way while the warp finds out where they go (a chain of dependent loads: starts, lengths, the page's id). Bound by HBM: it
-// reads each row once and writes 256 or 129 bytes of it; neighbouring tokens are in neighbouring
-// warps of a CTA, so the 128-byte pieces of a head's rows meet in L2. 131072 tokens of 8 heads from
-// bf16 to 8 bits: 142 us, 5.7 TB/s, two thirds of it reads (158 us when a lane's rows were K's of
-// one head and then another's: twice the instructions; 170 us with 32 lanes a row, whose maximum
-// is one instruction, but whose stores are half as wide). 16 tokens: 7.6 us, the launch and the
-// chain of four dependent loads.
+// lane. The first rows are under way while the warp finds out where they go (a chain of dependent
+// loads: starts, lengths, the page's id). Bound by HBM: it reads each row once and writes 256 or 129
+// bytes of it; neighbouring tokens are in neighbouring warps of a CTA, so the 128-byte pieces of a
+// head's rows meet in L2. 131072 tokens of 8 heads from bf16 to 8 bits: 142 us, 5.7 TB/s, two thirds
+// of it reads (158 us when a lane's rows were K's of one head and then another's: twice the
+// instructions; 170 us with 32 lanes a row, whose maximum is one instruction, but whose stores are
+// half as wide). 16 tokens: 8 us, which is the host's part of a call; 3.3 us each in a captured graph,
+// the launch and the chain of four dependent loads.
 constexpr int kWriteWarps = 8;
 
 // four values to e4m3, nearest even, saturating

@@ -29,13 +29,15 @@
 //  - a row's maximum is only brought up to date (three shuffles, O rescaled) when a score exceeds
 //    it by more than 2^8; sums stay per lane until the end of a range, where the warps merge.
 //
-// Measured (8 KV heads, groups of 4, whole calls): 16 sequences of 65536 bf16 tokens 600 us, 7.2
-// TB/s, HBM's bound; 16 of 32768 8-bit tokens 187 us, 5.8 TB/s; one of 131072 59 us, 4.6 TB/s, and
-// one of 4096 bf16 tokens 17 us, both with the chain of launch, lengths, page ids, first tiles and
-// join in them. (Three CTAs an SM with 64-token blocks: 61 us for the one of 131072.) Why tiles of 8 and of 16 rows: 2 tokens over
-// 65536 (8 rows) take 53.2 us in tiles of 8 and 55.0 in tiles of 16 in bf16, 39.6 and 57.0 in 8
-// bits. Why not the chunk kernel's tiles up to 16 rows: 4 tokens over 65536 take 59.2 us here and
-// 66.2 there in bf16, 61.4 and 85.2 in 8 bits; 8 sequences of 32768 170 and 204, 170 and 263.
+// Measured (8 KV heads, groups of 4, whole calls): 16 sequences of 65536 bf16 tokens 602 us, 7.1
+// TB/s, HBM's bound; 16 of 32768 8-bit tokens 206 us, 5.2 TB/s; one of 131072 58 us, 4.6 TB/s, with
+// the chain of launch, lengths, page ids, first tiles and join in it, and one of 4096 bf16 tokens 17.5
+// us, the host's part of a call (12.2 in a captured graph: that chain). To fp32: 4 tokens over 65536
+// 81.8 us in 8 bits and 67.5 in bf16, 16 of 32768 8-bit tokens 242 us. (Three CTAs an SM with
+// 64-token blocks: 61 us for the one of 131072.) Why tiles of 8 and of 16 rows: 2 tokens over 65536
+// (8 rows) take 53.2 us in tiles of 8 and 55.0 in tiles of 16 in bf16, 39.6 and 57.0 in 8 bits. Why
+// not the chunk kernel's tiles up to 16 rows: 4 tokens over 65536 take 59.2 us here and 66.2 there in
+// bf16, 61.4 and 85.2 in 8 bits; 8 sequences of 32768 170 and 204, 170 and 263.
 #include <cuda_fp16.h>
 
 #include "paged_async.cuh"

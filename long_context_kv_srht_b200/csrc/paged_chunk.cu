@@ -14,6 +14,10 @@
 //    two turns of 64 tokens, and the scores of the next turn are there before this one's are done;
 //  - O is rescaled only when a row's maximum has grown by more than 2^8 since the last time (P is
 //    then at most 2^8, which costs bf16 nothing), so tensor memory is not read back each block;
+//  - to bf16, P is rounded to bf16: off by half a step each, which the sum averages, so that outputs
+//    are off by 2.1e-3 (relative, all elements) where the output's own rounding makes 1.7e-3. A second
+//    part would take half as many products again, and they are what bounds the kernel; fp32 output
+//    (below) is there for whoever wants more;
 //  - K, V and Q tiles come by TMA through a ring of 32 KB stages, one copy a page and 64 columns;
 //    with 8-bit pages they come as bytes, and seven or eight warps widen them into the ring, scale
 //    and all (a power of two: the bf16 values are exact);
