@@ -23,17 +23,17 @@
 //    lane reads 16 consecutive codes and uses them for four MMAs. Q becomes fp16 too, each row
 //    times a power of two;
 //  - the 8-bit rows' scales are powers of two: K's multiply the scores, V's go into the exponents
-//    of the weights, which are then relative to maxima of their own (so that they fit fp16);
+//    of the weights, which a whole number a row (ex) brings to where they fit fp16;
 //  - P enters the second product in parts: two of bf16 (16 bits; 8-bit pages: one of fp16, 11
 //    bits, 8 at 2^-24 of the largest), three (24 bits and more) for fp32 output;
 //  - a row's maximum is only brought up to date (three shuffles, O rescaled) when a score exceeds
 //    it by more than 2^8; sums stay per lane until the end of a range, where the warps merge.
 //
 // Measured (8 KV heads, groups of 4, whole calls): 16 sequences of 65536 bf16 tokens 602 us, 7.1
-// TB/s, HBM's bound; 16 of 32768 8-bit tokens 206 us, 5.2 TB/s; one of 131072 58 us, 4.6 TB/s, with
+// TB/s, HBM's bound; 16 of 32768 8-bit tokens 204 us, 5.3 TB/s; one of 131072 58 us, 4.6 TB/s, with
 // the chain of launch, lengths, page ids, first tiles and join in it, and one of 4096 bf16 tokens 17.5
 // us, the host's part of a call (12.2 in a captured graph: that chain). To fp32: 4 tokens over 65536
-// 81.8 us in 8 bits and 67.5 in bf16, 16 of 32768 8-bit tokens 242 us. (Three CTAs an SM with
+// 77.7 us in 8 bits and 67.8 in bf16, 16 of 32768 8-bit tokens 242 us. (Three CTAs an SM with
 // 64-token blocks: 61 us for the one of 131072.) Why tiles of 8 and of 16 rows: 2 tokens over 65536
 // (8 rows) take 53.2 us in tiles of 8 and 55.0 in tiles of 16 in bf16, 39.6 and 57.0 in 8 bits. Why
 // not the chunk kernel's tiles up to 16 rows: 4 tokens over 65536 take 59.2 us here and 66.2 there in
@@ -53,16 +53,19 @@ constexpr int kFW = 4;                        // warps, 16 of every 64 tokens ea
 constexpr int kInline = 256;
 constexpr int kSegs = 8;                      // segment records between the loads and the others
 constexpr float kGrow = 8.0f;                 // growth of a maximum (base 2) that rescales O
-// 8-bit pages: the exponent that the fp16 weight of a maximum gets (with kGrow 15: fp16 ends just
-// below 2^16). Its steps end at 2^-24, so one part of a weight is off by 2^-12 of it or by 2^-32 of the
-// largest, whichever is more: 8 bits down to 2^-24, and all weights that can be lost are less than
-// 2^-12 of the largest together (180 GB of rows are 2^20 tokens a warp at most). What one part
-// leaves is taken kPartStep times for the next, so three have 24 bits and more down to 2^-30, and
-// are off by 2^-54 of the largest below. (Were the largest 1 and the parts as they are, weights would
-// be cut at 2^-25 of it, in three parts as in one, while their sum has them in full: a tail of 131072
-// tokens at 2^-26 would be missing. 2^13, with rescaling at a growth of 2^2, takes 62.4 us for 4
-// tokens over 65536, 2^7 60.8, as without any.)
-constexpr float kLift = 7.0f;
+// 8-bit pages: the largest fp16 weight of a row is put between 2^(kLift - 1) and 2^kLift when O is
+// rescaled for it, and may grow to 2^kTop before that happens again (fp16 ends just below 2^16). fp16's
+// steps end at 2^-24, so one part of a weight is off by 2^-12 of it or by 2^-32 of the largest,
+// whichever is more: 8 bits down to 2^-24, and all weights that can be lost are less than 2^-12 of the
+// largest together (180 GB of rows are 2^20 tokens a warp at most). What one part leaves is taken
+// kPartStep times for the next, so three have 24 bits and more down to 2^-30, and are off by 2^-54 of
+// the largest below. (Were the largest 1 and the parts as they are, weights would be cut at 2^-25 of
+// it, in three parts as in one, while their sum has them in full: a tail of 131072 tokens at 2^-26
+// would be missing. 2^13, with rescaling at a growth of 2^2, takes 62.4 us for 4 tokens over 65536,
+// 2^7 60.8, as without any. With the maxima of those weights in fp32 beside mx, in place of whole
+// numbers, 4 tokens to fp32 took 81.6 us, now 77.7, and above 2^24 their steps broke the 2^15.)
+constexpr float kLift = 8.0f, kTop = 15.0f;
+constexpr float kNoExp = -512.0f;             // the exponent of an O that has nothing in it
 constexpr float kPartStep = 2048.0f;
 
 template <bool kE4m3> struct FewShape {
@@ -138,8 +141,8 @@ __device__ __forceinline__ void mma16(float d[4], const uint32_t a[4], uint32_t 
 // o[j][i] += f * (the parts of 16 tokens' weights) for every group j of 8 rows. The tensor cores
 // truncate their sums, which over a long range would shrink o by half a step a product; three
 // parts are wanted for more than that leaves, so their sum begins anew every time and is added with
-// rounding. (16 sequences of 4 tokens, 16 rows, over 16384 8-bit tokens: 259 us with the parts' sums
-// apart, some 300 with one after the other; single tokens over 32768 242 with either.)
+// rounding. (16 sequences of 4 tokens, 16 rows, over 16384 8-bit tokens: 241 us with the parts' sums
+// apart, which are some 40 more one after the other; single tokens over 32768 242 with either.)
 template <bool kF16, int NT, int kParts>
 __device__ __forceinline__ void accumulate(float (&o)[NT][8][4], int i, const uint32_t f[4],
                                            const uint32_t (&p)[NT][kParts][2]) {
@@ -443,7 +446,7 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
     int lim[NT][2], shared = 0;
     int down[NT][2];     // exponents that undo what the rows of Q were multiplied by (8-bit)
     float mx[NT][2], den[NT][2], o[NT][8][4];
-    float mw[NT][2];     // maxima of the weights that O is relative to (8-bit: mx and V's scales)
+    float ex[NT][2];     // O is relative to mx + ex (8-bit; whole numbers)
     // the last token a row may attend
     auto limit = [&](int r) -> int {
         if (r >= sg.nrow) return -1;
@@ -513,7 +516,8 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     lim[j][e] = limit(8 * j + 2 * t + e);
-                    mx[j][e] = mw[j][e] = -INFINITY;
+                    mx[j][e] = -INFINITY;
+                    ex[j][e] = kNoExp;
                     den[j][e] = 0.0f;
                 }
 #pragma unroll
@@ -582,33 +586,27 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
 
         // softmax: weights with the maxima as they are, unless a score is far above
         float w[kSub][NT][4];
-        // brings maxima up to date with the scores where one is far above; factors for the old
-        auto raise = [&](float (&top)[NT][2], float (&co)[NT][2]) -> bool {
-            bool grown = false;
+        using Block = float[kSub][NT][4];
+        // the largest of a row in the block
+        auto highest = [&](const Block& x, int j, int e) -> float {
+            float bm = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < kSub; ++u) bm = fmaxf(bm, fmaxf(x[u][j][e], x[u][j][2 + e]));
+#pragma unroll
+            for (int k = 4; k < 32; k <<= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, k));
+            return bm;
+        };
+        // whether the warp has anything above its row's bound
+        auto above = [&](const Block& x, auto bound) -> bool {
+            bool some = false;
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        grown = grown || fmaxf(sc[u][j][e], sc[u][j][2 + e]) > top[j][e] + kGrow;
-            if (!__any_sync(0xffffffffu, grown)) return false;
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float bm = -INFINITY;
-#pragma unroll
-                    for (int u = 0; u < kSub; ++u)
-                        bm = fmaxf(bm, fmaxf(sc[u][j][e], sc[u][j][2 + e]));
-#pragma unroll
-                    for (int k = 4; k < 32; k <<= 1)
-                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, k));
-                    const float m1 = fmaxf(top[j][e], bm);
-                    co[j][e] = exp2f(top[j][e] - (m1 == -INFINITY ? 0.0f : m1));
-                    top[j][e] = m1;
-                }
-            return true;
+                        some = some || fmaxf(x[u][j][e], x[u][j][2 + e]) > bound(j, e);
+            return __any_sync(0xffffffffu, some);
         };
         auto rescale = [&](const float (&co)[NT][2]) {
 #pragma unroll
@@ -617,19 +615,6 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                 for (int i = 0; i < 8; ++i) {
                     o[j][i][0] *= co[j][0]; o[j][i][1] *= co[j][1];
                     o[j][i][2] *= co[j][0]; o[j][i][3] *= co[j][1];
-                }
-        };
-        auto weigh = [&](const float (&top)[NT][2], float lift) {   // of a maximum: 2^lift
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float ms = top[j][e] == -INFINITY ? 0.0f : top[j][e] - lift;
-#pragma unroll
-                    for (int u = 0; u < kSub; ++u) {
-                        w[u][j][e] = exp2f(sc[u][j][e] - ms);
-                        w[u][j][2 + e] = exp2f(sc[u][j][2 + e] - ms);
-                    }
                 }
         };
         if (any) {
@@ -650,15 +635,38 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                     }
                 }
             float co[NT][2];
-            if (raise(mx, co)) {
+            if (above(sc, [&](int j, int e) { return mx[j][e] + kGrow; })) {
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    den[j][0] *= co[j][0];
-                    den[j][1] *= co[j][1];
-                }
-                if (!kE4m3) rescale(co);
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float m1 = fmaxf(mx[j][e], highest(sc, j, e));
+                        const float down = mx[j][e] - (m1 == -INFINITY ? 0.0f : m1);
+                        co[j][e] = exp2f(down);
+                        den[j][e] *= co[j][e];
+                        mx[j][e] = m1;
+                        if (kE4m3) {   // O keeps its place, but for less than a step up
+                            const float k = ceilf(-down);
+                            const bool far = !(k < 600.0f);
+                            co[j][e] = far ? 0.0f : exp2f(down + k);
+                            ex[j][e] = far ? kNoExp : ex[j][e] - k;
+                        }
+                    }
+                rescale(co);
             }
-            weigh(mx, 0.0f);
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float ms = mx[j][e] == -INFINITY ? 0.0f : mx[j][e];
+#pragma unroll
+                    for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                        for (int i = e; i < 4; i += 2) {
+                            sc[u][j][i] -= ms;
+                            w[u][j][i] = exp2f(sc[u][j][i]);
+                        }
+                }
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
 #pragma unroll
@@ -720,27 +728,55 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                 __syncwarp();
             }
             if (kE4m3) {
-                // the weights of O: with V's scales in the exponent, relative to maxima of their own
+                // the weights of O: with V's scales and the row's ex in the exponent, which are whole
+                // numbers, so that a weight has the bits that it has in den however large mx is
+                float ea[kSub][2];
 #pragma unroll
-                for (int u = 0; u < kSub; ++u) {
-                    const int r0 = 64 * u + 16 * warp + pg;
-                    float ea = static_cast<float>(vsc[r0] - 127);
-                    float eb = static_cast<float>(vsc[r0 + 8] - 127);
-                    if (repair) {   // (a cleared NaN row weighs nothing)
-                        if (tok[u] > shared && vsc[r0] == kNanRow) ea = -INFINITY;
-                        if (tok[u] + 8 > shared && vsc[r0 + 8] == kNanRow) eb = -INFINITY;
+                for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint8_t byte = vsc[64 * u + 16 * warp + pg + 8 * k];
+                        ea[u][k] = static_cast<float>(byte - 127);
+                        // (a cleared NaN row weighs nothing)
+                        if (repair && tok[u] + 8 * k > shared && byte == kNanRow) ea[u][k] = -INFINITY;
                     }
+                // (one part is far coarser than what in-place exponents lose when ex grows)
+                constexpr bool kAnew = kParts > 1;
+                Block& x = kAnew ? w : sc;
+                auto place = [&] {
+#pragma unroll
+                    for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                x[u][j][i] = sc[u][j][i] + (ea[u][i >> 1] - ex[j][i & 1]);
+                };
+                place();
+                if (above(x, [](int, int) { return kTop; })) {
+                    float co[NT][2];
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            sc[u][j][e] += ea;
-                            sc[u][j][2 + e] += eb;
+                            const float k = fmaxf(ceilf(highest(x, j, e)) - kLift, 0.0f);
+                            co[j][e] = exp2f(-k);
+                            ex[j][e] += k;
+#pragma unroll
+                            for (int u = 0; u < kSub && !kAnew; ++u) {
+                                x[u][j][e] -= k;
+                                x[u][j][2 + e] -= k;
+                            }
                         }
+                    rescale(co);
+                    if (kAnew) place();
                 }
-                float co[NT][2];
-                if (raise(mw, co)) rescale(co);
-                weigh(mw, kLift);
+#pragma unroll
+                for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w[u][j][i] = exp2f(x[u][j][i]);
             }
 #pragma unroll
             for (int u = 0; u < kSub; ++u) {
@@ -825,7 +861,7 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
                 if (g == 0) {
                     p[D] = mx[j][e];
                     p[D + 1] = den[j][e];
-                    p[D + 2] = kE4m3 ? mw[j][e] - kLift : mx[j][e];   // (as the weights were put)
+                    p[D + 2] = ex[j][e];
                 }
             }
             if (!meet()) return;
@@ -840,8 +876,13 @@ __device__ void few_consume(const AttendArgs& a, Control& c, uint8_t* smem) {
 #pragma unroll
                 for (int x = 0; x < kFW; ++x) {
                     const float* src = scr + (x * 8 + r8) * kPart;
-                    dn += src[D + 1] * exp2f(src[D] - ms);
-                    const float f = exp2f(src[D + 2] - ms);
+                    float f = exp2f(src[D] - ms);
+                    dn += src[D + 1] * f;
+                    if (kE4m3) {   // (whole numbers apart, and in two steps: each may be out of range)
+                        const float d = fmaxf(src[D] - ms, -1000.0f);
+                        const int k = max(-252, min(252, static_cast<int>(floorf(d) + src[D + 2])));
+                        f = exp2f(d - floorf(d)) * pow2f(k / 2) * pow2f(k - k / 2);
+                    }
                     const float4 z = *reinterpret_cast<const float4*>(src + 4 * lane);
                     y[0] += z.x * f; y[1] += z.y * f; y[2] += z.z * f; y[3] += z.w * f;
                 }

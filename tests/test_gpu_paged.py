@@ -816,6 +816,78 @@ def test_a_long_tail_far_below_the_largest_counts(out_dtype, rows):
     assert (err <= tol).all(), (err / tol).max()
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rows", [1, 4, 40])
+@pytest.mark.parametrize("high", [64, 128, 256, 1024])
+@pytest.mark.parametrize("at", [3, 170, 299])
+def test_one_token_far_above_the_rest_is_the_output(fmt, rows, high, at):
+    """A token whose score is above all others' by 2^60 and more, scores of 2^10 to 2^14 and V of
+    scales 2^-10 to 2^10 (8 bits): fp32 output is that token's V, however coarse the scores are. Its
+    weight is the same number in both sums; left are the weight's 24 bits, the division, and at most
+    6 steps of the sums it is in, 2^-24 each."""
+    rng = np.random.default_rng(at + high)
+    n, page = 300, 32
+    k, v = rng.standard_normal((2, 320, D)).astype(np.float32)
+    q = ref.bf16_round(rng.standard_normal((1, 1, D)).astype(np.float32)) * np.ones((rows, 4, 1), np.float32)
+    k[at] = high * np.sign(q[0, 0])
+    kd, vd = (_dev(x.reshape(10, 1, page, D)) for x in (k, v))
+    if fmt == "bf16":
+        pages = pk.Pages(kd.to(torch.bfloat16), vd.to(torch.bfloat16))
+        kf, vf = (x.double().cpu().numpy().reshape(-1, D) for x in pages.tensors[:2])
+    else:
+        kb = np.full(320, 127, np.uint8)
+        kb[at] = 127 + 2
+        k[at] /= 4
+        vb = rng.integers(117, 138, 320).astype(np.uint8)
+        codes = [_dev(x.reshape(10, 1, page, D)).to(torch.float8_e4m3fn) for x in (k, v)]
+        pages = pk.Pages(*codes, *(_dev(x.reshape(10, 1, page)) for x in (kb, vb)))
+        kf, vf = (c.double().cpu().numpy().reshape(-1, D) * 2.0 ** (b.astype(np.float64) - 127)[:, None]
+                  for c, b in zip(codes, (kb, vb)))
+    x = kf[:n] @ q[0, 0].astype(np.float64) * SCALE / np.log(2)
+    assert np.sort(x)[-1] - np.sort(x)[-2] > 60 and x[at] > 2.0 ** 9
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    chunk = pk.Chunk(ints([list(range(10))]), ints([n]), ints([0, rows]), rows, rows)
+    cfg = pk.config(batch=1, num_kv_heads=1, group=4, dtype="bf16")
+    out, lse = pk.paged_attend(cfg, pages, chunk, _bf(q), SCALE, causal=False, want_lse=True,
+                               out_dtype=torch.float32)
+    err = np.abs(out.double().cpu().numpy() - vf[at])
+    assert (err <= 8 * 2.0 ** -24 * np.abs(vf[at]) + n * 2.0 ** -60 * np.abs(vf[:n]).max()).all(), \
+        (err / np.abs(vf[at])).max()
+    assert (np.abs(lse.double().cpu().numpy() - x[at] * np.log(2)) <= 2 * 136 * 2.0 ** -23 * x[at]).all()
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 4])
+@pytest.mark.parametrize("big", [1 << e for e in range(22, 29)])
+def test_maxima_whose_steps_are_as_wide_as_their_growth(out_dtype, rows, big):
+    """8-bit pages whose blocks of 128 tokens score `big` and big + 8 (base 2) in turn, V = -1 and 1:
+    the second is just not above what a maximum may lag by, where fp32 steps are 1/2 to 32. Scores
+    are exact (scale * log2(e) is 1 in fp32) but for big + 8 being rounded to a step."""
+    page, n, heads, batch = 128, 20, 8, 8
+    scale = np.nextafter(np.float32(np.log(2)), np.float32(0))
+    while np.float32(scale * np.float32(1.4426950408889634)) < 1:
+        scale = np.nextafter(scale, np.float32(1))
+    assert np.float32(scale * np.float32(1.4426950408889634)) == 1
+    k, v = np.zeros((2, heads, page, D), np.float32), np.ones((2, heads, page, D), np.float32)
+    k[..., 0], k[1, ..., 1] = 256, 2.0 ** -4                       # times 2^4
+    v[0] = -1
+    kd, vd = (_dev(x).to(torch.float8_e4m3fn) for x in (k, v))
+    up = torch.full((2, heads, page), 127 + 4, dtype=torch.uint8, device=DEV)
+    pages = pk.Pages(kd, vd, up, torch.full_like(up, 127))
+    q = np.zeros((rows * batch, heads * 4, D), np.float32)
+    q[..., 0], q[..., 1] = big / 4096, 8
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    chunk = pk.Chunk(ints([[i % 2 for i in range(n)]] * batch), ints([n * page] * batch),
+                     ints([rows * i for i in range(batch + 1)]), rows * batch, rows)
+    cfg = pk.config(batch=batch, num_kv_heads=heads, group=4, dtype="bf16")
+    out, _ = pk.paged_attend(cfg, pages, chunk, _bf(q), float(scale), causal=False,
+                             out_dtype=out_dtype)
+    grown = np.float64(np.float32(big) + np.float32(8)) - big
+    w = 2.0 ** grown
+    tol = 2.0 ** -8 if out_dtype == torch.bfloat16 else 2.0 ** -16
+    assert ((out.double() - (w - 1) / (w + 1)).abs() <= tol).all()
+
+
 @pytest.mark.parametrize("n", [1, 200])
 def test_of_two_threads_one_gets_the_report(n):
     """Two threads ask at once, on streams of their own, about one wait that ran out: it is reported
